@@ -309,6 +309,191 @@ MUON_API muon_status limuon_step_batched(const muon_rsvd_param* params, int n, m
                                          int* d_status, muon_stream_t stream);
 
 /*
+ * Activation checkpoints in 8 bits.  The matrix gradients the steps above read
+ * are G = dY^T X of a linear layer's input X and output gradient dY, so X is
+ * held from the forward to the backward pass.  A checkpoint holds it in one
+ * byte per element: the columns of each row in blocks of 32, per block the
+ * smallest e in [-120, 119] with max|x| <= 127 2^e, stored as the byte e + 127,
+ * and per element the whole number q = x 2^-e rounded to nearest even (two's
+ * complement, -127..127); the checkpoint stands for X^ = q 2^e.
+ *   - |X^ - x| <= 2^(e-1), below 1/127 of the block's largest magnitude (half a
+ *     step; e only exceeds the smallest exponent that fits at e = -120).
+ *   - q 2^e has 7 significant bits, so it is exact in bfloat16 and float.
+ *   - A block with a NaN, an infinity or a magnitude above 127 2^119 gets the
+ *     byte 255 and codes 0, and stands for 32 NaNs.
+ * Any row may hold nothing else than zeros.  rows == 0 is a valid empty
+ * checkpoint (an expert without tokens); its pointers may be NULL.
+ */
+typedef struct {
+    int rows, cols;        /* rows >= 0 (tokens), cols >= 1 */
+    signed char* q;        /* rows x cols codes, row r at q + r * ldq; 16-byte aligned */
+    long long ldq;         /* >= cols, a multiple of 16 */
+    unsigned char* e;      /* rows x ceil(cols / 32) exponent bytes, row r at e + r * lde */
+    long long lde;         /* >= ceil(cols / 32) */
+} muon_act8;
+
+/* One matrix to encode (x is read, c written) or to decode (c read, x written). */
+typedef struct {
+    muon_act8 c;
+    void* x;               /* c.rows x c.cols elements, row r at x + r * ldx elements */
+    long long ldx;         /* >= cols */
+} muon_act8_item;
+
+/*
+ * Encode n matrices of x_dtype.  Bytes of q and e outside rows x cols (rows x
+ * ceil(cols / 32)) are left as they were.  A block that cannot be held raises
+ * MUON_FLAG_NONFINITE in *d_status (when given).  One launch per 64 items;
+ * asynchronous on `stream`; argument errors (MUON_ERR_INVALID_ARG) return
+ * before any launch.  No workspace.
+ */
+MUON_API muon_status act8_encode_batched(const muon_act8_item* items, int n, muon_dtype x_dtype, int* d_status,
+                                         muon_stream_t stream);
+
+/* Decode n checkpoints into x_dtype (exact in bfloat16 and float; rounded to
+ * nearest even in fp16, where values beyond its range become infinite). */
+MUON_API muon_status act8_decode_batched(const muon_act8_item* items, int n, muon_dtype x_dtype,
+                                         muon_stream_t stream);
+
+/*
+ * Weight gradients of linear layers from checkpointed inputs.  Layer i maps
+ * rows of `cols` values to rows of `out` values by a weight out x cols; its input
+ * was X = X^ diag(gain) + 1 shift^T (gain NULL: 1, shift NULL: 0; a norm's weight
+ * and bias, when the checkpoint holds the normalised rows that also serve the
+ * norm's own backward pass), so its gradient is
+ *     G = beta G + (dY^T X^) diag(gain) + dy_sum shift^T
+ * with dy_sum = the column sums of dY (the layer's bias gradient).  beta = 0
+ * overwrites G without reading it; rows == 0 leaves beta G (+ the shift term).
+ * The product accumulates in fp32: 16-bit dY runs on tensor cores with X^ taken
+ * in dY's type (exact in bfloat16; in fp16 rounded, see act8_decode_batched); fp32
+ * dY is split into three bfloat16 parts that sum to it.  The sums run in a
+ * fixed order: equal inputs give equal bits.  A NaN block makes NaNs of its columns of
+ * G (the step then flags the matrix and keeps its W).
+ */
+typedef struct {
+    muon_act8 c;           /* X^: rows (tokens) x cols; e as above */
+    const void* dY;        /* c.rows x out elements of dy_dtype, row r at dY + r * lddy elements */
+    long long lddy;        /* >= out */
+    int out;               /* >= 1 */
+    void* G;               /* out x cols, w_dtype, contiguous */
+    const void* gain;      /* cols elements of w_dtype, or NULL */
+    const void* shift;     /* cols elements of w_dtype, or NULL; needs dy_sum */
+    const float* dy_sum;   /* out fp32 values; NULL if and only if shift is NULL */
+    float beta;            /* finite */
+} muon_act8_grad_item;
+
+/* Bytes of workspace act8_grad_batched needs for these items (pointers are
+ * only inspected for their alignment). */
+MUON_API muon_status act8_grad_workspace_size(const muon_act8_grad_item* items, int n, muon_dtype dy_dtype,
+                                              size_t* bytes);
+
+/*
+ * The gradients of n layers (any mix of shapes; two items may share a
+ * checkpoint or a dY, not a G), asynchronous on `stream`.  workspace: device,
+ * 256-byte aligned, at least act8_grad_workspace_size bytes (NULL when that is
+ * 0); no state is kept in it between calls.  Argument errors return before any
+ * launch.
+ */
+MUON_API muon_status act8_grad_batched(const muon_act8_grad_item* items, int n, muon_dtype dy_dtype,
+                                       muon_dtype w_dtype, void* workspace, size_t ws_bytes, int* d_status,
+                                       muon_stream_t stream);
+
+/*
+ * The seam between two blocks of a network: the norm behind a block, its gate
+ * and residual scale, the residual sum, and the norm ahead of the next block, in
+ * one pass over the rows; the backward pass works from 8-bit checkpoints of the
+ * normalised rows and makes the vector gradients muon_model_step hands to
+ * AdamW.  Row t, in fp32:
+ *     n_f = (f - mean f) r_f   r_f = 1 / sqrt(mean (f - mean f)^2 + eps)   (MUON_NORM_LAYER)
+ *     n_f = f r_f              r_f = 1 / sqrt(mean f^2 + eps)              (MUON_NORM_RMS)
+ *     n_f = f                                                              (MUON_NORM_NONE)
+ *     u   = n_f post_gain + post_bias
+ *     x'  = skip x + scale gate u          rounded to x_dtype, stored in `out`
+ *     y   = n pre_gain + pre_bias          n the normalised rows of the rounded x'
+ * The gate of row t is row t / gate_rows of `gate` (1: a value for each token; the
+ * tokens of a sequence: a row for each sequence; rows: one learned vector).
+ * Without f there is no residual sum: x' = x, and only y is made.  Without a
+ * pre-norm (MUON_NORM_NONE) there is no y.
+ */
+typedef enum {
+    MUON_NORM_NONE = 0,
+    MUON_NORM_RMS = 1,
+    MUON_NORM_LAYER = 2
+} muon_norm;
+
+/* Largest row the seams take (one row is held in the registers of one block). */
+#define MUON_SEAM_MAX_COLS 16384
+
+typedef struct {
+    int rows, cols;             /* rows >= 0; 1 <= cols <= MUON_SEAM_MAX_COLS */
+    muon_norm post, pre;        /* norm of f; norm of x'.  post must be NONE without f */
+    float eps;                  /* > 0 */
+    float skip, scale;          /* finite; skip must be 1 without f */
+    const void* x;  long long ldx;       /* rows x cols, x_dtype, as are f, gate, out and y; ld >= cols elements */
+    const void* f;  long long ldf;       /* the block's output, or NULL */
+    const void* gate; long long ldgate;  /* ceil(rows / gate_rows) x cols, or NULL; needs f */
+    int gate_rows;                       /* >= 1 with a gate */
+    const void *post_gain, *post_bias;   /* cols elements of w_dtype, or NULL; need f */
+    const void *pre_gain, *pre_bias;     /* likewise; need a pre-norm */
+    void* out; long long ldout;          /* x'; NULL if and only if f is NULL; may be x or f */
+    void* y;   long long ldy;            /* NULL if and only if pre is NONE; may not overlap the others */
+    muon_act8 post_c;           /* receives n_f (rows x cols); q NULL: not kept.  Needs f */
+    muon_act8 pre_c;            /* receives n; q NULL: not kept.  Needs a pre-norm */
+    float* post_rstd;           /* receives r_f (rows); NULL to skip */
+    float* pre_rstd;            /* receives r (rows); NULL to skip */
+} muon_seam;
+
+/*
+ * One seam, asynchronous on `stream`; one launch, no workspace.  Argument errors
+ * return before the launch (MUON_ERR_UNSUPPORTED: cols beyond
+ * MUON_SEAM_MAX_COLS).  A checkpoint block that cannot be held raises
+ * MUON_FLAG_NONFINITE in *d_status (when given).
+ */
+MUON_API muon_status seam_forward(const muon_seam* seam, muon_dtype x_dtype, muon_dtype w_dtype, int* d_status,
+                                  muon_stream_t stream);
+
+/*
+ * Gradients of a seam.  With g = dy pre_gain, n and n_f the checkpoints' values:
+ *     d    = dout + r (g - [mean g] - n mean(g n))      ([..]: MUON_NORM_LAYER)
+ *     dx   = skip d
+ *     du   = scale gate d;   h = du post_gain
+ *     df   = r_f (h - [mean h] - n_f mean(h n_f))       (MUON_NORM_NONE: df = h)
+ *     dgate = the sum over the gate row's tokens of scale d (n_f post_gain + post_bias)
+ *     d_pre_gain  = sum_t dy n       d_pre_bias  = sum_t dy
+ *     d_post_gain = sum_t du n_f     d_post_bias = sum_t du
+ * each of the last four as d_v = beta d_v + the sum (beta = 0: not read).  Sums over
+ * tokens run in fp32 in a fixed order and are rounded once.
+ */
+typedef struct {
+    int rows, cols;             /* as muon_seam */
+    muon_norm post, pre;
+    float skip, scale;
+    const void* gate; long long ldgate; int gate_rows;
+    const void *post_gain, *post_bias, *pre_gain;
+    muon_act8 post_c;           /* needed for a post-norm, dgate or d_post_gain; q NULL otherwise allowed */
+    muon_act8 pre_c;            /* needed for a pre-norm */
+    const float *post_rstd, *pre_rstd;   /* needed for that norm */
+    const void* dy;   long long lddy;    /* x_dtype, as all that follow; NULL if and only if pre is NONE */
+    const void* dout; long long lddout;  /* gradient that reaches x' on the residual path; NULL: none */
+    void* dx; long long lddx;            /* required; may be dout or dy */
+    void* df; long long lddf;            /* NULL: the seam had no f; may be dy or dout when dx is not */
+    void* dgate; long long lddgate;      /* as gate; NULL to skip */
+    void *d_post_gain, *d_post_bias, *d_pre_gain, *d_pre_bias;   /* cols elements of w_dtype; NULL to skip */
+    float beta;                 /* finite */
+} muon_seam_grad;
+
+/* Bytes of workspace seam_backward needs (pointers are compared with NULL only). */
+MUON_API muon_status seam_backward_workspace_size(const muon_seam_grad* seam, size_t* bytes);
+
+/*
+ * Asynchronous on `stream`: one launch, and a second one that joins the sums over
+ * tokens where vector or shared gate gradients are asked for.  workspace: device,
+ * 256-byte aligned, at least seam_backward_workspace_size bytes (NULL when that
+ * is 0); no state is kept in it between calls.  Errors as seam_forward.
+ */
+MUON_API muon_status seam_backward(const muon_seam_grad* seam, muon_dtype x_dtype, muon_dtype w_dtype,
+                                   void* workspace, size_t ws_bytes, int* d_status, muon_stream_t stream);
+
+/*
  * Bytes of workspace ns_polar / gram_polar need for a batch of rows x cols
  * matrices in `dtype`.
  */
@@ -395,7 +580,10 @@ typedef enum {
     MUON_KERNEL_OTHER = 4,     /* identity fill (work = bytes) */
     MUON_KERNEL_ADAMW = 5,     /* AdamW streaming pass over vector parameters (work = bytes) */
     MUON_KERNEL_RSVD = 6,      /* LiMuon streaming passes: momentum + sketch, projection, update (work = bytes) */
-    MUON_KERNEL_RSVD_SMALL = 7 /* LiMuon per-matrix factorisations: QR, eigen-decomposition (work = bytes) */
+    MUON_KERNEL_RSVD_SMALL = 7, /* LiMuon per-matrix factorisations: QR, eigen-decomposition (work = bytes) */
+    MUON_KERNEL_ACT8 = 8,      /* checkpoint encode / decode, gradient operand copies and joins (work = bytes) */
+    MUON_KERNEL_ACT8_GRAD = 9, /* weight gradients from checkpoints (work = flops) */
+    MUON_KERNEL_SEAM = 10      /* block seams and the joins of their sums (work = bytes) */
 } muon_kernel_kind;
 
 typedef struct {

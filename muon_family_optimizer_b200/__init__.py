@@ -11,6 +11,9 @@ Names follow the C ABI: :func:`muon_step_batched`, :func:`ns_polar`,
 :func:`adamw_step_batched` (vector parameters), :func:`muon_model_step` (matrices and
 vector parameters in one step), :func:`limuon_step_batched` and
 :func:`limuon_workspace_size` (LiMuon), :func:`ns_polar_noalloc`,
+:func:`act8_encode_batched`, :func:`act8_decode_batched` (8-bit activation checkpoints),
+:func:`act8_grad_batched` (weight gradients from them), :func:`seam_forward`,
+:func:`seam_backward` (norms, gate and residual sum between two blocks),
 :func:`muon_status_string`.
 """
 import ctypes
@@ -85,10 +88,50 @@ class AdamWHParams(ctypes.Structure):
                 ("eps", ctypes.c_float), ("weight_decay", ctypes.c_float)]
 
 
+class Act8(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int), ("cols", ctypes.c_int), ("q", ctypes.c_void_p), ("ldq", ctypes.c_longlong),
+                ("e", ctypes.c_void_p), ("lde", ctypes.c_longlong)]
+
+
+class Act8Item(ctypes.Structure):
+    _fields_ = [("c", Act8), ("x", ctypes.c_void_p), ("ldx", ctypes.c_longlong)]
+
+
+class Act8GradItem(ctypes.Structure):
+    _fields_ = [("c", Act8), ("dY", ctypes.c_void_p), ("lddy", ctypes.c_longlong), ("out", ctypes.c_int),
+                ("G", ctypes.c_void_p), ("gain", ctypes.c_void_p), ("shift", ctypes.c_void_p),
+                ("dy_sum", ctypes.c_void_p), ("beta", ctypes.c_float)]
+
+
+class Seam(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int), ("cols", ctypes.c_int), ("post", ctypes.c_int), ("pre", ctypes.c_int),
+                ("eps", ctypes.c_float), ("skip", ctypes.c_float), ("scale", ctypes.c_float),
+                ("x", ctypes.c_void_p), ("ldx", ctypes.c_longlong), ("f", ctypes.c_void_p),
+                ("ldf", ctypes.c_longlong), ("gate", ctypes.c_void_p), ("ldgate", ctypes.c_longlong),
+                ("gate_rows", ctypes.c_int), ("post_gain", ctypes.c_void_p), ("post_bias", ctypes.c_void_p),
+                ("pre_gain", ctypes.c_void_p), ("pre_bias", ctypes.c_void_p), ("out", ctypes.c_void_p),
+                ("ldout", ctypes.c_longlong), ("y", ctypes.c_void_p), ("ldy", ctypes.c_longlong),
+                ("post_c", Act8), ("pre_c", Act8), ("post_rstd", ctypes.c_void_p), ("pre_rstd", ctypes.c_void_p)]
+
+
+class SeamGrad(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int), ("cols", ctypes.c_int), ("post", ctypes.c_int), ("pre", ctypes.c_int),
+                ("skip", ctypes.c_float), ("scale", ctypes.c_float), ("gate", ctypes.c_void_p),
+                ("ldgate", ctypes.c_longlong), ("gate_rows", ctypes.c_int), ("post_gain", ctypes.c_void_p),
+                ("post_bias", ctypes.c_void_p), ("pre_gain", ctypes.c_void_p), ("post_c", Act8), ("pre_c", Act8),
+                ("post_rstd", ctypes.c_void_p), ("pre_rstd", ctypes.c_void_p), ("dy", ctypes.c_void_p),
+                ("lddy", ctypes.c_longlong), ("dout", ctypes.c_void_p), ("lddout", ctypes.c_longlong),
+                ("dx", ctypes.c_void_p), ("lddx", ctypes.c_longlong), ("df", ctypes.c_void_p),
+                ("lddf", ctypes.c_longlong), ("dgate", ctypes.c_void_p), ("lddgate", ctypes.c_longlong),
+                ("d_post_gain", ctypes.c_void_p), ("d_post_bias", ctypes.c_void_p),
+                ("d_pre_gain", ctypes.c_void_p), ("d_pre_bias", ctypes.c_void_p), ("beta", ctypes.c_float)]
+
+
 (KERNEL_PREPASS, KERNEL_SYM, KERNEL_UPD, KERNEL_SIMT, KERNEL_OTHER, KERNEL_ADAMW, KERNEL_RSVD,
- KERNEL_RSVD_SMALL) = range(8)
+ KERNEL_RSVD_SMALL, KERNEL_ACT8, KERNEL_ACT8_GRAD, KERNEL_SEAM) = range(11)
 KERNEL_NAMES = {KERNEL_PREPASS: "prepass", KERNEL_SYM: "tc_sym", KERNEL_UPD: "tc_upd", KERNEL_ADAMW: "adamw",
-                KERNEL_SIMT: "simt", KERNEL_OTHER: "other", KERNEL_RSVD: "rsvd", KERNEL_RSVD_SMALL: "rsvd_small"}
+                KERNEL_SIMT: "simt", KERNEL_OTHER: "other", KERNEL_RSVD: "rsvd", KERNEL_RSVD_SMALL: "rsvd_small",
+                KERNEL_ACT8: "act8", KERNEL_ACT8_GRAD: "act8_grad", KERNEL_SEAM: "seam"}
 TRACE_CAPACITY = 8192
 
 
@@ -155,6 +198,22 @@ def lib():
                                        ctypes.c_int, ctypes.POINTER(Schedule), vp, vp]
         L.ns_polar_noalloc_capacity.restype = ctypes.c_size_t
         L.ns_polar_noalloc_capacity.argtypes = []
+        L.act8_encode_batched.restype = st
+        L.act8_encode_batched.argtypes = [ctypes.POINTER(Act8Item), ctypes.c_int, ctypes.c_int, vp, vp]
+        L.act8_decode_batched.restype = st
+        L.act8_decode_batched.argtypes = [ctypes.POINTER(Act8Item), ctypes.c_int, ctypes.c_int, vp]
+        L.act8_grad_workspace_size.restype = st
+        L.act8_grad_workspace_size.argtypes = [ctypes.POINTER(Act8GradItem), ctypes.c_int, ctypes.c_int, sz]
+        L.act8_grad_batched.restype = st
+        L.act8_grad_batched.argtypes = [ctypes.POINTER(Act8GradItem), ctypes.c_int, ctypes.c_int, ctypes.c_int, vp,
+                                        ctypes.c_size_t, vp, vp]
+        L.seam_forward.restype = st
+        L.seam_forward.argtypes = [ctypes.POINTER(Seam), ctypes.c_int, ctypes.c_int, vp, vp]
+        L.seam_backward_workspace_size.restype = st
+        L.seam_backward_workspace_size.argtypes = [ctypes.POINTER(SeamGrad), sz]
+        L.seam_backward.restype = st
+        L.seam_backward.argtypes = [ctypes.POINTER(SeamGrad), ctypes.c_int, ctypes.c_int, vp, ctypes.c_size_t, vp,
+                                    vp]
         L.muon_trace_enable.restype = st
         L.muon_trace_enable.argtypes = [ctypes.c_int]
         L.muon_trace_read.restype = ctypes.c_int
@@ -386,6 +445,232 @@ def limuon_step_batched(params, w_dtype, hp, workspace, d_status=None, stream=No
     _check(lib().limuon_step_batched(arr, len(arr), int(w_dtype), ctypes.byref(h), _ptr(workspace),
                                      workspace.numel() * workspace.element_size(), _ptr(d_status),
                                      _stream_ptr(stream)), "limuon_step_batched")
+
+
+ACT8_BLOCK = 32
+NORMS = {"none": 0, "rms": 1, "layer": 2}
+SEAM_MAX_COLS = 16384
+
+
+def act8_empty(rows, cols, device="cuda"):
+    """An 8-bit activation checkpoint of a rows x cols matrix, not yet written:
+    dict(q=int8 codes with 16-byte aligned rows, e=uint8 exponents of the blocks of 32 columns)."""
+    import torch
+    q = torch.empty(rows, (cols + 15) // 16 * 16, dtype=torch.int8, device=device)
+    return dict(q=q[:, :cols], e=torch.empty(rows, (cols + ACT8_BLOCK - 1) // ACT8_BLOCK, dtype=torch.uint8,
+                                             device=device))
+
+
+def _row_stride(t, where, rows=None, cols=None, dtype=None):
+    """Row stride (elements) of a 2-D tensor on the current device whose rows are contiguous."""
+    import torch
+    if t.dim() != 2 or (rows is not None and tuple(t.shape) != (rows, cols)):
+        raise ValueError(f"{where}: expected a {rows} x {cols} tensor, got {tuple(t.shape)}")
+    if dtype is not None and t.dtype != dtype:
+        raise ValueError(f"{where}: expected {dtype}, got {t.dtype}")
+    _on_device(t, where)
+    if t.shape[0] == 0 or t.shape[1] == 0:
+        return t.shape[1]
+    if t.shape[1] > 1 and t.stride(1) != 1 or t.shape[0] > 1 and t.stride(0) < t.shape[1]:
+        raise ValueError(f"{where}: rows must be contiguous and not overlap")
+    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1])
+
+
+def _on_device(t, where):
+    import torch
+    if not t.is_cuda or t.device.index != torch.cuda.current_device():
+        raise ValueError(f"{where}: must be a tensor of the current CUDA device, is on {t.device}")
+
+
+def _vector(t, where, n, dtype):
+    """Address of a contiguous vector of n values, or None."""
+    if t is None:
+        return None
+    _on_device(t, where)
+    if t.numel() != n or not t.is_contiguous() or t.dtype != dtype:
+        raise ValueError(f"{where}: expected {n} contiguous values of {dtype}")
+    return t.data_ptr()
+
+
+def _act8(q, e, where, rows=None, cols=None):
+    import torch
+    rows, cols = (q.shape if q.dim() == 2 else (-1, -1)) if rows is None else (rows, cols)
+    ldq = _row_stride(q, where + " q", rows, cols, torch.int8)
+    blocks = (cols + ACT8_BLOCK - 1) // ACT8_BLOCK
+    lde = _row_stride(e, where + " e", rows, blocks, torch.uint8)
+    if rows <= 1:                      # the only row's stride means nothing
+        ldq = (cols + 15) // 16 * 16
+    if rows and (ldq % 16 or q.data_ptr() % 16):
+        raise ValueError(f"{where}: q needs 16-byte aligned rows (see act8_empty)")
+    return Act8(rows, cols, q.data_ptr() if rows else None, ldq, e.data_ptr() if rows else None, lde)
+
+
+def make_act8_items(items):
+    """items: list of dicts with a checkpoint's q and e (see act8_empty) and x, the matrix it is
+    made from or decoded into; all x of one dtype, rows contiguous (any row stride)."""
+    arr = (Act8Item * len(items))()
+    for i, p in enumerate(items):
+        x, where = p["x"], f"item {i}"
+        if x.dtype != items[0]["x"].dtype:
+            raise ValueError(f"{where}: every x of a call has one dtype")
+        c = _act8(p["q"], p["e"], where)
+        arr[i] = Act8Item(c, x.data_ptr(), _row_stride(x, where + " x", c.rows, c.cols))
+    arr.x_dtype = _dtype_code(items[0]["x"].dtype) if len(items) else BF16
+    return arr
+
+
+def act8_encode_batched(items, d_status=None, stream=None):
+    """Write the 8-bit checkpoint (q, e) of every item's x (see include/muon.h).
+    items: list of dicts (see make_act8_items) or the array made from it."""
+    arr = items if isinstance(items, ctypes.Array) else make_act8_items(items)
+    _check(lib().act8_encode_batched(arr, len(arr), arr.x_dtype, _ptr(d_status), _stream_ptr(stream)),
+           "act8_encode_batched")
+
+
+def act8_decode_batched(items, stream=None):
+    """Write into every item's x the values its checkpoint (q, e) stands for (see include/muon.h)."""
+    arr = items if isinstance(items, ctypes.Array) else make_act8_items(items)
+    _check(lib().act8_decode_batched(arr, len(arr), arr.x_dtype, _stream_ptr(stream)), "act8_decode_batched")
+
+
+def make_act8_grads(items):
+    """items: list of dicts with a checkpoint's q and e (rows x cols), dY (rows x out), G (out x cols,
+    contiguous) and optionally gain, shift (cols values of G's dtype), dy_sum (out float32 values, with
+    shift) and beta (default 0); all dY of one dtype, all G of one dtype."""
+    import torch
+    arr = (Act8GradItem * len(items))()
+    for i, p in enumerate(items):
+        dY, G, where = p["dY"], p["G"], f"item {i}"
+        if dY.dtype != items[0]["dY"].dtype or G.dtype != items[0]["G"].dtype:
+            raise ValueError(f"{where}: every dY, and every G, of a call has one dtype")
+        c = _act8(p["q"], p["e"], where)
+        if dY.dim() != 2:
+            raise ValueError(f"{where} dY: must be 2-D")
+        out = dY.shape[1]
+        lddy = _row_stride(dY, where + " dY", c.rows, out)
+        _row_stride(G, where + " G", out, c.cols)
+        if not G.is_contiguous():
+            raise ValueError(f"{where} G: must be contiguous")
+        arr[i] = Act8GradItem(c, dY.data_ptr(), lddy, out, G.data_ptr(),
+                              _vector(p.get("gain"), where + " gain", c.cols, G.dtype),
+                              _vector(p.get("shift"), where + " shift", c.cols, G.dtype),
+                              _vector(p.get("dy_sum"), where + " dy_sum", out, torch.float32),
+                              float(p.get("beta", 0.0)))
+    arr.dy_dtype = _dtype_code(items[0]["dY"].dtype) if len(items) else BF16
+    arr.w_dtype = _dtype_code(items[0]["G"].dtype) if len(items) else BF16
+    return arr
+
+
+def act8_grad_workspace_size(items):
+    """Workspace bytes of act8_grad_batched for these items."""
+    arr = items if isinstance(items, ctypes.Array) else make_act8_grads(items)
+    out = ctypes.c_size_t(0)
+    _check(lib().act8_grad_workspace_size(arr, len(arr), arr.dy_dtype, ctypes.byref(out)),
+           "act8_grad_workspace_size")
+    return out.value
+
+
+def act8_grad_batched(items, workspace=None, d_status=None, stream=None):
+    """G = beta G + (dY^T X) for every item, X the layer's input held as an 8-bit checkpoint, scaled and
+    shifted by gain and shift (see include/muon.h): the G that muon_step_batched reads.
+    workspace: a CUDA uint8 tensor of at least act8_grad_workspace_size(...) bytes."""
+    arr = items if isinstance(items, ctypes.Array) else make_act8_grads(items)
+    _check(lib().act8_grad_batched(arr, len(arr), arr.dy_dtype, arr.w_dtype, _ptr(workspace),
+                                   workspace.numel() if workspace is not None else 0, _ptr(d_status),
+                                   _stream_ptr(stream)), "act8_grad_batched")
+
+
+_NO_ACT8 = Act8(0, 0, None, 0, None, 0)
+
+
+def _seam_common(s, lead):
+    """(rows, cols, x dtype, w dtype, post, pre, matrix(), vector(), checkpoint()) of a seam's dict."""
+    import torch
+    rows, cols = lead.shape if lead.dim() == 2 else (-1, -1)
+    vecs = [s[k] for k in ("post_gain", "post_bias", "pre_gain", "pre_bias", "d_post_gain", "d_post_bias",
+                           "d_pre_gain", "d_pre_bias") if s.get(k) is not None]
+    wt = vecs[0].dtype if vecs else lead.dtype
+
+    def matrix(k, n=rows):
+        t = s.get(k)
+        return (None, 0) if t is None else (t.data_ptr(), _row_stride(t, k, n, cols, lead.dtype))
+
+    def checkpoint(k):
+        c = s.get(k)
+        return _NO_ACT8 if c is None else _act8(c["q"], c["e"], k, rows, cols)
+
+    def norm(k):
+        kind = s.get(k, "none")
+        if kind not in NORMS:
+            raise ValueError(f"{k}: must be one of {sorted(NORMS)}")
+        return NORMS[kind]
+
+    gr = int(s.get("gate_rows") or 1)
+    if gr < 1:
+        raise ValueError("gate_rows: must be at least 1")
+    return dict(rows=rows, cols=cols, wt=wt, norm=norm, matrix=matrix, checkpoint=checkpoint, gate_rows=gr,
+                gate_len=-(-rows // gr), vector=lambda k: _vector(s.get(k), k, cols, wt),
+                rstd=lambda k: _vector(s.get(k), k, rows, torch.float32))
+
+
+def make_seam(s):
+    """s: dict with x (rows x cols) and, as the seam has them, f, gate (ceil(rows / gate_rows) x cols),
+    gate_rows, post and pre ("none", "rms" or "layer"), post_gain, post_bias, pre_gain, pre_bias (cols
+    values of one dtype), eps, skip, scale; outputs out, y, post_c and pre_c (checkpoints, see
+    act8_empty), post_rstd and pre_rstd (rows float32 values).  Matrices: x's dtype, rows contiguous."""
+    h = _seam_common(s, s["x"])
+    m, v = h["matrix"], h["vector"]
+    d = Seam(h["rows"], h["cols"], h["norm"]("post"), h["norm"]("pre"), float(s.get("eps", 1e-5)),
+             float(s.get("skip", 1.0)), float(s.get("scale", 1.0)), *m("x"), *m("f"), *m("gate", h["gate_len"]),
+             h["gate_rows"], v("post_gain"), v("post_bias"), v("pre_gain"), v("pre_bias"), *m("out"), *m("y"),
+             h["checkpoint"]("post_c"), h["checkpoint"]("pre_c"), h["rstd"]("post_rstd"), h["rstd"]("pre_rstd"))
+    d.x_dtype, d.w_dtype = _dtype_code(s["x"].dtype), _dtype_code(h["wt"])
+    return d
+
+
+def seam_forward(seam, d_status=None, stream=None):
+    """The seam between two blocks (see include/muon.h): out = skip x + scale gate norm(f) and
+    y = norm(out), the normalised rows kept as 8-bit checkpoints.  seam: dict (see make_seam) or the
+    descriptor made from it."""
+    d = seam if isinstance(seam, Seam) else make_seam(seam)
+    _check(lib().seam_forward(ctypes.byref(d), d.x_dtype, d.w_dtype, _ptr(d_status), _stream_ptr(stream)),
+           "seam_forward")
+
+
+def make_seam_grad(s):
+    """s: dict with dx (rows x cols, written) and, as the seam has them, post, pre, skip, scale, gate,
+    gate_rows, post_gain, post_bias, pre_gain, post_c, pre_c, post_rstd, pre_rstd as given to and made
+    by seam_forward; dy and dout, the gradients of y and of out; outputs df, dgate (as gate),
+    d_post_gain, d_post_bias, d_pre_gain, d_pre_bias (cols values of the gains' dtype) and beta
+    (default 0) that scales what those four held."""
+    h = _seam_common(s, s["dx"])
+    m, v = h["matrix"], h["vector"]
+    d = SeamGrad(h["rows"], h["cols"], h["norm"]("post"), h["norm"]("pre"), float(s.get("skip", 1.0)),
+                 float(s.get("scale", 1.0)), *m("gate", h["gate_len"]), h["gate_rows"], v("post_gain"),
+                 v("post_bias"), v("pre_gain"), h["checkpoint"]("post_c"), h["checkpoint"]("pre_c"),
+                 h["rstd"]("post_rstd"), h["rstd"]("pre_rstd"), *m("dy"), *m("dout"), *m("dx"), *m("df"),
+                 *m("dgate", h["gate_len"]), v("d_post_gain"), v("d_post_bias"), v("d_pre_gain"), v("d_pre_bias"),
+                 float(s.get("beta", 0.0)))
+    d.x_dtype, d.w_dtype = _dtype_code(s["dx"].dtype), _dtype_code(h["wt"])
+    return d
+
+
+def seam_backward_workspace_size(seam):
+    """Workspace bytes of seam_backward."""
+    d = seam if isinstance(seam, SeamGrad) else make_seam_grad(seam)
+    out = ctypes.c_size_t(0)
+    _check(lib().seam_backward_workspace_size(ctypes.byref(d), ctypes.byref(out)), "seam_backward_workspace_size")
+    return out.value
+
+
+def seam_backward(seam, workspace=None, d_status=None, stream=None):
+    """Gradients of a seam from its checkpoints (see include/muon.h): dx, df, dgate and the vector
+    gradients that muon_model_step's AdamW reads.  seam: dict (see make_seam_grad) or the descriptor
+    made from it; workspace: a CUDA uint8 tensor of at least seam_backward_workspace_size(...) bytes."""
+    d = seam if isinstance(seam, SeamGrad) else make_seam_grad(seam)
+    _check(lib().seam_backward(ctypes.byref(d), d.x_dtype, d.w_dtype, _ptr(workspace),
+                               workspace.numel() if workspace is not None else 0, _ptr(d_status),
+                               _stream_ptr(stream)), "seam_backward")
 
 
 def muon_wait_selftest(wait_ms, d_status, stream=None):

@@ -1,0 +1,116 @@
+// act8.cuh -- the 8-bit activation checkpoint format (muon_act8 in muon.h):
+// device code shared by the kernels that write it (act8.cu, seam.cu) and read
+// it (act8.cu, act8_grad.cu, seam.cu), and the host checks of its arguments.
+//
+// A block of 32 columns of one row holds x as q 2^e, e the smallest exponent
+// in [kActExpMin, kActExpMax] with max|x| <= 127 2^e and q = rne(x 2^-e).  The
+// scale is a power of two so that q 2^e has 7 significant bits: exact as a
+// bfloat16 tensor-core operand, where a general fp32 scale would round every
+// value a second time (2^-9 relative) or need the scale outside the sum over
+// tokens, which a scale per token and block cannot have.  It costs at most one
+// bit of resolution against the general scale.
+#pragma once
+
+#include "muon_internal.cuh"
+
+namespace muon {
+
+constexpr int kActBlock = 32;
+constexpr int kActExpMin = -120, kActExpMax = 119;
+constexpr int kActBad = 255;        // exponent byte of a block that stands for NaNs
+
+__host__ __device__ inline int act8_blocks(int cols) { return (cols + kActBlock - 1) / kActBlock; }
+
+// |x| as bits: unsigned integer order is magnitude order, with NaNs above infinity.
+__device__ __forceinline__ uint32_t abs_bits(float x) { return __float_as_uint(x) & 0x7FFFFFFFu; }
+
+// Exponent byte of a block whose largest magnitude has the bits m: with
+// max = f 2^E (1 <= f < 2), 127 2^(E-6) = (127/64) 2^E holds it unless f > 127/64.
+__device__ __forceinline__ int act8_exp_byte(uint32_t m) {
+    const int e = (int)(m >> 23) - 127 - 6 + ((m & 0x7FFFFFu) > 0x7E0000u ? 1 : 0);
+    return e > kActExpMax ? kActBad : max(e, kActExpMin) + 127;
+}
+
+// 2^e and 2^-e of a valid exponent byte.
+__device__ __forceinline__ float act8_scale(int byte) { return __uint_as_float((uint32_t)byte << 23); }
+__device__ __forceinline__ float act8_inv(int byte) { return __uint_as_float((uint32_t)(254 - byte) << 23); }
+
+// Codes of four values.  x 2^-e is exact, so the fused multiply-add onto 1.5 2^23
+// rounds once, to the nearest whole number (ties to even), whose two's
+// complement is the sum's low byte.
+__device__ __forceinline__ uint32_t act8_codes4(float a, float b, float c, float d, float inv) {
+    const float magic = 12582912.f;
+    const uint32_t ua = __float_as_uint(__fmaf_rn(a, inv, magic)), ub = __float_as_uint(__fmaf_rn(b, inv, magic));
+    const uint32_t uc = __float_as_uint(__fmaf_rn(c, inv, magic)), ud = __float_as_uint(__fmaf_rn(d, inv, magic));
+    return __byte_perm(__byte_perm(ua, ub, 0x0040), __byte_perm(uc, ud, 0x0040), 0x5410);
+}
+
+// Eight columns col..col+7 of one row (col a multiple of 8; values past the row
+// given as 0), the block's four lanes in step: the block's exponent by two
+// shuffles (every lane of the warp takes part), the codes as two words, and by
+// the block's first lane the exponent byte.  Returns false for a block that
+// cannot be held.
+__device__ __forceinline__ bool act8_encode8(const float (&x)[8], int col, int nvalid, signed char* qrow,
+                                             unsigned char* erow, int lane) {
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) m = max(m, abs_bits(x[i]));
+    m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
+    m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
+    const int byte = act8_exp_byte(m);
+    const bool ok = byte != kActBad;
+    uint2 w = make_uint2(0u, 0u);
+    if (ok) {
+        const float inv = act8_inv(byte);
+        w.x = act8_codes4(x[0], x[1], x[2], x[3], inv);
+        w.y = act8_codes4(x[4], x[5], x[6], x[7], inv);
+    }
+    if (nvalid >= 8) {
+        *reinterpret_cast<uint2*>(qrow + col) = w;
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (i < nvalid) qrow[col + i] = (signed char)((i < 4 ? w.x : w.y) >> (8 * (i & 3)));
+    }
+    if ((lane & 3) == 0 && nvalid > 0) erow[col / kActBlock] = (unsigned char)byte;
+    return ok;
+}
+
+// The values of eight codes (two words) under an exponent byte.
+__device__ __forceinline__ void act8_decode8(uint2 w, int byte, float (&v)[8]) {
+    const float s = byte == kActBad ? __uint_as_float(0x7FC00000u) : act8_scale(byte);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const int q = (int)(signed char)((i < 4 ? w.x : w.y) >> (8 * (i & 3)));
+        v[i] = (float)q * s;
+    }
+}
+
+// Codes col..col+7 of a row; those past the row read as 0.
+__device__ __forceinline__ uint2 act8_load8(const signed char* qrow, int col, int nvalid) {
+    if (nvalid >= 8) return *reinterpret_cast<const uint2*>(qrow + col);
+    uint2 w = make_uint2(0u, 0u);
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        if (i < nvalid) {
+            const uint32_t b = (uint32_t)(unsigned char)qrow[col + i] << (8 * (i & 3));
+            if (i < 4) w.x |= b; else w.y |= b;
+        }
+    return w;
+}
+
+// Host: whether a checkpoint's fields can be used (an empty one needs no pointers).
+inline bool act8_valid(const muon_act8& c) {
+    if (c.rows < 0 || c.cols < 1 || c.ldq < c.cols || c.ldq % 16 != 0 || c.lde < act8_blocks(c.cols)) return false;
+    if (c.rows == 0) return true;
+    return c.q && c.e && (reinterpret_cast<uintptr_t>(c.q) & 15) == 0;
+}
+
+// Host: 16-byte accesses of rows of `esz`-byte elements are allowed.
+inline bool rows_aligned(const void* p, long long ld, int esz) {
+    return (reinterpret_cast<uintptr_t>(p) & 15) == 0 && (ld * esz) % 16 == 0;
+}
+
+muon_status check_device();     // muon_api.cu: the current device runs sm_100 code
+
+}  // namespace muon

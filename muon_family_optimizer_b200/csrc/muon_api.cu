@@ -11,9 +11,19 @@
 #include <map>
 #include <vector>
 
+#include "act8.cuh"
 #include "gemm.h"
 
 namespace muon {
+
+muon_status check_device() {
+    int dev = 0, major = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return MUON_ERR_CUDA;
+    if (cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess)
+        return MUON_ERR_CUDA;
+    return major == 10 ? MUON_OK : MUON_ERR_UNSUPPORTED;
+}
+
 namespace {
 
 constexpr size_t kAlign = 1024;
@@ -47,14 +57,6 @@ bool is_restart(const muon_schedule* s, int k) {
     for (int i = 0; i < s->n_restarts; ++i)
         if (s->restarts[i] == k) return true;
     return false;
-}
-
-muon_status check_device() {
-    int dev = 0, major = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess) return MUON_ERR_CUDA;
-    if (cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess)
-        return MUON_ERR_CUDA;
-    return major == 10 ? MUON_OK : MUON_ERR_UNSUPPORTED;
 }
 
 // ---------------------------------------------------------------- layouts

@@ -1,0 +1,643 @@
+// seam.cu -- the seam between two blocks: norm behind a block, gate, residual
+// scale, residual sum and the norm ahead of the next block in one pass, and the
+// gradients of all of it from 8-bit checkpoints of the normalised rows
+// (formulas at muon_seam and muon_seam_grad in muon.h).
+//
+// Both passes are bound by HBM.  A row lives in the registers of one group of TPR
+// threads (VPT chunks of 8 consecutive columns each), so that the two norms of a
+// seam, the second of which depends on every element the first has made, cost one
+// read of the inputs.  Sums over a row: warp shuffles, then (TPR > 32) one round
+// through shared memory, in a fixed order.  Sums over tokens (backward): every block
+// takes a run of consecutive rows, keeps its columns' sums in registers and writes
+// them once; a second launch adds the runs in order.
+#include <algorithm>
+#include <cmath>
+
+#include "act8.cuh"
+#include "gemm.h"
+
+namespace muon {
+
+namespace {
+
+template <typename T> struct DtOf;
+template <> struct DtOf<__nv_bfloat16> { static constexpr int v = DT_BF16; };
+template <> struct DtOf<__half> { static constexpr int v = DT_FP16; };
+template <> struct DtOf<float> { static constexpr int v = DT_FP32; };
+
+// Sums of N values over the TPR threads of a row; every thread gets them.  `slot`
+// alternates between two shared-memory areas, so one barrier per call is enough.
+template <int TPR, int N>
+__device__ __forceinline__ void row_sum(float (&v)[N], float* red, int& slot) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1)
+#pragma unroll
+        for (int k = 0; k < N; ++k) v[k] += __shfl_xor_sync(0xFFFFFFFFu, v[k], o);
+    if constexpr (TPR > 32) {
+        constexpr int NW = TPR / 32;
+        float* s = red + slot * (NW * 2);
+        slot ^= 1;
+        if ((threadIdx.x & 31) == 0)
+#pragma unroll
+            for (int k = 0; k < N; ++k) s[k * NW + (threadIdx.x >> 5)] = v[k];
+        __syncthreads();
+#pragma unroll
+        for (int k = 0; k < N; ++k) {
+            if constexpr (NW <= 8) {
+                float t = s[k * NW];
+#pragma unroll
+                for (int w = 1; w < NW; ++w) t += s[k * NW + w];
+                v[k] = t;
+            } else {
+                const int lane = threadIdx.x & 31;
+                float t = lane < NW ? s[k * NW + lane] : 0.f;
+#pragma unroll
+                for (int o = 16; o > 0; o >>= 1) t += __shfl_xor_sync(0xFFFFFFFFu, t, o);
+                v[k] = t;
+            }
+        }
+    }
+}
+
+// Normalise the row in v (columns beyond the row hold 0 and stay 0): returns the
+// reciprocal deviation.  The two-pass variance keeps rows whose mean is large
+// against their deviation exact; a sum of squares beyond fp32's range is formed
+// again at 2^-100.
+template <int TPR, int VPT>
+__device__ __forceinline__ float row_normalise(float (&v)[VPT][8], const int (&nv)[VPT], int kind, float eps,
+                                               float inv_c, float* red, int& slot) {
+    if (kind == MUON_NORM_LAYER) {
+        float m[1] = {0.f};
+#pragma unroll
+        for (int j = 0; j < VPT; ++j)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) m[0] = fmaf(v[j][i], inv_c, m[0]);
+        row_sum<TPR, 1>(m, red, slot);
+#pragma unroll
+        for (int j = 0; j < VPT; ++j)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[j][i] = i < nv[j] ? v[j][i] - m[0] : 0.f;
+    }
+    float s[1] = {0.f};
+#pragma unroll
+    for (int j = 0; j < VPT; ++j)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) s[0] = fmaf(v[j][i], v[j][i], s[0]);
+    row_sum<TPR, 1>(s, red, slot);
+    float r;
+    if (s[0] == __uint_as_float(0x7F800000u)) {      // uniform over the row
+        const float down = __uint_as_float((127u - 100u) << 23);
+        s[0] = 0.f;
+#pragma unroll
+        for (int j = 0; j < VPT; ++j)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) s[0] = fmaf(v[j][i] * down, v[j][i] * down, s[0]);
+        row_sum<TPR, 1>(s, red, slot);
+        r = __frsqrt_rn(s[0] * inv_c) * down;
+    } else {
+        r = __frsqrt_rn(fmaf(s[0], inv_c, eps));
+    }
+#pragma unroll
+    for (int j = 0; j < VPT; ++j)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[j][i] *= r;
+    return r;
+}
+
+// u = n gain + bias on one chunk (either may be NULL)
+__device__ __forceinline__ void affine8(float (&v)[8], const void* gain, const void* bias, int col, int dt, bool vec,
+                                        int nvalid) {
+    if (gain) {
+        float g[8];
+        load8_dt(gain, col, dt, vec, nvalid, g);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] *= g[i];
+    }
+    if (bias) {
+        float b[8];
+        load8_dt(bias, col, dt, vec, nvalid, b);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] += b[i];
+    }
+}
+
+struct FwdParams {
+    muon_seam s;
+    float inv_c;
+    int w_dt, vec, wvec;
+    int* d_status;
+};
+
+template <typename T, int TPR, int VPT>
+__global__ void __launch_bounds__(TPR == 32 ? 128 : TPR) seam_fwd_kernel(const __grid_constant__ FwdParams p) {
+    constexpr int DT = DtOf<T>::v;
+    constexpr int RPB = TPR == 32 ? 4 : 1;
+    __shared__ float red[TPR > 32 ? 4 * (TPR / 32) : 1];
+    const muon_seam& S = p.s;
+    const int lane = threadIdx.x & 31, tr = threadIdx.x % TPR;
+    int col[VPT], nv[VPT];
+#pragma unroll
+    for (int j = 0; j < VPT; ++j) {
+        col[j] = (j * TPR + tr) * 8;
+        nv[j] = min(8, max(0, S.cols - col[j]));
+    }
+    int slot = 0;
+    bool bad = false;
+    for (long long row = (long long)blockIdx.x * RPB + threadIdx.x / TPR; row < S.rows;
+         row += (long long)gridDim.x * RPB) {
+        float x[VPT][8], u[VPT][8];
+#pragma unroll
+        for (int j = 0; j < VPT; ++j) {
+            load8_dt(S.x, row * S.ldx + col[j], DT, p.vec && nv[j] == 8, nv[j], x[j]);
+            if (S.f) load8_dt(S.f, row * S.ldf + col[j], DT, p.vec && nv[j] == 8, nv[j], u[j]);
+        }
+        if (S.f) {
+            if (S.post != MUON_NORM_NONE) {
+                const float r = row_normalise<TPR, VPT>(u, nv, S.post, S.eps, p.inv_c, red, slot);
+                if (S.post_rstd && tr == 0) S.post_rstd[row] = r;
+            }
+#pragma unroll
+            for (int j = 0; j < VPT; ++j) {
+                const bool vec = p.vec && nv[j] == 8, wvec = p.wvec && nv[j] == 8;
+                if (S.post_c.q)
+                    bad |= !act8_encode8(u[j], col[j], nv[j], S.post_c.q + row * S.post_c.ldq,
+                                         S.post_c.e + row * S.post_c.lde, lane);
+                affine8(u[j], S.post_gain, S.post_bias, col[j], p.w_dt, wvec, nv[j]);
+                if (S.gate) {
+                    float g[8];
+                    load8_dt(S.gate, (row / S.gate_rows) * S.ldgate + col[j], DT, vec, nv[j], g);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) u[j][i] *= g[i];
+                }
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    x[j][i] = to_float(from_float<T>(fmaf(S.scale, u[j][i], S.skip * x[j][i])));
+                if (nv[j] < 8)
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) x[j][i] = i < nv[j] ? x[j][i] : 0.f;
+                store8_dt(S.out, row * S.ldout + col[j], DT, vec, nv[j], x[j]);
+            }
+        }
+        if (S.pre != MUON_NORM_NONE) {
+            const float r = row_normalise<TPR, VPT>(x, nv, S.pre, S.eps, p.inv_c, red, slot);
+            if (S.pre_rstd && tr == 0) S.pre_rstd[row] = r;
+#pragma unroll
+            for (int j = 0; j < VPT; ++j) {
+                if (S.pre_c.q)
+                    bad |= !act8_encode8(x[j], col[j], nv[j], S.pre_c.q + row * S.pre_c.ldq,
+                                         S.pre_c.e + row * S.pre_c.lde, lane);
+                affine8(x[j], S.pre_gain, S.pre_bias, col[j], p.w_dt, p.wvec && nv[j] == 8, nv[j]);
+                store8_dt(S.y, row * S.ldy + col[j], DT, p.vec && nv[j] == 8, nv[j], x[j]);
+            }
+        }
+    }
+    if (__any_sync(0xFFFFFFFFu, bad) && lane == 0 && p.d_status) atomicOr(p.d_status, MUON_FLAG_NONFINITE);
+}
+
+// ---------------------------------------------------------------------------
+// Backward
+// ---------------------------------------------------------------------------
+constexpr int kPlanSms = 148;       // runs are planned for a whole B200, so a size query needs no device
+
+enum Vec : int { V_POST_GAIN, V_POST_BIAS, V_PRE_GAIN, V_PRE_BIAS, V_COUNT };
+
+// Rows cut into runs, one per block.  A run holds whole gate groups (direct: their
+// sums are finished in the run), or lies inside one group of which `parts` runs
+// share the rows.
+struct RunPlan {
+    long long runs;
+    int run_rows;      // rows of a run
+    int parts;         // runs per gate group (0: the runs hold whole groups)
+};
+
+RunPlan plan_runs(int rows, int cols, int gate_rows, bool gate_sums) {
+    const int per_sm = cols <= 1024 ? 8 : cols <= 2048 ? 4 : cols <= 4096 ? 2 : 1;
+    RunPlan P;
+    const long long want = (long long)kPlanSms * per_sm;
+    P.run_rows = (int)std::max<long long>(1, (rows + want - 1) / want);
+    P.parts = 0;
+    P.runs = (rows + P.run_rows - 1) / P.run_rows;
+    if (gate_sums) {
+        const long long groups = ((long long)rows + gate_rows - 1) / gate_rows;
+        if (gate_rows <= P.run_rows) {
+            P.run_rows = P.run_rows / gate_rows * gate_rows;
+            P.runs = (rows + P.run_rows - 1) / P.run_rows;
+        } else {
+            const int span = std::min(gate_rows, rows);
+            P.parts = (span + P.run_rows - 1) / P.run_rows;
+            P.run_rows = (span + P.parts - 1) / P.parts;
+            P.runs = groups * P.parts;
+        }
+    }
+    return P;
+}
+
+struct BwdParams {
+    muon_seam_grad s;
+    RunPlan plan;
+    float inv_c;
+    int w_dt, vec, wvec, gate_sums;
+    float* part;           // [V_COUNT + 1][runs][cols]: sums of one run (the last: shared gate rows)
+};
+
+template <typename T, int TPR, int VPT, bool ALL>
+__global__ void __launch_bounds__(TPR) seam_bwd_kernel(const __grid_constant__ BwdParams p) {
+    constexpr int DT = DtOf<T>::v;
+    __shared__ float red[TPR > 32 ? 4 * (TPR / 32) : 1];
+    const muon_seam_grad& S = p.s;
+    const int tr = threadIdx.x;
+    int col[VPT], nv[VPT];
+#pragma unroll
+    for (int j = 0; j < VPT; ++j) {
+        col[j] = (j * TPR + tr) * 8;
+        nv[j] = min(8, max(0, S.cols - col[j]));
+    }
+    long long r0, r1;
+    if (p.plan.parts == 0) {
+        r0 = (long long)blockIdx.x * p.plan.run_rows;
+        r1 = min((long long)S.rows, r0 + p.plan.run_rows);
+    } else {
+        const long long g = blockIdx.x / p.plan.parts;
+        r0 = g * S.gate_rows + (long long)(blockIdx.x % p.plan.parts) * p.plan.run_rows;
+        r1 = min(min((long long)S.rows, r0 + p.plan.run_rows), (g + 1) * S.gate_rows);
+    }
+    float a_pg[VPT][8] = {}, a_qg[VPT][8] = {};               // d_pre_gain, d_post_gain
+    float a_pb[ALL ? VPT : 1][8] = {}, a_qb[ALL ? VPT : 1][8] = {}, a_gt[ALL ? VPT : 1][8] = {};
+    int slot = 0;
+    const bool post_c = S.post_c.q != nullptr;
+    for (long long row = r0; row < r1; ++row) {
+        float d[VPT][8];
+#pragma unroll
+        for (int j = 0; j < VPT; ++j) {
+            if (S.dout) load8_dt(S.dout, row * S.lddout + col[j], DT, p.vec && nv[j] == 8, nv[j], d[j]);
+            else
+#pragma unroll
+                for (int i = 0; i < 8; ++i) d[j][i] = 0.f;
+        }
+        if (S.pre != MUON_NORM_NONE) {
+            float g[VPT][8], n[VPT][8];
+            float sums[2] = {0.f, 0.f};
+#pragma unroll
+            for (int j = 0; j < VPT; ++j) {
+                const bool vec = p.vec && nv[j] == 8;
+                load8_dt(S.dy, row * S.lddy + col[j], DT, vec, nv[j], g[j]);
+                act8_decode8(act8_load8(S.pre_c.q + row * S.pre_c.ldq, col[j], nv[j]),
+                             nv[j] > 0 ? S.pre_c.e[row * S.pre_c.lde + col[j] / kActBlock] : 127, n[j]);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    a_pg[j][i] = fmaf(g[j][i], n[j][i], a_pg[j][i]);
+                    if constexpr (ALL) a_pb[j][i] += g[j][i];
+                }
+                affine8(g[j], S.pre_gain, nullptr, col[j], p.w_dt, p.wvec && nv[j] == 8, nv[j]);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    sums[0] = fmaf(g[j][i], n[j][i], sums[0]);
+                    sums[1] += g[j][i];
+                }
+            }
+            row_sum<TPR, 2>(sums, red, slot);
+            const float r = S.pre_rstd[row];
+            const float s1 = sums[0] * p.inv_c, s0 = S.pre == MUON_NORM_LAYER ? sums[1] * p.inv_c : 0.f;
+#pragma unroll
+            for (int j = 0; j < VPT; ++j)
+#pragma unroll
+                for (int i = 0; i < 8; ++i) d[j][i] = fmaf(r, fmaf(-n[j][i], s1, g[j][i] - s0), d[j][i]);
+        }
+        if (S.df) {
+            float n[VPT][8], h[VPT][8];
+            float sums[2] = {0.f, 0.f};
+            const long long grow = S.gate ? row / S.gate_rows : 0;
+#pragma unroll
+            for (int j = 0; j < VPT; ++j) {
+                const bool vec = p.vec && nv[j] == 8, wvec = p.wvec && nv[j] == 8;
+                if (post_c)
+                    act8_decode8(act8_load8(S.post_c.q + row * S.post_c.ldq, col[j], nv[j]),
+                                 nv[j] > 0 ? S.post_c.e[row * S.post_c.lde + col[j] / kActBlock] : 127, n[j]);
+                else
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) n[j][i] = 0.f;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) h[j][i] = S.scale * d[j][i];
+                if (S.gate) {
+                    float g[8];
+                    load8_dt(S.gate, grow * S.ldgate + col[j], DT, vec, nv[j], g);
+                    if (S.dgate) {
+                        float t[8];
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) t[i] = n[j][i];
+                        affine8(t, S.post_gain, S.post_bias, col[j], p.w_dt, wvec, nv[j]);
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) t[i] *= h[j][i];
+                        if (!p.gate_sums) store8_dt(S.dgate, grow * S.lddgate + col[j], DT, vec, nv[j], t);
+                        if constexpr (ALL)
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) a_gt[j][i] += t[i];
+                    }
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) h[j][i] *= g[i];
+                }
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    a_qg[j][i] = fmaf(h[j][i], n[j][i], a_qg[j][i]);
+                    if constexpr (ALL) a_qb[j][i] += h[j][i];
+                }
+                affine8(h[j], S.post_gain, nullptr, col[j], p.w_dt, wvec, nv[j]);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    sums[0] = fmaf(h[j][i], n[j][i], sums[0]);
+                    sums[1] += h[j][i];
+                }
+            }
+            if (S.post != MUON_NORM_NONE) {
+                row_sum<TPR, 2>(sums, red, slot);
+                const float r = S.post_rstd[row];
+                const float s1 = sums[0] * p.inv_c, s0 = S.post == MUON_NORM_LAYER ? sums[1] * p.inv_c : 0.f;
+#pragma unroll
+                for (int j = 0; j < VPT; ++j)
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) h[j][i] = r * fmaf(-n[j][i], s1, h[j][i] - s0);
+            }
+#pragma unroll
+            for (int j = 0; j < VPT; ++j)
+                store8_dt(S.df, row * S.lddf + col[j], DT, p.vec && nv[j] == 8, nv[j], h[j]);
+        }
+#pragma unroll
+        for (int j = 0; j < VPT; ++j) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) d[j][i] *= S.skip;
+            store8_dt(S.dx, row * S.lddx + col[j], DT, p.vec && nv[j] == 8, nv[j], d[j]);
+        }
+        if constexpr (ALL) {
+            if (p.gate_sums && p.plan.parts == 0 && ((row + 1) % S.gate_rows == 0 || row + 1 == S.rows)) {
+                const long long grow = row / S.gate_rows;
+#pragma unroll
+                for (int j = 0; j < VPT; ++j) {
+                    store8_dt(S.dgate, grow * S.lddgate + col[j], DT, p.vec && nv[j] == 8, nv[j], a_gt[j]);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) a_gt[j][i] = 0.f;
+                }
+            }
+        }
+    }
+    auto put = [&](int v, const float (&a)[8], int j) {
+        store8_dt(p.part, ((long long)v * p.plan.runs + blockIdx.x) * S.cols + col[j], DT_FP32,
+                  (S.cols & 3) == 0 && nv[j] == 8, nv[j], a);
+    };
+#pragma unroll
+    for (int j = 0; j < VPT; ++j) {
+        if (S.d_pre_gain) put(V_PRE_GAIN, a_pg[j], j);
+        if (S.d_post_gain) put(V_POST_GAIN, a_qg[j], j);
+        if constexpr (ALL) {
+            if (S.d_pre_bias) put(V_PRE_BIAS, a_pb[j], j);
+            if (S.d_post_bias) put(V_POST_BIAS, a_qb[j], j);
+            if (p.gate_sums && p.plan.parts) put(V_COUNT, a_gt[j], j);
+        }
+    }
+}
+
+// Sums of the runs' parts: blockIdx.y < V_COUNT a vector gradient (over every
+// run), above that one shared gate row (over its runs).  32 columns x 32 lanes of
+// runs; a lane adds its runs in order, the lanes are added in order.
+__global__ void __launch_bounds__(1024) seam_join_kernel(const __grid_constant__ BwdParams p, int dt) {
+    __shared__ float sm[32][33];
+    const muon_seam_grad& S = p.s;
+    const int c = blockIdx.x * 32 + threadIdx.x;
+    int v = blockIdx.y;
+    void* dst;
+    long long first = 0, count = p.plan.runs, at = c;
+    int odt = p.w_dt;
+    float beta = S.beta;
+    if (v < V_COUNT) {
+        dst = v == V_POST_GAIN ? S.d_post_gain : v == V_POST_BIAS ? S.d_post_bias
+              : v == V_PRE_GAIN ? S.d_pre_gain : S.d_pre_bias;
+    } else {
+        const long long g = v - V_COUNT;
+        v = V_COUNT;
+        dst = S.dgate;
+        first = g * p.plan.parts;
+        count = p.plan.parts;
+        at = g * S.lddgate + c;
+        odt = dt;
+        beta = 0.f;
+    }
+    if (!dst) return;
+    float s = 0.f;
+    if (c < S.cols) {
+        const float* src = p.part + ((long long)v * p.plan.runs + first) * S.cols + c;
+#pragma unroll 4
+        for (long long r = threadIdx.y; r < count; r += 32) s += src[r * S.cols];
+    }
+    sm[threadIdx.y][threadIdx.x] = s;
+    __syncthreads();
+    if (threadIdx.y == 0 && c < S.cols) {
+        float t = 0.f;
+#pragma unroll
+        for (int k = 0; k < 32; ++k) t += sm[k][threadIdx.x];
+        if (beta != 0.f) t = fmaf(beta, ld_elem(dst, at, odt), t);
+        st_elem(dst, at, odt, t);
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Host
+// ---------------------------------------------------------------------------
+bool dtype_ok(int d) { return d == DT_BF16 || d == DT_FP16 || d == DT_FP32; }
+bool norm_ok(int k) { return k == MUON_NORM_NONE || k == MUON_NORM_RMS || k == MUON_NORM_LAYER; }
+
+// a kept checkpoint covers the seam's rows and columns
+bool kept_ok(const muon_act8& c, int rows, int cols) {
+    if (!c.q) return true;
+    return c.rows == rows && c.cols == cols && act8_valid(c);
+}
+
+muon_status check_seam(const muon_seam* s) {
+    if (!s || s->rows < 0 || s->cols < 1 || !norm_ok(s->post) || !norm_ok(s->pre)) return MUON_ERR_INVALID_ARG;
+    if (!(s->eps > 0.f) || !std::isfinite(s->eps) || !std::isfinite(s->skip) || !std::isfinite(s->scale))
+        return MUON_ERR_INVALID_ARG;
+    if (s->cols > MUON_SEAM_MAX_COLS) return MUON_ERR_UNSUPPORTED;
+    if (s->rows == 0) return MUON_OK;                  // nothing is read or written, pointers may be NULL
+    const long long c = s->cols;
+    const bool f = s->f != nullptr, pre = s->pre != MUON_NORM_NONE;
+    if (!s->x || s->ldx < c || (f && s->ldf < c)) return MUON_ERR_INVALID_ARG;
+    if (!f && (s->post != MUON_NORM_NONE || s->skip != 1.f || s->gate || s->post_gain || s->post_bias || s->post_c.q ||
+               s->post_rstd || s->out))
+        return MUON_ERR_INVALID_ARG;
+    if (f && (!s->out || s->ldout < c)) return MUON_ERR_INVALID_ARG;
+    if (s->gate && (s->ldgate < c || s->gate_rows < 1)) return MUON_ERR_INVALID_ARG;
+    if (!pre && (s->y || s->pre_gain || s->pre_bias || s->pre_c.q || s->pre_rstd)) return MUON_ERR_INVALID_ARG;
+    if (pre && (!s->y || s->ldy < c)) return MUON_ERR_INVALID_ARG;
+    if (!f && !pre) return MUON_ERR_INVALID_ARG;       // nothing to make
+    return kept_ok(s->post_c, s->rows, s->cols) && kept_ok(s->pre_c, s->rows, s->cols) ? MUON_OK : MUON_ERR_INVALID_ARG;
+}
+
+muon_status check_grad(const muon_seam_grad* s) {
+    if (!s || s->rows < 0 || s->cols < 1 || !norm_ok(s->post) || !norm_ok(s->pre)) return MUON_ERR_INVALID_ARG;
+    if (!std::isfinite(s->skip) || !std::isfinite(s->scale) || !std::isfinite(s->beta)) return MUON_ERR_INVALID_ARG;
+    if (s->cols > MUON_SEAM_MAX_COLS) return MUON_ERR_UNSUPPORTED;
+    if (s->rows == 0) return MUON_OK;                  // only the vector gradients are written (beta times what they hold)
+    const long long c = s->cols;
+    const bool pre = s->pre != MUON_NORM_NONE, f = s->df != nullptr;
+    if (pre && (!s->dy || !s->pre_c.q || !s->pre_rstd || s->lddy < c)) return MUON_ERR_INVALID_ARG;
+    if (!pre && (s->dy || s->pre_gain || s->d_pre_gain || s->d_pre_bias)) return MUON_ERR_INVALID_ARG;
+    if (s->dout && s->lddout < c) return MUON_ERR_INVALID_ARG;
+    if (!s->dx || s->lddx < c || !(pre || s->dout)) return MUON_ERR_INVALID_ARG;
+    if (!f && (s->post != MUON_NORM_NONE || s->skip != 1.f || s->gate || s->dgate || s->post_gain || s->post_bias ||
+               s->d_post_gain || s->d_post_bias))
+        return MUON_ERR_INVALID_ARG;
+    if (f && (s->lddf < c || s->df == s->dx)) return MUON_ERR_INVALID_ARG;
+    if (s->gate && (s->ldgate < c || s->gate_rows < 1)) return MUON_ERR_INVALID_ARG;
+    if (s->dgate && (!s->gate || s->lddgate < c)) return MUON_ERR_INVALID_ARG;
+    if (s->post != MUON_NORM_NONE && !s->post_rstd) return MUON_ERR_INVALID_ARG;
+    if (!s->post_c.q && (s->post != MUON_NORM_NONE || s->dgate || s->d_post_gain)) return MUON_ERR_INVALID_ARG;
+    return kept_ok(s->post_c, s->rows, s->cols) && kept_ok(s->pre_c, s->rows, s->cols) ? MUON_OK : MUON_ERR_INVALID_ARG;
+}
+
+bool gate_sums(const muon_seam_grad& s) { return s.rows > 0 && s.dgate && s.gate_rows > 1; }
+bool any_vector(const muon_seam_grad& s) { return s.d_post_gain || s.d_post_bias || s.d_pre_gain || s.d_pre_bias; }
+
+size_t part_bytes(const muon_seam_grad& s, const RunPlan& P) {
+    if (!any_vector(s) && !(gate_sums(s) && P.parts)) return 0;
+    return (size_t)(V_COUNT + 1) * P.runs * s.cols * sizeof(float);
+}
+
+int sm_count() {
+    int dev = 0, nsm = kPlanSms;
+    cudaGetDevice(&dev);
+    cudaDeviceGetAttribute(&nsm, cudaDevAttrMultiProcessorCount, dev);
+    return nsm;
+}
+
+template <typename T>
+void launch_fwd(const FwdParams& p, cudaStream_t s) {
+    const int c = p.s.cols;
+#define SEAM_FWD(TPR, VPT)                                                                              \
+    do {                                                                                                \
+        const int rpb = TPR == 32 ? 4 : 1, threads = TPR == 32 ? 128 : TPR;                             \
+        const long long blocks = ((long long)p.s.rows + rpb - 1) / rpb;                                 \
+        const int grid = (int)std::min<long long>(blocks, (long long)sm_count() * (2048 / threads));    \
+        seam_fwd_kernel<T, TPR, VPT><<<grid, threads, 0, s>>>(p);                                       \
+    } while (0)
+    if (c <= 256) SEAM_FWD(32, 1);
+    else if (c <= 512) SEAM_FWD(32, 2);
+    else if (c <= 1024) SEAM_FWD(32, 4);
+    else if (c <= 2048) SEAM_FWD(128, 2);
+    else if (c <= 4096) SEAM_FWD(256, 2);
+    else if (c <= 8192) SEAM_FWD(512, 2);
+    else SEAM_FWD(1024, 2);
+#undef SEAM_FWD
+}
+
+template <typename T>
+void launch_bwd(const BwdParams& p, bool all, cudaStream_t s) {
+    const int c = p.s.cols;
+    const unsigned grid = (unsigned)p.plan.runs;
+#define SEAM_BWD(TPR, VPT)                                                       \
+    do {                                                                         \
+        if (all) seam_bwd_kernel<T, TPR, VPT, true><<<grid, TPR, 0, s>>>(p);     \
+        else seam_bwd_kernel<T, TPR, VPT, false><<<grid, TPR, 0, s>>>(p);        \
+    } while (0)
+    if (c <= 256) SEAM_BWD(32, 1);
+    else if (c <= 512) SEAM_BWD(64, 1);
+    else if (c <= 1024) SEAM_BWD(128, 1);
+    else if (c <= 2048) SEAM_BWD(256, 1);
+    else if (c <= 4096) SEAM_BWD(512, 1);
+    else if (c <= 8192) SEAM_BWD(1024, 1);
+    else SEAM_BWD(1024, 2);
+#undef SEAM_BWD
+}
+
+bool vec_ok(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
+
+}  // namespace
+}  // namespace muon
+
+using namespace muon;
+
+extern "C" {
+
+muon_status seam_forward(const muon_seam* seam, muon_dtype x_dtype, muon_dtype w_dtype, int* d_status,
+                         muon_stream_t stream) {
+    if (!dtype_ok(x_dtype) || !dtype_ok(w_dtype)) return MUON_ERR_INVALID_ARG;
+    muon_status st = check_seam(seam);
+    if (st != MUON_OK) return st;
+    st = check_device();
+    if (st != MUON_OK) return st;
+    if (seam->rows == 0) return MUON_OK;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    FwdParams p;
+    p.s = *seam;
+    p.inv_c = 1.f / (float)seam->cols;
+    p.w_dt = w_dtype;
+    p.d_status = d_status;
+    const int esz = dt_size(x_dtype);
+    const muon_seam& q = *seam;
+    p.vec = rows_aligned(q.x, q.ldx, esz) && (!q.f || (rows_aligned(q.f, q.ldf, esz) && rows_aligned(q.out, q.ldout, esz))) &&
+            (!q.gate || rows_aligned(q.gate, q.ldgate, esz)) && (!q.y || rows_aligned(q.y, q.ldy, esz));
+    p.wvec = vec_ok(q.post_gain) && vec_ok(q.post_bias) && vec_ok(q.pre_gain) && vec_ok(q.pre_bias);
+    const double el = (double)q.rows * q.cols;
+    trace_begin(MUON_KERNEL_SEAM, el * (esz * (1 + (q.f ? 2 : 0) + (q.y ? 1 : 0) + (q.gate && q.gate_rows == 1 ? 1 : 0)) +
+                                        33.0 / 32 * ((q.post_c.q ? 1 : 0) + (q.pre_c.q ? 1 : 0))), s);
+    if (x_dtype == MUON_BF16) launch_fwd<__nv_bfloat16>(p, s);
+    else if (x_dtype == MUON_FP16) launch_fwd<__half>(p, s);
+    else launch_fwd<float>(p, s);
+    trace_end(s);
+    return cudaGetLastError() == cudaSuccess ? MUON_OK : MUON_ERR_CUDA;
+}
+
+muon_status seam_backward_workspace_size(const muon_seam_grad* seam, size_t* bytes) {
+    if (!bytes) return MUON_ERR_INVALID_ARG;
+    const muon_status st = check_grad(seam);
+    if (st != MUON_OK) return st;
+    *bytes = part_bytes(*seam, plan_runs(seam->rows, seam->cols, seam->gate_rows, gate_sums(*seam)));
+    return MUON_OK;
+}
+
+muon_status seam_backward(const muon_seam_grad* seam, muon_dtype x_dtype, muon_dtype w_dtype, void* workspace,
+                          size_t ws_bytes, int* d_status, muon_stream_t stream) {
+    (void)d_status;
+    if (!dtype_ok(x_dtype) || !dtype_ok(w_dtype)) return MUON_ERR_INVALID_ARG;
+    muon_status st = check_grad(seam);
+    if (st != MUON_OK) return st;
+    BwdParams p;
+    p.s = *seam;
+    const muon_seam_grad& q = *seam;
+    p.gate_sums = gate_sums(q);
+    p.plan = plan_runs(q.rows, q.cols, q.gate_rows, p.gate_sums);
+    const size_t need = part_bytes(q, p.plan);
+    if (need && (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255) || ws_bytes < need))
+        return MUON_ERR_WORKSPACE;
+    st = check_device();
+    if (st != MUON_OK) return st;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    p.part = static_cast<float*>(workspace);
+    p.inv_c = 1.f / (float)q.cols;
+    p.w_dt = w_dtype;
+    const int esz = dt_size(x_dtype);
+    p.vec = (!q.dy || rows_aligned(q.dy, q.lddy, esz)) && (!q.dout || rows_aligned(q.dout, q.lddout, esz)) &&
+            rows_aligned(q.dx, q.lddx, esz) && (!q.df || rows_aligned(q.df, q.lddf, esz)) &&
+            (!q.gate || rows_aligned(q.gate, q.ldgate, esz)) && (!q.dgate || rows_aligned(q.dgate, q.lddgate, esz));
+    p.wvec = vec_ok(q.post_gain) && vec_ok(q.post_bias) && vec_ok(q.pre_gain);
+    const bool all = q.d_post_bias || q.d_pre_bias || p.gate_sums;
+    const bool tok = q.gate && q.gate_rows == 1;
+    if (p.plan.runs > 0) {
+        trace_begin(MUON_KERNEL_SEAM, (double)q.rows * q.cols *
+                        (esz * (1.0 + (q.dy ? 1 : 0) + (q.dout ? 1 : 0) + (q.df ? 1 : 0) + (tok ? 1 : 0) + (tok && q.dgate ? 1 : 0)) +
+                         33.0 / 32 * ((q.dy ? 1 : 0) + (q.post_c.q ? 1 : 0))), s);
+        if (x_dtype == MUON_BF16) launch_bwd<__nv_bfloat16>(p, all, s);
+        else if (x_dtype == MUON_FP16) launch_bwd<__half>(p, all, s);
+        else launch_bwd<float>(p, all, s);
+        trace_end(s);
+        if (cudaGetLastError() != cudaSuccess) return MUON_ERR_CUDA;
+    }
+    const long long groups = p.gate_sums && p.plan.parts ? p.plan.runs / p.plan.parts : 0;
+    if (any_vector(q) || groups) {
+        const int xt = (q.cols + 31) / 32;
+        trace_begin(MUON_KERNEL_SEAM, 4.0 * p.plan.runs * q.cols, s);
+        seam_join_kernel<<<dim3(xt, (unsigned)(V_COUNT + groups)), dim3(32, 32), 0, s>>>(p, x_dtype);
+        trace_end(s);
+        if (cudaGetLastError() != cudaSuccess) return MUON_ERR_CUDA;
+    }
+    return MUON_OK;
+}
+
+}  // extern "C"

@@ -1,0 +1,194 @@
+"""Host-side checks of the checkpoint, gradient and seam entry points (CPU): the
+descriptors' layout against the header, refusals before any launch (the pointers below
+are never read), workspace queries, and the binding's own checks."""
+import ctypes
+import math
+import os
+import subprocess
+
+import pytest
+import torch
+
+import muon_family_optimizer_b200 as mo
+from muon_family_optimizer_b200 import build as mbuild
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+P = 1 << 20          # an address that is never read
+
+
+@pytest.fixture(scope="module")
+def L():
+    mbuild.build()
+    return mo.lib()
+
+
+STRUCTS = {"muon_act8": mo.Act8, "muon_act8_item": mo.Act8Item, "muon_act8_grad_item": mo.Act8GradItem,
+           "muon_seam": mo.Seam, "muon_seam_grad": mo.SeamGrad}
+
+
+def test_struct_layouts_match_header(tmp_path):
+    lines = []
+    for name, cls in STRUCTS.items():
+        lines.append(f'printf("{name} %zu\\n", sizeof({name}));')
+        lines += [f'printf("{name}.{f} %zu\\n", offsetof({name}, {f}));' for f, _ in cls._fields_]
+    lines.append('printf("MUON_SEAM_MAX_COLS %d\\n", MUON_SEAM_MAX_COLS);')
+    src = tmp_path / "probe.c"
+    src.write_text('#include <stdio.h>\n#include <stddef.h>\n#include "muon.h"\nint main(void){%s return 0;}' % "\n".join(lines))
+    exe = tmp_path / "probe"
+    subprocess.check_call(["gcc", "-I", os.path.join(ROOT, "include"), "-o", str(exe), str(src)])
+    got = dict(line.rsplit(" ", 1) for line in subprocess.check_output([str(exe)], text=True).splitlines())
+    assert int(got.pop("MUON_SEAM_MAX_COLS")) == mo.SEAM_MAX_COLS
+    for key, val in got.items():
+        if "." in key:
+            name, field = key.split(".")
+            assert getattr(STRUCTS[name], field).offset == int(val), key
+        else:
+            assert ctypes.sizeof(STRUCTS[key]) == int(val), key
+
+
+def _ckpt(**kw):
+    d = dict(rows=4, cols=40, q=P, ldq=48, e=P, lde=2)
+    d.update(kw)
+    return mo.Act8(*[d[k] for k in ("rows", "cols", "q", "ldq", "e", "lde")])
+
+
+BAD_CKPT = [dict(rows=-1), dict(cols=0), dict(q=None), dict(e=None), dict(q=P + 8), dict(ldq=40), dict(ldq=32),
+            dict(lde=1)]
+
+
+@pytest.mark.parametrize("bad", BAD_CKPT + [dict(x=None), dict(ldx=39), dict(n=0), dict(dt=3), dict(dt=-1)])
+@pytest.mark.parametrize("fn", ["act8_encode_batched", "act8_decode_batched"])
+def test_encode_decode_refusals(L, fn, bad):
+    bad = dict(bad)
+    n, dt = bad.pop("n", 1), bad.pop("dt", mo.BF16)
+    x, ldx = bad.pop("x", P), bad.pop("ldx", 40)
+    arr = (mo.Act8Item * 1)(mo.Act8Item(_ckpt(**bad), x, ldx))
+    args = (arr, n, dt) + ((None,) if fn == "act8_encode_batched" else ()) + (None,)
+    assert getattr(L, fn)(*args) == mo.ERR_INVALID_ARG
+    if not bad:
+        args = (None,) + args[1:]
+        assert getattr(L, fn)(*args) == mo.ERR_INVALID_ARG
+
+
+def _grad(**kw):
+    c = _ckpt(**{k: kw.pop(k) for k in list(kw) if k in ("rows", "cols", "q", "ldq", "e", "lde")})
+    d = dict(dY=P, lddy=24, out=24, G=P, gain=None, shift=None, dy_sum=None, beta=0.0)
+    d.update(kw)
+    return mo.Act8GradItem(c, *[d[k] for k in ("dY", "lddy", "out", "G", "gain", "shift", "dy_sum", "beta")])
+
+
+@pytest.mark.parametrize("bad", BAD_CKPT + [dict(dY=None), dict(lddy=23), dict(out=0), dict(G=None), dict(shift=P),
+                                            dict(dy_sum=P), dict(beta=math.nan), dict(beta=math.inf)])
+def test_grad_refusals(L, bad):
+    arr = (mo.Act8GradItem * 2)(_grad(), _grad(**bad))
+    out = ctypes.c_size_t(7)
+    assert L.act8_grad_workspace_size(arr, 2, mo.BF16, ctypes.byref(out)) == mo.ERR_INVALID_ARG
+    assert L.act8_grad_batched(arr, 2, mo.BF16, mo.BF16, P, 1 << 40, None, None) == mo.ERR_INVALID_ARG
+
+
+def test_grad_refusals_of_the_call(L):
+    arr = (mo.Act8GradItem * 1)(_grad())
+    out = ctypes.c_size_t(0)
+    assert L.act8_grad_workspace_size(arr, 1, 3, ctypes.byref(out)) == mo.ERR_INVALID_ARG
+    assert L.act8_grad_workspace_size(arr, 1, mo.BF16, None) == mo.ERR_INVALID_ARG
+    assert L.act8_grad_workspace_size(arr, 0, mo.BF16, ctypes.byref(out)) == mo.ERR_INVALID_ARG
+    assert L.act8_grad_workspace_size(None, 1, mo.BF16, ctypes.byref(out)) == mo.ERR_INVALID_ARG
+    assert L.act8_grad_batched(arr, 1, 3, mo.BF16, None, 0, None, None) == mo.ERR_INVALID_ARG
+    assert L.act8_grad_batched(arr, 1, mo.BF16, 5, None, 0, None, None) == mo.ERR_INVALID_ARG
+
+
+def _seam(**kw):
+    d = dict(rows=4, cols=40, post=1, pre=1, eps=1e-5, skip=1.0, scale=1.0, x=P, ldx=40, f=P, ldf=40, gate=P, ldgate=40,
+             gate_rows=3, post_gain=P, post_bias=None, pre_gain=P, pre_bias=None, out=P, ldout=40, y=P, ldy=40,
+             post_c=_ckpt(), pre_c=_ckpt(), post_rstd=P, pre_rstd=P)
+    d.update(kw)
+    return mo.Seam(*[d[f] for f, _ in mo.Seam._fields_])
+
+
+NOTHING = mo.Act8(0, 0, None, 0, None, 0)
+BAD_SEAM = [dict(rows=-1), dict(cols=0), dict(post=3), dict(pre=-1), dict(eps=0.0), dict(eps=-1.0), dict(eps=math.nan),
+            dict(eps=math.inf), dict(skip=math.inf), dict(scale=math.nan), dict(x=None), dict(ldx=39), dict(ldf=39),
+            dict(out=None), dict(ldout=39), dict(y=None), dict(ldy=39), dict(ldgate=39), dict(gate_rows=0),
+            dict(f=None), dict(pre=0), dict(post_c=_ckpt(rows=3)), dict(pre_c=_ckpt(cols=41)),
+            dict(pre_c=_ckpt(ldq=40)), dict(f=None, post=0, gate=None, post_gain=None, post_c=NOTHING, post_rstd=None)]
+
+
+@pytest.mark.parametrize("bad", BAD_SEAM)
+def test_seam_refusals(L, bad):
+    assert L.seam_forward(ctypes.byref(_seam(**bad)), mo.BF16, mo.BF16, None, None) == mo.ERR_INVALID_ARG
+
+
+def test_seam_refusals_of_the_call(L):
+    s = _seam()
+    assert L.seam_forward(None, mo.BF16, mo.BF16, None, None) == mo.ERR_INVALID_ARG
+    assert L.seam_forward(ctypes.byref(s), 3, mo.BF16, None, None) == mo.ERR_INVALID_ARG
+    assert L.seam_forward(ctypes.byref(s), mo.BF16, -1, None, None) == mo.ERR_INVALID_ARG
+    wide = dict(cols=16385, ldx=16385, ldf=16385, ldgate=16385, ldout=16385, ldy=16385, post_c=NOTHING, pre_c=NOTHING)
+    assert L.seam_forward(ctypes.byref(_seam(**wide)), mo.BF16, mo.BF16, None, None) == mo.ERR_UNSUPPORTED
+    # a residual sum without f, and no output at all
+    lone = dict(f=None, post=0, gate=None, post_gain=None, post_c=NOTHING, post_rstd=None, out=None)
+    assert L.seam_forward(ctypes.byref(_seam(**lone, skip=0.5)), mo.BF16, mo.BF16, None, None) == mo.ERR_INVALID_ARG
+    none = dict(lone, pre=0, y=None, pre_gain=None, pre_c=NOTHING, pre_rstd=None)
+    assert L.seam_forward(ctypes.byref(_seam(**none)), mo.BF16, mo.BF16, None, None) == mo.ERR_INVALID_ARG
+
+
+def _back(**kw):
+    d = dict(rows=4, cols=40, post=1, pre=1, skip=1.0, scale=1.0, gate=P, ldgate=40, gate_rows=3, post_gain=P,
+             post_bias=None, pre_gain=P, post_c=_ckpt(), pre_c=_ckpt(), post_rstd=P, pre_rstd=P, dy=P, lddy=40, dout=P,
+             lddout=40, dx=P, lddx=40, df=2 * P, lddf=40, dgate=P, lddgate=40, d_post_gain=P, d_post_bias=None,
+             d_pre_gain=P, d_pre_bias=None, beta=0.0)
+    d.update(kw)
+    return mo.SeamGrad(*[d[f] for f, _ in mo.SeamGrad._fields_])
+
+
+BAD_BACK = [dict(rows=-1), dict(cols=0), dict(post=3), dict(pre=7), dict(skip=math.nan), dict(scale=math.inf),
+            dict(beta=math.nan), dict(gate_rows=0), dict(ldgate=39), dict(lddgate=39), dict(gate=None), dict(dy=None),
+            dict(lddy=39), dict(lddout=39), dict(dx=None), dict(lddx=39), dict(lddf=39), dict(df=P), dict(df=None),
+            dict(post_c=NOTHING), dict(pre_c=NOTHING), dict(post_rstd=None), dict(pre_rstd=None),
+            dict(post_c=_ckpt(rows=5)), dict(pre_c=_ckpt(q=P + 1)), dict(pre=0), dict(pre=0, dy=None),
+            dict(post=0, post_c=NOTHING)]
+
+
+@pytest.mark.parametrize("bad", BAD_BACK)
+def test_seam_backward_refusals(L, bad):
+    s, out = _back(**bad), ctypes.c_size_t(0)
+    assert L.seam_backward_workspace_size(ctypes.byref(s), ctypes.byref(out)) == mo.ERR_INVALID_ARG
+    assert L.seam_backward(ctypes.byref(s), mo.BF16, mo.BF16, P, 1 << 40, None, None) == mo.ERR_INVALID_ARG
+
+
+def test_seam_backward_workspace(L):
+    s, out = _back(), ctypes.c_size_t(0)
+    assert L.seam_backward_workspace_size(ctypes.byref(s), ctypes.byref(out)) == mo.OK and out.value > 0
+    need = out.value
+    for ws, size in ((None, need), (P, need - 1), (P + 128, need)):
+        assert L.seam_backward(ctypes.byref(s), mo.BF16, mo.BF16, ws, size, None, None) == mo.ERR_WORKSPACE
+    assert L.seam_backward_workspace_size(ctypes.byref(s), None) == mo.ERR_INVALID_ARG
+    # nothing to sum over tokens: no workspace
+    s = _back(d_post_gain=None, d_pre_gain=None, gate_rows=1)
+    assert L.seam_backward_workspace_size(ctypes.byref(s), ctypes.byref(out)) == mo.OK and out.value == 0
+    wide = _back(cols=20000, ldgate=20000, lddy=20000, lddout=20000, lddx=20000, lddf=20000, lddgate=20000,
+                 post_c=_ckpt(cols=20000, ldq=20000, lde=625), pre_c=_ckpt(cols=20000, ldq=20000, lde=625))
+    assert L.seam_backward_workspace_size(ctypes.byref(wide), ctypes.byref(out)) == mo.ERR_UNSUPPORTED
+
+
+def test_act8_empty_rows_are_aligned():
+    c = mo.act8_empty(5, 70, device="cpu")
+    assert c["q"].shape == (5, 70) and c["q"].stride(0) == 80 and c["e"].shape == (5, 3)
+    assert c["q"].dtype == torch.int8 and c["e"].dtype == torch.uint8
+    assert mo.act8_empty(0, 70, device="cpu")["q"].shape == (0, 70)
+
+
+def test_binding_refuses_other_devices_and_shapes():
+    # host tensors never reach the library
+    c = mo.act8_empty(4, 40, device="cpu")
+    x = torch.zeros(4, 40)
+    for call in (lambda: mo.act8_encode_batched([dict(x=x, **c)]), lambda: mo.act8_decode_batched([dict(x=x, **c)]),
+                 lambda: mo.act8_grad_batched([dict(dY=torch.zeros(4, 8), G=torch.zeros(8, 40), **c)]),
+                 lambda: mo.seam_forward(dict(x=x, y=x, pre="rms")),
+                 lambda: mo.seam_backward(dict(dx=x, dout=x))):
+        with pytest.raises(ValueError):
+            call()
+    with pytest.raises(ValueError):
+        mo.seam_forward(dict(x=x, y=x, pre="batch"))
+    with pytest.raises(ValueError):
+        mo.seam_forward(dict(x=x[0], y=x, pre="rms"))

@@ -1,0 +1,335 @@
+"""GPU parity of the 8-bit activation checkpoints and the weight gradients made from
+them, against the fp64 oracle (oracle/acts.py).
+
+Tolerances, from the arithmetic:
+  codes and exponents   equal: x 2^-e is exact and rounded once, in both
+  values                equal: q 2^e is exact in bfloat16 and fp32; fp16 one rounding, the same in both
+  G     a product of a dY and a checkpoint value is exact in fp32 (at most 11 + 11 significant
+        bits; fp32 dY: three bfloat16 parts that sum to it), so an element's error is that of the
+        fp32 sum of T (fp32 dY: 3 T) terms, at most 2^-23 each times S = sum |dY| |X^| (a sum that
+        truncates loses a whole unit in the last place per addition), of the three operations of the
+        epilogue, and the rounding to G's type: half a unit, eps / 2 of the result.
+"""
+import numpy as np
+import pytest
+import torch
+
+import muon_family_optimizer_b200 as mo
+from oracle import acts
+
+pytestmark = pytest.mark.gpu
+
+DTS = [torch.bfloat16, torch.float16, torch.float32]
+GUARD = 77          # what memory outside a result holds, before and after
+
+
+def _np(t):
+    return t.detach().double().cpu().numpy()
+
+
+def _x(T, C, dt, seed=0, spread=3.0):
+    g = torch.Generator().manual_seed(seed)
+    x = torch.randn(T, C, generator=g) * torch.exp(spread * torch.randn(T, 1, generator=g))
+    if T and C > 40:
+        x[0, :32] = 0                               # an empty block
+    if T > 2:
+        x[2] = 0                                    # an empty row
+    return x.to(dt).cuda()
+
+
+def _padded(T, C, pad, dtype, fill=GUARD, base=0):
+    """A T x C view with row stride C + pad, `base` elements into its buffer, and the buffer."""
+    buf = torch.full((base + T * (C + pad) + 64,), fill, dtype=dtype, device="cuda")
+    return buf.as_strided((T, C), (C + pad, 1), base), buf
+
+
+def _ckpt_of(x):
+    c = mo.act8_empty(*x.shape)
+    mo.act8_encode_batched([dict(x=x, **c)])
+    return c
+
+
+@pytest.mark.parametrize("dt", DTS)
+@pytest.mark.parametrize("T,C", [(1, 1), (1, 31), (3, 32), (5, 33), (4, 40), (7, 255), (2, 256), (9, 1000), (130, 768),
+                                 (33, 4097)])
+@pytest.mark.parametrize("layout", ["dense", "strided", "unaligned"])
+def test_encode_and_decode(dt, T, C, layout):
+    x = _x(T, C, dt, seed=T + C)
+    if layout != "dense":
+        v, _ = _padded(T, C, 24 if layout == "strided" else 3, dt, 0, 0 if layout == "strided" else 1)
+        v.copy_(x)
+        x = v
+    ld = (C + 15) // 16 * 16 + 32
+    qb = torch.full((T * ld,), GUARD, dtype=torch.int8, device="cuda")
+    q = qb.view(T, ld)[:, :C]
+    nb = -(-C // 32)
+    e, eb = _padded(T, nb, 5, torch.uint8)
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    mo.act8_encode_batched([dict(x=x, q=q, e=e)], d_status=status)
+    q_ref, e_ref = acts.encode(_np(x))
+    assert int(status.item()) == 0
+    assert np.array_equal(q.cpu().numpy(), q_ref) and np.array_equal(e.cpu().numpy(), e_ref)
+    assert bool((qb.view(T, ld)[:, C:] == GUARD).all())            # the rest of the buffers is untouched
+    assert int((eb == GUARD).sum()) >= eb.numel() - T * nb
+    for to in DTS:
+        out, ob = _padded(T, C, 8, to)
+        mo.act8_decode_batched([dict(x=out, q=q, e=e)])
+        ref = torch.from_numpy(acts.decode(q_ref, e_ref)).to(to)
+        assert torch.equal(out.cpu(), ref)
+        assert bool((ob.as_strided((T, 8), (C + 8, 1), C) == GUARD).all())
+
+
+def test_encode_marks_blocks_it_cannot_hold():
+    x = torch.ones(4, 100, device="cuda")
+    x[0, 40] = float("nan")
+    x[1, 99] = float("inf")
+    x[2, 0] = 3e38
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    c = mo.act8_empty(4, 100)
+    mo.act8_encode_batched([dict(x=x, **c)], d_status=status)
+    assert int(status.item()) == mo.FLAG_NONFINITE
+    out = torch.empty_like(x)
+    mo.act8_decode_batched([dict(x=out, **c)])
+    nan = torch.isnan(out).cpu()
+    expect = torch.zeros(4, 100, dtype=torch.bool)
+    expect[0, 32:64] = True
+    expect[1, 96:] = True
+    expect[2, :32] = True
+    assert torch.equal(nan, expect)
+    q_ref, e_ref = acts.encode(_np(x))
+    assert np.array_equal(c["q"].cpu().numpy(), q_ref) and np.array_equal(c["e"].cpu().numpy(), e_ref)
+
+
+def test_many_items_of_ragged_length_one_of_them_empty():
+    # more items than one launch takes; an item without rows changes nothing
+    sizes = [(0, 64)] + [(1 + 7 * i % 23, 1 + 37 * i % 300) for i in range(130)] + [(0, 5)]
+    xs = [_x(t, c, torch.bfloat16, seed=i) for i, (t, c) in enumerate(sizes)]
+    cs = [mo.act8_empty(t, c) for t, c in sizes]
+    mo.act8_encode_batched([dict(x=x, **c) for x, c in zip(xs, cs)])
+    outs = [torch.empty_like(x) for x in xs]
+    mo.act8_decode_batched([dict(x=x, **c) for x, c in zip(outs, cs)])
+    for x, c, o in zip(xs, cs, outs):
+        q_ref, e_ref = acts.encode(_np(x))
+        assert np.array_equal(c["q"].cpu().numpy(), q_ref) and np.array_equal(c["e"].cpu().numpy(), e_ref)
+        assert torch.equal(o.double().cpu(), torch.from_numpy(acts.decode(q_ref, e_ref)))
+
+
+def test_offsets_beyond_32_bits():
+    # rows 2^31 + 16 bytes apart: row 2 starts past 2^32
+    ld, T, C = 2 ** 31 + 16, 3, 72
+    buf = torch.empty(2 * ld + C + 16, dtype=torch.int8, device="cuda")
+    q = buf.as_strided((T, C), (ld, 1))
+    c = dict(q=q, e=torch.empty(T, 3, dtype=torch.uint8, device="cuda"))
+    x = _x(T, C, torch.bfloat16, seed=5, spread=0.5)
+    x[2] = 1.5
+    mo.act8_encode_batched([dict(x=x, **c)])
+    q_ref, e_ref = acts.encode(_np(x))
+    assert np.array_equal(q.cpu().numpy(), q_ref)
+    dY = torch.randn(T, 40, generator=torch.Generator().manual_seed(1)).to(torch.bfloat16).cuda()
+    G = torch.empty(40, C, device="cuda")
+    items = [dict(dY=dY, G=G, **c)]
+    mo.act8_grad_batched(items, _ws(items))
+    _check_G(G, dY, acts.decode(q_ref, e_ref))
+    out = torch.empty_like(x)
+    mo.act8_decode_batched([dict(x=out, **c)])
+    assert torch.equal(out.double().cpu(), torch.from_numpy(acts.decode(q_ref, e_ref)))
+
+
+# ---------------------------------------------------------------- gradients
+def _ws(items):
+    n = mo.act8_grad_workspace_size(items)
+    return torch.full((n,), 0xFF, dtype=torch.uint8, device="cuda") if n else None      # no state: any contents
+
+
+def _check_G(G, dY, X, gain=None, shift=None, dy_sum=None, beta=0.0, G0=None):
+    if dY.dtype == torch.float16:
+        X = torch.from_numpy(X).to(torch.float16).double().numpy()
+    d = _np(dY)
+    ref = acts.grad(d, X, gain=gain, shift=shift, dy_sum=dy_sum, beta=beta, G=G0)
+    terms = d.shape[0] * (3 if dY.dtype == torch.float32 else 1)
+    S = np.abs(d).T @ np.abs(X)
+    if gain is not None:
+        S = S * np.abs(gain)[None, :]
+    own = np.abs(S)
+    if shift is not None:
+        own = own + np.abs(np.outer(dy_sum, shift))
+    if beta:
+        own = own + np.abs(beta * G0)
+    half = torch.finfo(G.dtype).eps / 2
+    tiny = torch.finfo(G.dtype).smallest_normal * torch.finfo(G.dtype).eps      # a step of the subnormals
+    tol = terms * 2.0 ** -23 * S + 3 * 2.0 ** -23 * own
+    tol = tol + half * (np.abs(ref) + tol) + tiny
+    got = _np(G)
+    assert np.isfinite(got).all()
+    bad = np.abs(got - ref) > tol
+    assert not bad.any(), (float(np.max(np.abs(got - ref) - tol)), np.argwhere(bad)[:5].tolist())
+
+
+def _case(T, O, C, dt, wt, seed=0, gain=False, shift=False, beta=0.0, pad=0, base=0):
+    g = torch.Generator().manual_seed(seed)
+    x = _x(T, C, torch.float32, seed=seed + 1, spread=0.3)
+    c = _ckpt_of(x) if T else mo.act8_empty(0, C)
+    dY, _ = _padded(T, O, pad, dt, 0, base)
+    dY.copy_((torch.randn(T, O, generator=g) * 0.1).to(dt))
+    G, buf = _padded(O, C, 0, wt, GUARD)
+    it = dict(dY=dY, G=G, beta=beta, **c)
+    if gain:
+        it["gain"] = (1 + torch.randn(C, generator=g)).to(wt).cuda()
+    if shift:
+        it["shift"] = torch.randn(C, generator=g).to(wt).cuda()
+        it["dy_sum"] = dY.float().sum(0)
+    if beta:
+        G.copy_(torch.randn(O, C, generator=g).to(wt))
+    return it, buf
+
+
+def _run_and_check(items, status=None):
+    before = [_np(it["G"]) if it["beta"] else None for it in items]
+    mo.act8_grad_batched(items, _ws(items), d_status=status)
+    for it, G0 in zip(items, before):
+        X = acts.decode(it["q"].cpu().numpy(), it["e"].cpu().numpy())
+        opt = {k: _np(it[k]) for k in ("gain", "shift", "dy_sum") if it.get(k) is not None}
+        _check_G(it["G"], it["dY"], X, beta=it["beta"], G0=G0, **opt)
+
+
+SHAPES = [(1, 1, 1), (1, 64, 32), (2, 5, 3), (15, 33, 65), (16, 128, 128), (63, 130, 64), (64, 256, 256),
+          (65, 257, 129), (100, 96, 520), (200, 300, 264), (333, 200, 768), (1000, 520, 72), (1025, 768, 256)]
+
+
+@pytest.mark.parametrize("dt", DTS)
+@pytest.mark.parametrize("T,O,C", SHAPES)
+def test_grad(dt, T, O, C):
+    items = []
+    for k, wt in enumerate([torch.float32, dt]):
+        it, buf = _case(T, O, C, dt, wt, seed=T + O + C + k, gain=k == 1)
+        _run_and_check([it])
+        assert bool((buf[O * C:] == GUARD).all())
+        items.append(it)
+
+
+@pytest.mark.parametrize("dt", DTS)
+@pytest.mark.parametrize("gain,shift,beta", [(True, True, 0.0), (False, True, 1.0), (True, False, 0.5), (False, False, -1.0)])
+def test_grad_epilogue(dt, gain, shift, beta):
+    for T, O, C in [(70, 72, 104), (0, 40, 64), (3, 300, 33)]:
+        for wt in (torch.float32, torch.bfloat16):
+            it, _ = _case(T, O, C, dt, wt, seed=3, gain=gain, shift=shift, beta=beta)
+            _run_and_check([it])
+
+
+@pytest.mark.parametrize("pad,base", [(8, 0), (1, 0), (0, 1), (3, 5)])
+@pytest.mark.parametrize("dt", DTS)
+def test_grad_strided_and_unaligned_dY(dt, pad, base):
+    it, _ = _case(77, 136, 96, dt, torch.float32, seed=4, pad=pad, base=base)
+    _run_and_check([it])
+
+
+def test_grad_without_tokens_writes_zeros():
+    it, buf = _case(0, 130, 70, torch.bfloat16, torch.bfloat16)
+    it["G"].fill_(float("nan"))
+    mo.act8_grad_batched([it], _ws([it]))
+    assert not it["G"].any()
+    assert bool((buf[130 * 70:] == GUARD).all())
+
+
+def test_grad_beta_zero_does_not_read_G():
+    it, _ = _case(40, 64, 64, torch.bfloat16, torch.float32, seed=6)
+    it["G"].fill_(float("nan"))
+    _run_and_check([it])
+
+
+def test_grad_ragged_experts_in_one_call():
+    # experts with 0, 1, few and many tokens, of several shapes, a checkpoint and a dY used twice, more than one launch
+    items = [_case(t, o, c, torch.bfloat16, torch.float32, seed=i, gain=i % 2 == 0)[0]
+             for i, (t, o, c) in enumerate([(0, 72, 64), (1, 72, 64), (37, 72, 64), (300, 72, 64), (64, 40, 520)] * 30)]
+    items.append(dict(items[3], G=torch.empty_like(items[3]["G"])))
+    _run_and_check(items)
+    assert torch.equal(items[3]["G"], items[-1]["G"])
+
+
+def test_grad_equal_inputs_give_equal_bits():
+    it, _ = _case(5000, 200, 264, torch.bfloat16, torch.float32, seed=8)
+    _run_and_check([it])
+    first = it["G"].clone()
+    for _ in range(5):
+        mo.act8_grad_batched([it], _ws([it]))
+        assert torch.equal(it["G"], first)
+
+
+def test_grad_long_sum():
+    it, _ = _case(20001, 96, 64, torch.bfloat16, torch.float32, seed=9)
+    _run_and_check([it])
+
+
+def test_grad_extreme_exponents():
+    # blocks at the ends of the exponent range times a dY that brings the sum back into range
+    for s, d in ((2.0 ** 118, 2.0 ** -100), (2.0 ** -116, 2.0 ** 100)):
+        x = torch.randn(40, 64, generator=torch.Generator().manual_seed(2)).cuda() * s
+        c = _ckpt_of(x)
+        dY = (torch.randn(40, 48, generator=torch.Generator().manual_seed(3)) * d).to(torch.bfloat16).cuda()
+        it = dict(dY=dY, G=torch.empty(48, 64, device="cuda"), beta=0.0, **c)
+        _run_and_check([it])
+
+
+def test_grad_fp16_small_and_subnormal_values():
+    # values below fp16's normal range are rounded to its subnormals, as the oracle's are
+    x = torch.randn(33, 64, generator=torch.Generator().manual_seed(2)).cuda() * torch.exp2(
+        torch.arange(33, device="cuda") - 34.0)[:, None]
+    it = dict(dY=torch.ones(33, 8, dtype=torch.float16, device="cuda"), G=torch.empty(8, 64, device="cuda"), beta=0.0,
+              **_ckpt_of(x))
+    it["dY"] *= torch.linspace(1, 8, 33, device="cuda").half()[:, None]
+    _run_and_check([it])
+
+
+def test_grad_nan_blocks_reach_only_their_columns():
+    x = torch.randn(50, 96, generator=torch.Generator().manual_seed(2)).cuda()
+    x[17, 40] = float("inf")
+    for dt in DTS:
+        it = dict(dY=torch.randn(50, 70, generator=torch.Generator().manual_seed(3)).to(dt).cuda(),
+                  G=torch.empty(70, 96, device="cuda"), **_ckpt_of(x))
+        mo.act8_grad_batched([it], _ws([it]))
+        nan = torch.isnan(it["G"])
+        assert bool(nan[:, 32:64].all()) and not bool(nan[:, :32].any()) and not bool(nan[:, 64:].any())
+
+
+def test_grad_infinite_dY_reaches_only_its_rows():
+    it, _ = _case(50, 70, 96, torch.bfloat16, torch.float32, seed=10)
+    it["dY"][3, 5] = float("nan")
+    mo.act8_grad_batched([it], _ws([it]))
+    nan = torch.isnan(it["G"])
+    assert bool(nan[5].all()) and int(nan.sum()) == 96
+
+
+def test_grad_workspace_is_required():
+    it, _ = _case(20000, 64, 64, torch.bfloat16, torch.float32, seed=9, pad=1)
+    need = mo.act8_grad_workspace_size([it])
+    if need:
+        for ws in (None, torch.empty(need - 1, dtype=torch.uint8, device="cuda"),
+                   torch.empty(need + 256, dtype=torch.uint8, device="cuda")[1:]):
+            with pytest.raises(mo.MuonError) as err:
+                mo.act8_grad_batched([it], ws)
+            assert err.value.status == mo.ERR_WORKSPACE
+
+
+def test_other_stream_and_captured_graph():
+    # encode and gradient captured once and replayed on new inputs, on a stream of its own
+    x = _x(700, 264, torch.bfloat16, seed=1, spread=0.3)
+    it, _ = _case(700, 200, 264, torch.bfloat16, torch.float32, seed=11)
+    ws = _ws([it])
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        mo.act8_encode_batched([dict(x=x, q=it["q"], e=it["e"])])
+        mo.act8_grad_batched([it], ws)
+    s.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=s):
+        mo.act8_encode_batched([dict(x=x, q=it["q"], e=it["e"])])
+        mo.act8_grad_batched([it], ws)
+    for seed in (20, 21):
+        x.copy_(_x(700, 264, torch.bfloat16, seed=seed, spread=0.3))
+        it["dY"].mul_(-0.5)
+        g.replay()
+        torch.cuda.synchronize()
+        q_ref, e_ref = acts.encode(_np(x))
+        assert np.array_equal(it["q"].cpu().numpy(), q_ref)
+        _check_G(it["G"], it["dY"], acts.decode(q_ref, e_ref))
