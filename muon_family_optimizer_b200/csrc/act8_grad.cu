@@ -1,63 +1,497 @@
 // act8_grad.cu -- weight gradients of linear layers from 8-bit activation
 // checkpoints: G = beta G + (dY^T X^) diag(gain) + dy_sum shift^T.
 //
-// First form: CUDA cores, fp32, one 64 x 64 tile of G per block, 16 tokens at a
-// time through shared memory.
+// The sum runs over tokens, the rows of both operands, so both are read
+// MN-major: A = dY^T (M = out) and B = X^ (N = cols), K = tokens.  X^ = q 2^e is
+// exact in bfloat16, so the tensor cores take it as a 16-bit operand
+// (kind::f16, fp32 accumulation), and the kernel turns codes into that operand on
+// the way into shared memory: the codes are what crosses HBM and L2.
+//
+// One persistent CTA pair per two SMs (cta_group::2, 256 x 256 tiles of G), a
+// work list of (tile, range of tokens) over all layers of the call:
+//   warp 0      TMA producer: this CTA's 128 columns of dY, 128-byte-swizzled
+//               boxes of 64 x 64 tokens (no multicast);
+//   warp 1      allocates tensor memory; one thread of the leader CTA issues the MMAs;
+//   warps 2-9   epilogue: tcgen05.ld, gain, shift, beta, store (or the fp32 part of a
+//               range of tokens), overlapped with the next tile through two
+//               accumulator buffers;
+//   warps 10-17 converters: 16 codes and their exponent byte per load, kept
+//               kAhead k-blocks ahead in registers, to two 16-byte pieces of the
+//               swizzled operand.
+// A stage is full when both CTAs' boxes have landed and the converters of
+// both have arrived on the leader's barrier.
+//
+// Layers with few tiles split the tokens (plan_batch): the ranges write fp32
+// parts to the workspace and a second kernel adds them in order.
 #include <algorithm>
 #include <cmath>
+#include <cstring>
+#include <mutex>
 
 #include "act8.cuh"
 #include "gemm.h"
 
 namespace muon {
-
 namespace {
 
-constexpr int kT = 64, kKT = 16;
+constexpr int kItems = 48;              // layers per launch
+constexpr int kBM = 128, kBN = 256;     // rows of a CTA, columns of a pair's tile
+constexpr int kBK = 64;                 // tokens per stage
+constexpr int kStages = 6;
+constexpr int kABytes = kBM * kBK * 2, kBBytes = kBN / 2 * kBK * 2;
+constexpr int kStageBytes = kABytes + kBBytes;
+constexpr int kEpiWarps = 8, kConvWarps = 8;
+constexpr int kThreads = 64 + 32 * (kEpiWarps + kConvWarps);
+constexpr int kAhead = 4;               // k-blocks of codes in a converter's registers
+constexpr int kGroup = 8;               // tile rows walked together
+constexpr int kSmem = 1024 + kStages * kStageBytes + 256;
+constexpr int kPlanSms = 148;           // work lists are planned for a whole B200, so a size query needs no device
 
-__global__ void __launch_bounds__(256) act8_grad_simple(muon_act8_grad_item I, int dy_dt, int w_dt) {
-    __shared__ float sd[kKT][kT + 4], sx[kKT][kT + 4];
-    const int o0 = blockIdx.y * kT, i0 = blockIdx.x * kT;
-    const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-    float acc[4][4] = {};
-    for (int t0 = 0; t0 < I.c.rows; t0 += kKT) {
-        for (int k = threadIdx.x; k < kKT * kT; k += 256) {
-            const int r = k / kT, c = k % kT;
-            const long long t = t0 + r;
-            const bool in = t < I.c.rows;
-            sd[r][c] = in && o0 + c < I.out ? ld_elem(I.dY, t * I.lddy + o0 + c, dy_dt) : 0.f;
-            float x = 0.f;
-            if (in && i0 + c < I.c.cols) {
-                const int b = I.c.e[t * I.c.lde + (i0 + c) / kActBlock];
-                x = (float)I.c.q[t * I.c.ldq + i0 + c] * (b == kActBad ? __uint_as_float(0x7FC00000u) : act8_scale(b));
-                if (dy_dt == DT_FP16) x = __half2float(__float2half_rn(x));
-            }
-            sx[r][c] = x;
-        }
-        __syncthreads();
-#pragma unroll
-        for (int k = 0; k < kKT; ++k)
-#pragma unroll
-            for (int a = 0; a < 4; ++a)
-#pragma unroll
-                for (int b = 0; b < 4; ++b) acc[a][b] = fmaf(sd[k][ty * 4 + a], sx[k][tx * 4 + b], acc[a][b]);
-        __syncthreads();
-    }
-#pragma unroll
-    for (int a = 0; a < 4; ++a)
-#pragma unroll
-        for (int b = 0; b < 4; ++b) {
-            const int o = o0 + ty * 4 + a, c = i0 + tx * 4 + b;
-            if (o >= I.out || c >= I.c.cols) continue;
-            const long long at = (long long)o * I.c.cols + c;
-            float g = acc[a][b];
-            if (I.gain) g *= ld_elem(I.gain, c, w_dt);
-            if (I.shift) g = fmaf(I.dy_sum[o], ld_elem(I.shift, c, w_dt), g);
-            if (I.beta != 0.f) g = fmaf(I.beta, ld_elem(I.G, at, w_dt), g);
-            st_elem(I.G, at, w_dt, g);
-        }
+struct GradItem {
+    CUtensorMap map;                    // dY: boxes of 64 columns x 64 tokens, parts as the third dimension
+    const signed char* q;
+    const unsigned char* e;
+    long long ldq, lde;
+    int rows, cols, out;
+    int nkb;                            // k-blocks of one part
+    int splits, len;                    // ranges of tokens, k-blocks (over all parts) of one range
+    int total;                          // nkb * parts
+    int tiles_m, tiles_n;
+    long long begin;                    // first entry of the work list
+    void* G;
+    const void *gain, *shift;
+    const float* dy_sum;
+    float beta;
+    int vec;                            // G (and gain) rows may be accessed in 16-byte pieces
+    float* part;                        // splits != 1: [splits][out][ldp] fp32
+    long long ldp;
+};
+
+struct GradParams {
+    GradItem it[kItems];
+    int n, w_dt;
+    long long works;
+    int* d_status;
+};
+
+struct Work {
+    int item, split, ti, tj;
+};
+
+__device__ __forceinline__ Work decode_work(const GradParams& p, long long w) {
+    Work k;
+    k.item = 0;
+    while (k.item + 1 < p.n && w >= p.it[k.item + 1].begin) ++k.item;
+    const GradItem& I = p.it[k.item];
+    const int tiles = I.tiles_m * I.tiles_n;
+    const long long local = w - I.begin;
+    k.split = (int)(local / tiles);
+    const int r = (int)(local - (long long)k.split * tiles);
+    const int g = r / (kGroup * I.tiles_n);                 // tile rows in groups: concurrent tiles form a block
+    const int gm = min(kGroup, I.tiles_m - g * kGroup);
+    const int in = r - g * kGroup * I.tiles_n;
+    k.ti = g * kGroup + in % gm;
+    k.tj = in / gm;
+    return k;
 }
 
+// Two codes of `h` (each byte doubled into a 16-bit half) as bfloat16 values.
+// 0x4300 | (b & 127) is 128 + the low seven bits; q = that - 128, or - 256 for a
+// negative code, whose sign bit 7 raises the subtrahend's exponent by one.
+// (128 + low) 2^e - 128 2^e in one fused operation is exact.
+__device__ __forceinline__ uint32_t codes_bf16(uint32_t h, uint32_t scale2, uint32_t sub2) {
+    const uint32_t v = (h & 0x007F007Fu) | 0x43004300u;
+    const uint32_t c = (h & 0x00800080u) + sub2;
+    const __nv_bfloat162 r = __hfma2(*reinterpret_cast<const __nv_bfloat162*>(&v),
+                                     *reinterpret_cast<const __nv_bfloat162*>(&scale2),
+                                     *reinterpret_cast<const __nv_bfloat162*>(&c));
+    return *reinterpret_cast<const uint32_t*>(&r);
+}
+
+// Sixteen codes under one exponent byte to sixteen 16-bit values, lower columns first.
+template <typename T>
+__device__ __forceinline__ void convert16(const uint4& q, int byte, uint4& lo, uint4& hi) {
+    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+    uint32_t o[8];
+    if constexpr (IsBf16<T>::value) {
+        // 2^e has the byte as its exponent field; a bad block's NaN goes through the product
+        const uint32_t scale2 = byte == kActBad ? 0x7FC07FC0u : (uint32_t)byte * 0x00800080u;
+        const uint32_t sub2 = 0x80008000u + (uint32_t)(byte == kActBad ? 0 : byte + 7) * 0x00800080u;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            o[2 * i] = codes_bf16(__byte_perm(w[i], 0, 0x1100), scale2, sub2);
+            o[2 * i + 1] = codes_bf16(__byte_perm(w[i], 0, 0x3322), scale2, sub2);
+        }
+    } else {
+        // fp16's range ends at 2^-24 and 2^16: through fp32, one rounding at the end
+        const float s = byte == kActBad ? __uint_as_float(0x7FC00000u) : act8_scale(byte);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float a = (float)(signed char)(w[i]) * s, b = (float)(signed char)(w[i] >> 8) * s;
+            const float c = (float)(signed char)(w[i] >> 16) * s, d = (float)(signed char)(w[i] >> 24) * s;
+            o[2 * i] = pack2<__half>(a, b);
+            o[2 * i + 1] = pack2<__half>(c, d);
+        }
+    }
+    lo = make_uint4(o[0], o[1], o[2], o[3]);
+    hi = make_uint4(o[4], o[5], o[6], o[7]);
+}
+
+__device__ __forceinline__ uint4 ld_codes(const signed char* p) {
+    uint4 v;
+    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+    return v;
+}
+
+// gain, shift and beta on 32 columns of one row, and the store.  gn, sh: this lane's
+// column's gain and shift (lane = column - c0).
+__device__ __forceinline__ void finish32(const GradItem& I, int w_dt, int row, int c0, float gn, float sh, float (&v)[32]) {
+    const bool in = row < I.out;
+    if (I.gain)
+#pragma unroll
+        for (int i = 0; i < 32; ++i) v[i] *= __shfl_sync(0xFFFFFFFFu, gn, i);
+    if (I.shift) {
+        const float d = in ? I.dy_sum[row] : 0.f;
+#pragma unroll
+        for (int i = 0; i < 32; ++i) v[i] = fmaf(d, __shfl_sync(0xFFFFFFFFu, sh, i), v[i]);
+    }
+    if (!in) return;
+    const long long at = (long long)row * I.cols + c0;
+    const int n = min(32, I.cols - c0);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const bool vec = I.vec && 8 * i + 8 <= n;
+        const int nv = max(0, min(8, n - 8 * i));
+        float x[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) x[j] = v[8 * i + j];
+        if (I.beta != 0.f) {
+            float g[8];
+            load8_dt(I.G, at + 8 * i, w_dt, vec, nv, g);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) x[j] = fmaf(I.beta, g[j], x[j]);
+        }
+        store8_dt(I.G, at + 8 * i, w_dt, vec, nv, x);
+    }
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kThreads, 1) act8_grad_kernel(const __grid_constant__ GradParams p) {
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint64_t* full_bar = reinterpret_cast<uint64_t*>(smem + kStages * kStageBytes);
+    uint64_t* empty_bar = full_bar + kStages;
+    uint64_t* tfull_bar = empty_bar + kStages;
+    uint64_t* tempty_bar = tfull_bar + 2;
+    uint64_t* drain_bar = tempty_bar + 2;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain_bar + 1);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = cluster_ctarank();
+    const long long unit = blockIdx.x >> 1, nunits = gridDim.x >> 1;
+    int* d_status = p.d_status;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < kStages; ++s) {
+            mbar_init(&full_bar[s], 1 + 2 * kConvWarps);    // the armed byte count, both CTAs' converter warps
+            mbar_init(&empty_bar[s], 1);
+        }
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(&tfull_bar[b], 1);
+            mbar_init(&tempty_bar[b], 2 * kEpiWarps);
+        }
+        mbar_init(drain_bar, 1);
+        *abort_flag = 0;
+        fence_mbar_init();
+    }
+    if (warp == 1) {
+        tmem_alloc_pair(tmem_slot, 512);
+        tmem_relinquish_pair();
+    }
+    tc_fence_before();
+    __syncwarp();
+    cluster_sync();
+    tc_fence_after();
+    const uint32_t tmem_base = *tmem_slot;
+
+    if (warp == 0) {
+        if (lane == 0) {
+            // ------------------------------------------------ TMA producer
+            int stage = 0;
+            uint32_t phase = 0;
+            for (long long w = unit; w < p.works && !*abort_flag; w += nunits) {
+                const Work k = decode_work(p, w);
+                const GradItem& I = p.it[k.item];
+                const int col = k.ti * 2 * kBM + (int)rank * kBM;
+                const int kb1 = min(I.total, (k.split + 1) * I.len);
+                for (int kb = k.split * I.len; kb < kb1; ++kb) {
+                    if (!mbar_wait(&empty_bar[stage], phase ^ 1, abort_flag, d_status)) break;
+                    uint8_t* sa = smem + stage * kStageBytes;
+                    if (rank == 0) mbar_arrive_expect_tx(&full_bar[stage], 2 * kABytes);
+                    const uint32_t fb = mapa_shared(smem_u32(&full_bar[stage]), 0);
+                    const int part = kb / I.nkb, tok = (kb - part * I.nkb) * kBK;
+                    tma_load_3d_pair(&I.map, fb, sa, col, tok, part);
+                    tma_load_3d_pair(&I.map, fb, sa + 64 * kBK * 2, col + 64, tok, part);
+                    if (++stage == kStages) { stage = 0; phase ^= 1; }
+                }
+            }
+            if (*abort_flag) {      // give the copies in flight time to land before the CTA exits
+                const unsigned long long t0 = global_ns();
+                while (global_ns() - t0 < 200000ull) {
+                }
+            }
+        }
+    } else if (warp == 1) {
+        if (lane == 0 && rank == 0) {
+            // ------------------------------------------------ MMA issuer
+            constexpr uint32_t idesc = make_idesc_f16(IsBf16<T>::value ? 1 : 0, 1, 2 * kBM, kBN) | 1u << 15;
+            int stage = 0, it = 0;
+            uint32_t phase = 0;
+            bool ok = true;
+            for (long long w = unit; ok && w < p.works; w += nunits, ++it) {
+                const Work k = decode_work(p, w);
+                const GradItem& I = p.it[k.item];
+                const int buf = it & 1;
+                if (!mbar_wait(&tempty_bar[buf], ((it >> 1) & 1) ^ 1, abort_flag, d_status)) break;
+                tc_fence_after();
+                const uint32_t d_tmem = tmem_base + (uint32_t)(buf * kBN);
+                const int kb0 = k.split * I.len, kb1 = min(I.total, kb0 + I.len);
+                for (int kb = kb0; kb < kb1; ++kb) {
+                    if (!mbar_wait(&full_bar[stage], phase, abort_flag, d_status)) { ok = false; break; }
+                    tc_fence_after();
+                    const uint32_t sa = smem_u32(smem + stage * kStageBytes), sb = sa + kABytes;
+#pragma unroll
+                    for (int s = 0; s < kBK / 16; ++s)      // 16 tokens: 16 rows of 128 bytes in each 64-wide box
+                        tc_mma_f16_pair(d_tmem, smem_desc_sw128(sa + s * 2048, 64 * kBK * 2, 1024),
+                                        smem_desc_sw128(sb + s * 2048, 64 * kBK * 2, 1024), idesc,
+                                        kb > kb0 || s > 0 ? 1u : 0u);
+                    tc_commit_pair(smem_u32(&empty_bar[stage]));
+                    tc_commit_pair(mapa_shared(smem_u32(&empty_bar[stage]), 1));
+                    if (++stage == kStages) { stage = 0; phase ^= 1; }
+                }
+                if (!ok) break;
+                tc_commit_pair(smem_u32(&tfull_bar[buf]));
+                tc_commit_pair(mapa_shared(smem_u32(&tfull_bar[buf]), 1));
+            }
+            // no MMA may still be writing tensor memory when it is freed
+            tc_commit_pair(smem_u32(drain_bar));
+            const unsigned long long t0 = global_ns();
+            while (!mbar_try_wait(drain_bar, 0) && global_ns() - t0 < kWaitLimitNs) {
+            }
+        }
+    } else if (warp < 2 + kEpiWarps) {
+        // ---------------------------------------------------- epilogue
+        const int quad = warp & 3, half = (warp - 2) >> 2;
+        int it = 0;
+        for (long long w = unit; w < p.works; w += nunits, ++it) {
+            const Work k = decode_work(p, w);
+            const GradItem& I = p.it[k.item];
+            const int buf = it & 1;
+            if (!mbar_wait(&tfull_bar[buf], (it >> 1) & 1, abort_flag, d_status)) break;
+            tc_fence_after();
+            const int row0 = k.ti * 2 * kBM + (int)rank * kBM + quad * 32, row = row0 + lane;
+#pragma unroll 1
+            for (int c = 0; c < kBN / 64; ++c) {
+                const int lc = half * (kBN / 2) + c * 32, c0 = k.tj * kBN + lc;
+                if (c0 >= I.cols || row0 >= I.out) break;            // uniform over the warp
+                float gn = 1.f, sh = 0.f;
+                if (I.splits == 1 && c0 + lane < I.cols) {
+                    if (I.gain) gn = ld_elem(I.gain, c0 + lane, p.w_dt);
+                    if (I.shift) sh = ld_elem(I.shift, c0 + lane, p.w_dt);
+                }
+                float v[32];
+                tmem_ld_32x32b_x32(tmem_base + ((uint32_t)(quad * 32) << 16) + (uint32_t)(buf * kBN + lc), v);
+                if (I.splits == 1) {
+                    finish32(I, p.w_dt, row, c0, gn, sh, v);
+                } else if (row < I.out) {
+                    float* dst = I.part + ((long long)k.split * I.out + row) * I.ldp + c0;
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        if (c0 + 4 * i < I.ldp)
+                            reinterpret_cast<float4*>(dst)[i] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+                }
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(&tempty_bar[buf]), 0));
+        }
+    } else {
+        // ---------------------------------------------------- converters
+        const int tid = (int)threadIdx.x - 64 - 32 * kEpiWarps;
+        const int piece = tid & 7, tok0 = tid >> 3;         // 16 columns, tokens tok0 and tok0 + 32 of a k-block
+        // the two 16-byte pieces of 16 columns in a 64-column box: row = token, pieces XORed with the token's low bits
+        const int box = (piece >> 2) * (64 * kBK * 2), pc = (piece & 3) * 2;
+        int stage = 0;
+        uint32_t phase = 0;
+        bool ok = true;
+        for (long long w = unit; ok && w < p.works; w += nunits) {
+            const Work k = decode_work(p, w);
+            const GradItem& I = p.it[k.item];
+            const int col = k.tj * kBN + (int)rank * (kBN / 2) + piece * 16;
+            const bool in = col < I.cols;
+            const signed char* qc = I.q + col;
+            const unsigned char* ec = I.e + col / kActBlock;
+            const int kb0 = k.split * I.len, kb1 = min(I.total, kb0 + I.len);
+            uint4 q[kAhead][2];
+            int e[kAhead][2];
+            auto fetch = [&](int kb, uint4 (&qq)[2], int (&ee)[2]) {
+                const int tb = (kb % I.nkb) * kBK + tok0;
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const long long t = tb + 32 * h;
+                    qq[h] = make_uint4(0u, 0u, 0u, 0u);
+                    ee[h] = 127;
+                    if (in && kb < kb1 && t < I.rows) {
+                        qq[h] = ld_codes(qc + t * I.ldq);
+                        ee[h] = __ldg(ec + t * I.lde);
+                    }
+                }
+            };
+#pragma unroll
+            for (int d = 0; d < kAhead; ++d) fetch(kb0 + d, q[d], e[d]);
+            for (int kb = kb0; ok && kb < kb1; kb += kAhead) {
+#pragma unroll
+                for (int d = 0; d < kAhead; ++d) {
+                    if (!ok || kb + d >= kb1) break;
+                    uint4 lo[2], hi[2];
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) convert16<T>(q[d][h], e[d][h], lo[h], hi[h]);
+                    fetch(kb + d + kAhead, q[d], e[d]);
+                    if (!mbar_wait(&empty_bar[stage], phase ^ 1, abort_flag, d_status)) { ok = false; break; }
+                    uint8_t* sb = smem + stage * kStageBytes + kABytes + box;
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const int t = tok0 + 32 * h;
+                        *reinterpret_cast<uint4*>(sb + t * 128 + ((pc ^ (t & 7)) << 4)) = lo[h];
+                        *reinterpret_cast<uint4*>(sb + t * 128 + (((pc + 1) ^ (t & 7)) << 4)) = hi[h];
+                    }
+                    fence_proxy_async_smem();       // the tensor cores read what was stored here
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(&full_bar[stage]), 0));
+                    if (++stage == kStages) { stage = 0; phase ^= 1; }
+                }
+            }
+        }
+    }
+
+    tc_fence_before();
+    __syncwarp();
+    cluster_sync();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc_pair(tmem_base, 512);
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Copies of dY the tensor maps can read: rows that are not 16-byte aligned, and
+// fp32 rows as three bfloat16 parts hi + mid + lo (8 significant bits each,
+// so the three hold all 24; a part of a non-finite value keeps it in hi).
+// ---------------------------------------------------------------------------
+struct CopyItem {
+    const void* src;
+    unsigned short* dst;
+    long long ld, lddst, part_stride, begin;
+    int rows, out, segs;
+};
+
+struct CopyParams {
+    CopyItem it[kItems];
+    int n;
+    long long units;
+};
+
+template <int DT>
+__global__ void __launch_bounds__(256) act8_copy_kernel(const __grid_constant__ CopyParams p) {
+    const int lane = threadIdx.x & 31;
+    const long long nwarps = (long long)gridDim.x * 8;
+    int ci = 0;
+    for (long long u = (long long)blockIdx.x * 8 + (threadIdx.x >> 5); u < p.units; u += nwarps) {
+        while (ci + 1 < p.n && u >= p.it[ci + 1].begin) ++ci;
+        const CopyItem& I = p.it[ci];
+        const long long local = u - I.begin, row = local / I.segs;
+        const int col = (int)(local - row * I.segs) * 256 + lane * 8;
+        const int nv = max(0, min(8, I.out - col));
+        if (nv == 0) continue;
+        unsigned short* dst = I.dst + row * I.lddst + col;
+        if constexpr (DT == DT_FP32) {
+            const float* src = static_cast<const float*>(I.src) + row * I.ld + col;
+            uint32_t o[3][4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                float a = 2 * i < nv ? src[2 * i] : 0.f, b = 2 * i + 1 < nv ? src[2 * i + 1] : 0.f;
+#pragma unroll
+                for (int k = 0; k < 3; ++k) {
+                    o[k][i] = pack2<__nv_bfloat16>(a, b);
+                    const float ra = a - unpack_lo<__nv_bfloat16>(o[k][i]), rb = b - unpack_hi<__nv_bfloat16>(o[k][i]);
+                    a = fabsf(a) <= 3.0e38f ? ra : 0.f;
+                    b = fabsf(b) <= 3.0e38f ? rb : 0.f;
+                }
+            }
+#pragma unroll
+            for (int k = 0; k < 3; ++k)
+                *reinterpret_cast<uint4*>(dst + k * I.part_stride) = make_uint4(o[k][0], o[k][1], o[k][2], o[k][3]);
+        } else {
+            const unsigned short* src = static_cast<const unsigned short*>(I.src) + row * I.ld + col;
+            uint32_t o[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const uint32_t a = 2 * i < nv ? src[2 * i] : 0u, b = 2 * i + 1 < nv ? src[2 * i + 1] : 0u;
+                o[i] = a | b << 16;
+            }
+            *reinterpret_cast<uint4*>(dst) = make_uint4(o[0], o[1], o[2], o[3]);
+        }
+    }
+}
+
+// G from the parts of the token ranges (none: no tokens), added in order.
+__global__ void __launch_bounds__(256) act8_join_kernel(const __grid_constant__ GradParams p) {
+    for (int i = 0; i < p.n; ++i) {
+        const GradItem& I = p.it[i];
+        if (I.splits == 1) continue;
+        const int segs = (I.cols + 7) / 8;
+        const long long units = (long long)I.out * segs;
+        for (long long u = (long long)blockIdx.x * blockDim.x + threadIdx.x; u < units;
+             u += (long long)gridDim.x * blockDim.x) {
+            const long long row = u / segs;
+            const int col = (int)(u - row * segs) * 8;
+            const int nv = min(8, I.cols - col);
+            const bool vec = I.vec && nv == 8;
+            float s[8] = {};
+            const float* src = I.part + row * I.ldp + col;
+            const long long step = (long long)I.out * I.ldp;
+#pragma unroll 4
+            for (int k = 0; k < I.splits; ++k) {
+                const float4 a = *reinterpret_cast<const float4*>(src + k * step);
+                const float4 b = *reinterpret_cast<const float4*>(src + k * step + 4);
+                s[0] += a.x; s[1] += a.y; s[2] += a.z; s[3] += a.w;
+                s[4] += b.x; s[5] += b.y; s[6] += b.z; s[7] += b.w;
+            }
+            float g[8];
+            if (I.gain) {
+                load8_dt(I.gain, col, p.w_dt, vec, nv, g);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) s[j] *= g[j];
+            }
+            if (I.shift) {
+                const float d = I.dy_sum[row];
+#pragma unroll
+                for (int j = 0; j < 8; ++j) s[j] = fmaf(d, j < nv ? ld_elem(I.shift, col + j, p.w_dt) : 0.f, s[j]);
+            }
+            if (I.beta != 0.f) {
+                load8_dt(I.G, row * I.cols + col, p.w_dt, vec, nv, g);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) s[j] = fmaf(I.beta, g[j], s[j]);
+            }
+            store8_dt(I.G, row * I.cols + col, p.w_dt, vec, nv, s);
+        }
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Host
+// ---------------------------------------------------------------------------
 bool valid(int dt) { return dt == DT_BF16 || dt == DT_FP16 || dt == DT_FP32; }
 
 muon_status check_items(const muon_act8_grad_item* items, int n) {
@@ -71,6 +505,181 @@ muon_status check_items(const muon_act8_grad_item* items, int n) {
     return MUON_OK;
 }
 
+long long align256(long long x) { return (x + 255) / 256 * 256; }
+
+// Whether the tensor map can read dY where it is.
+bool direct(const muon_act8_grad_item& q, int dt) {
+    return dt != DT_FP32 && rows_aligned(q.dY, q.lddy, 2) && q.lddy < (1LL << 38);
+}
+
+struct Plan {
+    int splits[kItems], len[kItems];
+    long long copy_at[kItems], part_at[kItems];   // workspace offsets (-1: none)
+    long long bytes;
+};
+
+// Ranges of tokens.  Without splits every work item is a whole sum of nkb
+// k-blocks and the pairs run ceil(tiles / pairs) rounds of them; with ranges of
+// `len` k-blocks the rounds are shorter and fuller, for fp32 parts that are written
+// and read again.  The estimate in k-blocks' time (about 0.3 us: 256 x 256 x 64
+// multiply-adds on a pair) is compared for ranges of 1/1, 1/2, ... of the longest sum.
+void plan_batch(const muon_act8_grad_item* items, int n, int dt, Plan& P) {
+    const int parts = dt == DT_FP32 ? 3 : 1;
+    const double pairs = kPlanSms / 2, kb_us = 0.3, gbs = 4e6 /* bytes per us: parts through L2 and HBM */, fixed_us = 4.0;
+    int total[kItems];
+    long long tiles[kItems];
+    int longest = 0;
+    for (int i = 0; i < n; ++i) {
+        total[i] = (items[i].c.rows + kBK - 1) / kBK * parts;
+        tiles[i] = (long long)((items[i].out + 2 * kBM - 1) / (2 * kBM)) * ((items[i].c.cols + kBN - 1) / kBN);
+        longest = std::max(longest, total[i]);
+    }
+    int best_len = std::max(1, longest);
+    double best = -1.0;
+    for (int s = 1; s <= 74 && s <= longest; ++s) {
+        const int len = (longest + s - 1) / s;
+        double works = 0.0, bytes = 0.0;
+        for (int i = 0; i < n; ++i) {
+            const int k = (total[i] + len - 1) / len;
+            works += (double)tiles[i] * k;
+            if (k > 1) bytes += 8.0 * k * items[i].out * items[i].c.cols;
+        }
+        const double us = std::ceil(works / pairs) * len * kb_us + (bytes > 0 ? bytes / gbs + fixed_us : 0.0);
+        if (best < 0.0 || us < best) {
+            best = us;
+            best_len = len;
+        }
+    }
+    P.bytes = 0;
+    for (int i = 0; i < n; ++i) {
+        P.len[i] = best_len;
+        P.splits[i] = (total[i] + best_len - 1) / best_len;
+        P.copy_at[i] = P.part_at[i] = -1;
+        if (items[i].c.rows > 0 && !direct(items[i], dt)) {
+            P.copy_at[i] = P.bytes;
+            P.bytes += align256(2LL * parts * items[i].c.rows * ((items[i].out + 7) / 8 * 8));
+        }
+        if (P.splits[i] > 1) {
+            P.part_at[i] = P.bytes;
+            P.bytes += align256(4LL * P.splits[i] * items[i].out * ((items[i].c.cols + 7) / 8 * 8));
+        }
+    }
+}
+
+template <typename T>
+cudaError_t launch_grad(const GradParams& prm, cudaStream_t stream) {
+    auto kern = act8_grad_kernel<T>;
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+    if (e != cudaSuccess) return e;
+    int dev = 0, nsm = kPlanSms;
+    cudaGetDevice(&dev);
+    cudaDeviceGetAttribute(&nsm, cudaDevAttrMultiProcessorCount, dev);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(2 * std::min<long long>(prm.works, nsm / 2)));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = kSmem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 2;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    e = cudaLaunchKernelEx(&cfg, kern, prm);
+    return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+muon_status run_batch(const muon_act8_grad_item* items, int n, int dt, int w_dt, uint8_t* ws, int* d_status,
+                      cudaStream_t stream) {
+    static GradParams prm;             // large: kept off the stack, filled and consumed per launch
+    static CopyParams cp;
+    static std::mutex mu;
+    std::lock_guard<std::mutex> lock(mu);
+    Plan P;
+    plan_batch(items, n, dt, P);
+    memset(&prm, 0, sizeof(prm));
+    memset(&cp, 0, sizeof(cp));
+    const int parts = dt == DT_FP32 ? 3 : 1;
+    double flops = 0.0, copy_bytes = 0.0, join_bytes = 0.0;
+    bool join = false;
+    for (int i = 0; i < n; ++i) {
+        const muon_act8_grad_item& q = items[i];
+        GradItem& I = prm.it[i];
+        I.q = q.c.q; I.e = q.c.e; I.ldq = q.c.ldq; I.lde = q.c.lde;
+        I.rows = q.c.rows; I.cols = q.c.cols; I.out = q.out;
+        I.nkb = (q.c.rows + kBK - 1) / kBK;
+        I.total = I.nkb * parts;
+        I.splits = P.splits[i];
+        I.len = P.len[i];
+        I.tiles_m = (q.out + 2 * kBM - 1) / (2 * kBM);
+        I.tiles_n = (q.c.cols + kBN - 1) / kBN;
+        I.begin = prm.works;
+        prm.works += (long long)I.tiles_m * I.tiles_n * I.splits;
+        I.G = q.G; I.gain = q.gain; I.shift = q.shift; I.dy_sum = q.dy_sum; I.beta = q.beta;
+        I.vec = rows_aligned(q.G, q.c.cols, dt_size(w_dt)) && (reinterpret_cast<uintptr_t>(q.gain) & 15) == 0;
+        I.ldp = (q.c.cols + 7) / 8 * 8;
+        I.part = P.part_at[i] < 0 ? nullptr : reinterpret_cast<float*>(ws + P.part_at[i]);
+        join |= I.splits != 1;
+        if (I.splits != 1) join_bytes += (double)q.out * q.c.cols * (4.0 * I.splits + dt_size(w_dt));
+        if (q.c.rows == 0) continue;
+        flops += 2.0 * q.c.rows * q.out * q.c.cols;
+        const void* base = q.dY;
+        long long ld = q.lddy, stride = q.lddy * q.c.rows;
+        if (P.copy_at[i] >= 0) {
+            base = ws + P.copy_at[i];
+            ld = (q.out + 7) / 8 * 8;
+            stride = ld * q.c.rows;
+            CopyItem& c = cp.it[cp.n++];
+            c.src = q.dY; c.dst = reinterpret_cast<unsigned short*>(ws + P.copy_at[i]);
+            c.ld = q.lddy; c.lddst = ld; c.part_stride = stride; c.begin = cp.units;
+            c.rows = q.c.rows; c.out = q.out; c.segs = (q.out + 255) / 256;
+            cp.units += (long long)c.rows * c.segs;
+            copy_bytes += (double)q.c.rows * q.out * (dt_size(dt) + 2.0 * parts);
+        }
+        if (!tc::encode_map(&I.map, dt == DT_FP16 ? DT_FP16 : DT_BF16, base, q.out, q.c.rows, parts, ld,
+                            parts == 1 ? ld : stride, 64, kBK))
+            return MUON_ERR_CUDA;
+    }
+    prm.n = n;
+    prm.w_dt = w_dt;
+    prm.d_status = d_status;
+    int dev = 0, nsm = kPlanSms;
+    cudaGetDevice(&dev);
+    cudaDeviceGetAttribute(&nsm, cudaDevAttrMultiProcessorCount, dev);
+    if (cp.n > 0) {
+        const int grid = (int)std::min<long long>((cp.units + 7) / 8, (long long)nsm * 8);
+        trace_begin(MUON_KERNEL_ACT8, copy_bytes, stream);
+        if (dt == DT_FP32) act8_copy_kernel<DT_FP32><<<grid, 256, 0, stream>>>(cp);
+        else act8_copy_kernel<DT_BF16><<<grid, 256, 0, stream>>>(cp);
+        trace_end(stream);
+        if (cudaGetLastError() != cudaSuccess) return MUON_ERR_CUDA;
+    }
+    if (prm.works > 0) {
+        trace_begin(MUON_KERNEL_ACT8_GRAD, flops, stream);
+        const cudaError_t e = dt == DT_FP16 ? launch_grad<__half>(prm, stream) : launch_grad<__nv_bfloat16>(prm, stream);
+        trace_end(stream);
+        if (e != cudaSuccess) return MUON_ERR_CUDA;
+    }
+    if (join) {
+        trace_begin(MUON_KERNEL_ACT8, join_bytes, stream);
+        act8_join_kernel<<<nsm * 4, 256, 0, stream>>>(prm);
+        trace_end(stream);
+        if (cudaGetLastError() != cudaSuccess) return MUON_ERR_CUDA;
+    }
+    return MUON_OK;
+}
+
+size_t workspace_bytes(const muon_act8_grad_item* items, int n, int dt) {
+    long long most = 0;
+    Plan P;
+    for (int b = 0; b < n; b += kItems) {
+        plan_batch(items + b, std::min(kItems, n - b), dt, P);
+        most = std::max(most, P.bytes);
+    }
+    return (size_t)most;
+}
+
 }  // namespace
 }  // namespace muon
 
@@ -82,26 +691,24 @@ muon_status act8_grad_workspace_size(const muon_act8_grad_item* items, int n, mu
     if (!bytes || !valid(dy_dtype)) return MUON_ERR_INVALID_ARG;
     const muon_status st = check_items(items, n);
     if (st != MUON_OK) return st;
-    *bytes = 0;
+    *bytes = workspace_bytes(items, n, dy_dtype);
     return MUON_OK;
 }
 
 muon_status act8_grad_batched(const muon_act8_grad_item* items, int n, muon_dtype dy_dtype, muon_dtype w_dtype,
                               void* workspace, size_t ws_bytes, int* d_status, muon_stream_t stream) {
-    (void)workspace; (void)ws_bytes; (void)d_status;
     if (!valid(dy_dtype) || !valid(w_dtype)) return MUON_ERR_INVALID_ARG;
     muon_status st = check_items(items, n);
     if (st != MUON_OK) return st;
+    const size_t need = workspace_bytes(items, n, dy_dtype);
+    if (need && (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255) || ws_bytes < need))
+        return MUON_ERR_WORKSPACE;
     st = check_device();
     if (st != MUON_OK) return st;
-    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    for (int i = 0; i < n; ++i) {
-        const muon_act8_grad_item& q = items[i];
-        const dim3 grid((q.c.cols + kT - 1) / kT, (q.out + kT - 1) / kT);
-        trace_begin(MUON_KERNEL_ACT8_GRAD, 2.0 * q.c.rows * q.out * q.c.cols, s);
-        act8_grad_simple<<<grid, 256, 0, s>>>(q, dy_dtype, w_dtype);
-        trace_end(s);
-        if (cudaGetLastError() != cudaSuccess) return MUON_ERR_CUDA;
+    for (int b = 0; b < n; b += kItems) {
+        st = run_batch(items + b, std::min(kItems, n - b), dy_dtype, w_dtype, static_cast<uint8_t*>(workspace), d_status,
+                       reinterpret_cast<cudaStream_t>(stream));
+        if (st != MUON_OK) return st;
     }
     return MUON_OK;
 }

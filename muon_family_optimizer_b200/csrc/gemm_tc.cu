@@ -1158,9 +1158,8 @@ static PFN_cuTensorMapEncodeTiled_v12000 get_encode() {
 
 // 3-D map over `count` matrices of `rows` x `inner` 16-bit elements with row
 // stride `ld` and matrix stride `mstride` (elements); box = box_inner x box_rows x 1.
-static bool encode_map(CUtensorMap* map, int dt, const void* base, long long inner, long long rows,
-                       long long count, long long ld, long long mstride, int box_inner, int box_rows,
-                       bool swizzle = true) {
+bool encode_map(CUtensorMap* map, int dt, const void* base, long long inner, long long rows,
+                long long count, long long ld, long long mstride, int box_inner, int box_rows, bool swizzle) {
     auto enc = get_encode();
     if (!enc) return false;
     cuuint64_t dims[3] = {(cuuint64_t)inner, (cuuint64_t)rows, (cuuint64_t)count};
