@@ -15,11 +15,15 @@
 //   warps 2-9   epilogue: tcgen05.ld, gain, shift, beta, store (or the fp32 part of a
 //               range of tokens), overlapped with the next tile through two
 //               accumulator buffers;
-//   warps 10-17 converters: 16 codes and their exponent byte per load, kept
-//               kAhead k-blocks ahead in registers, to two 16-byte pieces of the
-//               swizzled operand.
+//   warps 10-17 converters: 16 codes and their exponent byte from a ring of raw
+//               stages to two 16-byte pieces of the swizzled operand;
+//   warp 18     fills the raw ring: codes by TMA (128 columns x 64 tokens), exponent
+//               bytes (any alignment) through registers, kAhead k-blocks in flight.
 // A stage is full when both CTAs' boxes have landed and the converters of
-// both have arrived on the leader's barrier.
+// both have arrived on the leader's barrier.  The converters touch no global memory: the
+// fence that shows their stores to the tensor cores waits for every access of
+// the thread, and with the codes loaded by the converters themselves it waited
+// for the loads of later k-blocks too (2.44 ms for 14336 x 4096 over 8192 tokens).
 //
 // Layers with few tiles split the tokens (plan_batch): the ranges write fp32
 // parts to the workspace and a second kernel adds them in order.
@@ -37,21 +41,25 @@ namespace {
 constexpr int kItems = 48;              // layers per launch
 constexpr int kBM = 128, kBN = 256;     // rows of a CTA, columns of a pair's tile
 constexpr int kBK = 64;                 // tokens per stage
-constexpr int kStages = 6;
+constexpr int kStages = 5;
+constexpr int kRaw = 6;                 // raw stages: more than kAhead (see the raw producer)
 constexpr int kABytes = kBM * kBK * 2, kBBytes = kBN / 2 * kBK * 2;
 constexpr int kStageBytes = kABytes + kBBytes;
 constexpr int kEpiWarps = 8, kConvWarps = 8;
-constexpr int kThreads = 64 + 32 * (kEpiWarps + kConvWarps);
-constexpr int kAhead = 4;               // k-blocks of codes in a converter's registers
+constexpr int kGroupWarps = 2, kConvGroups = kConvWarps / kGroupWarps;     // converters of one k-block; k-blocks at once
+constexpr int kThreads = 96 + 32 * (kEpiWarps + kConvWarps);
+constexpr int kAhead = 4;               // k-blocks whose exponent bytes are in flight
+constexpr int kRawCodes = kBN / 2 * kBK, kRawBytes = kRawCodes + 4 * kBK;
 constexpr int kGroup = 8;               // tile rows walked together
-constexpr int kSmem = 1024 + kStages * kStageBytes + 256;
+constexpr int kSmem = 1024 + kStages * kStageBytes + kRaw * kRawBytes + 256;
 constexpr int kPlanSms = 148;           // work lists are planned for a whole B200, so a size query needs no device
 
 struct GradItem {
     CUtensorMap map;                    // dY: boxes of 64 columns x 64 tokens, parts as the third dimension
-    const signed char* q;
+    CUtensorMap codes;                  // q: boxes of 128 columns x 64 tokens
     const unsigned char* e;
-    long long ldq, lde;
+    long long lde;
+    int e_words;                        // rows of e may be read in aligned 4-byte words
     int rows, cols, out;
     int nkb;                            // k-blocks of one part
     int splits, len;                    // ranges of tokens, k-blocks (over all parts) of one range
@@ -122,8 +130,19 @@ __device__ __forceinline__ void convert16(const uint4& q, int byte, uint4& lo, u
             o[2 * i] = codes_bf16(__byte_perm(w[i], 0, 0x1100), scale2, sub2);
             o[2 * i + 1] = codes_bf16(__byte_perm(w[i], 0, 0x3322), scale2, sub2);
         }
+    } else if (byte >= 127 - 24 && byte <= 127 + 15) {
+        // 2^e is an fp16 value: 0x6400 | (q + 128) is 1152 + q, less 1152 exactly q, times 2^e rounded once
+        const uint32_t sc = byte >= 127 - 14 ? (uint32_t)(byte - 112) << 10 : 1u << (byte - 103);
+        const uint32_t scale2 = sc * 0x00010001u, off2 = 0x64806480u;
+        const __half2 s2 = *reinterpret_cast<const __half2*>(&scale2), o2 = *reinterpret_cast<const __half2*>(&off2);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const uint32_t h = __byte_perm(w[i >> 1] ^ 0x80808080u, 0x64646464u, i & 1 ? 0x4342 : 0x4140);
+            const __half2 r = __hmul2(__hsub2(*reinterpret_cast<const __half2*>(&h), o2), s2);
+            o[i] = *reinterpret_cast<const uint32_t*>(&r);
+        }
     } else {
-        // fp16's range ends at 2^-24 and 2^16: through fp32, one rounding at the end
+        // below fp16's smallest step or beyond its range: through fp32, one rounding
         const float s = byte == kActBad ? __uint_as_float(0x7FC00000u) : act8_scale(byte);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -135,13 +154,6 @@ __device__ __forceinline__ void convert16(const uint4& q, int byte, uint4& lo, u
     }
     lo = make_uint4(o[0], o[1], o[2], o[3]);
     hi = make_uint4(o[4], o[5], o[6], o[7]);
-}
-
-__device__ __forceinline__ uint4 ld_codes(const signed char* p) {
-    uint4 v;
-    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
-                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
-    return v;
 }
 
 // gain, shift and beta on 32 columns of one row, and the store.  gn, sh: this lane's
@@ -180,9 +192,12 @@ template <typename T>
 __global__ void __launch_bounds__(kThreads, 1) act8_grad_kernel(const __grid_constant__ GradParams p) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    uint64_t* full_bar = reinterpret_cast<uint64_t*>(smem + kStages * kStageBytes);
+    uint8_t* raw = smem + kStages * kStageBytes;
+    uint64_t* full_bar = reinterpret_cast<uint64_t*>(raw + kRaw * kRawBytes);
     uint64_t* empty_bar = full_bar + kStages;
-    uint64_t* tfull_bar = empty_bar + kStages;
+    uint64_t* rfull_bar = empty_bar + kStages;
+    uint64_t* rempty_bar = rfull_bar + kRaw;
+    uint64_t* tfull_bar = rempty_bar + kRaw;
     uint64_t* tempty_bar = tfull_bar + 2;
     uint64_t* drain_bar = tempty_bar + 2;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain_bar + 1);
@@ -194,8 +209,12 @@ __global__ void __launch_bounds__(kThreads, 1) act8_grad_kernel(const __grid_con
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < kStages; ++s) {
-            mbar_init(&full_bar[s], 1 + 2 * kConvWarps);    // the armed byte count, both CTAs' converter warps
+            mbar_init(&full_bar[s], 1 + 2 * kGroupWarps);   // the armed byte count, both CTAs' converter warps
             mbar_init(&empty_bar[s], 1);
+        }
+        for (int s = 0; s < kRaw; ++s) {
+            mbar_init(&rfull_bar[s], 2);                    // the armed byte count, the exponent bytes
+            mbar_init(&rempty_bar[s], kGroupWarps);
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(&tfull_bar[b], 1);
@@ -316,61 +335,107 @@ __global__ void __launch_bounds__(kThreads, 1) act8_grad_kernel(const __grid_con
             __syncwarp();
             if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(&tempty_bar[buf]), 0));
         }
-    } else {
+    } else if (warp < 2 + kEpiWarps + kConvWarps) {
         // ---------------------------------------------------- converters
-        const int tid = (int)threadIdx.x - 64 - 32 * kEpiWarps;
-        const int piece = tid & 7, tok0 = tid >> 3;         // 16 columns, tokens tok0 and tok0 + 32 of a k-block
+        // Pairs of warps take k-blocks in turn, so that the latencies of kConvGroups of them (barrier, shared
+        // memory, fence) overlap.
+        const int cw = warp - 2 - kEpiWarps, group = cw / kGroupWarps;
+        const int tid = (cw % kGroupWarps) * 32 + lane;
+        const int piece = tid & 7, tok0 = tid >> 3;         // 16 columns, tokens tok0 + 8 i of a k-block
         // the two 16-byte pieces of 16 columns in a 64-column box: row = token, pieces XORed with the token's low bits
-        const int box = (piece >> 2) * (64 * kBK * 2), pc = (piece & 3) * 2;
-        int stage = 0;
-        uint32_t phase = 0;
+        const int pc = (piece & 3) * 2, at = (piece >> 2) * (64 * kBK * 2) + tok0 * 128;
+        const int at0 = at + ((pc ^ tok0) << 4), at1 = at + (((pc + 1) ^ tok0) << 4);
+        uint32_t n = 0;                                     // k-blocks of this CTA before this work item
         bool ok = true;
         for (long long w = unit; ok && w < p.works; w += nunits) {
             const Work k = decode_work(p, w);
             const GradItem& I = p.it[k.item];
-            const int col = k.tj * kBN + (int)rank * (kBN / 2) + piece * 16;
-            const bool in = col < I.cols;
-            const signed char* qc = I.q + col;
-            const unsigned char* ec = I.e + col / kActBlock;
-            const int kb0 = k.split * I.len, kb1 = min(I.total, kb0 + I.len);
-            uint4 q[kAhead][2];
-            int e[kAhead][2];
-            auto fetch = [&](int kb, uint4 (&qq)[2], int (&ee)[2]) {
-                const int tb = (kb % I.nkb) * kBK + tok0;
+            const uint32_t len = (uint32_t)(min(I.total, (k.split + 1) * I.len) - k.split * I.len);
+            for (uint32_t j = n + (((uint32_t)group - n) & (kConvGroups - 1)); j < n + len; j += kConvGroups) {
+                const uint32_t rs = j % kRaw, stage = j % kStages;
+                if (!mbar_wait(&rfull_bar[rs], (j / kRaw) & 1, abort_flag, d_status)) { ok = false; break; }
+                const uint8_t* r = raw + rs * kRawBytes;
+                if (!mbar_wait(&empty_bar[stage], ((j / kStages) & 1) ^ 1, abort_flag, d_status)) { ok = false; break; }
+                uint8_t* sb = smem + stage * kStageBytes + kABytes;
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const long long t = tb + 32 * h;
-                    qq[h] = make_uint4(0u, 0u, 0u, 0u);
-                    ee[h] = 127;
-                    if (in && kb < kb1 && t < I.rows) {
-                        qq[h] = ld_codes(qc + t * I.ldq);
-                        ee[h] = __ldg(ec + t * I.lde);
-                    }
+                for (int i = 0; i < 8; ++i) {
+                    const uint4 q = *reinterpret_cast<const uint4*>(r + (tok0 + 8 * i) * (kBN / 2) + piece * 16);
+                    const int e = r[kRawCodes + (tok0 + 8 * i) * 4 + (piece >> 1)];
+                    uint4 lo, hi;
+                    convert16<T>(q, e, lo, hi);
+                    *reinterpret_cast<uint4*>(sb + at0 + i * 1024) = lo;
+                    *reinterpret_cast<uint4*>(sb + at1 + i * 1024) = hi;
                 }
-            };
-#pragma unroll
-            for (int d = 0; d < kAhead; ++d) fetch(kb0 + d, q[d], e[d]);
-            for (int kb = kb0; ok && kb < kb1; kb += kAhead) {
+                fence_proxy_async_smem();                   // the tensor cores read what was stored here
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive_cluster(mapa_shared(smem_u32(&full_bar[stage]), 0));
+                    mbar_arrive(&rempty_bar[rs]);
+                }
+            }
+            n += len;
+        }
+    } else {
+        // ---------------------------------------------------- raw producer
+        // Issues k-block kb's codes and loads its exponent bytes, and stores those of kb - kAhead: they have
+        // arrived by then.  A raw stage is waited for only after every k-block kAhead or more back has been
+        // handed over, so kRaw > kAhead stages cannot lock.
+        int ls = 0, ss = 0;         // stages of the next load and the next store
+        uint32_t lphase = 0;
+        bool ok = true;
+        for (long long w = unit; ok && w < p.works; w += nunits) {
+            const Work k = decode_work(p, w);
+            const GradItem& I = p.it[k.item];
+            const int col = k.tj * kBN + (int)rank * (kBN / 2), b0 = col / kActBlock, nb = act8_blocks(I.cols);
+            const bool words = I.e_words && b0 + 4 <= nb;
+            const int kb0 = k.split * I.len, kb1 = min(I.total, kb0 + I.len);
+            uint32_t e[kAhead][2];
+            for (int base = kb0; ok && base < kb1 + kAhead; base += kAhead) {
 #pragma unroll
                 for (int d = 0; d < kAhead; ++d) {
-                    if (!ok || kb + d >= kb1) break;
-                    uint4 lo[2], hi[2];
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) convert16<T>(q[d][h], e[d][h], lo[h], hi[h]);
-                    fetch(kb + d + kAhead, q[d], e[d]);
-                    if (!mbar_wait(&empty_bar[stage], phase ^ 1, abort_flag, d_status)) { ok = false; break; }
-                    uint8_t* sb = smem + stage * kStageBytes + kABytes + box;
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        const int t = tok0 + 32 * h;
-                        *reinterpret_cast<uint4*>(sb + t * 128 + ((pc ^ (t & 7)) << 4)) = lo[h];
-                        *reinterpret_cast<uint4*>(sb + t * 128 + (((pc + 1) ^ (t & 7)) << 4)) = hi[h];
+                    const int kbs = base + d - kAhead, kbl = base + d;
+                    if (kbs >= kb0 && kbs < kb1) {
+                        uint32_t* dst = reinterpret_cast<uint32_t*>(raw + ss * kRawBytes + kRawCodes);
+                        dst[lane] = e[d][0];
+                        dst[lane + 32] = e[d][1];
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&rfull_bar[ss]);
+                        if (++ss == kRaw) ss = 0;
                     }
-                    fence_proxy_async_smem();       // the tensor cores read what was stored here
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(&full_bar[stage]), 0));
-                    if (++stage == kStages) { stage = 0; phase ^= 1; }
+                    if (kbl < kb1 && ok) {
+                        if (!mbar_wait(&rempty_bar[ls], lphase ^ 1, abort_flag, d_status)) ok = false;
+                        ok = __all_sync(0xFFFFFFFFu, ok);
+                        if (ok) {
+                            const int tok = (kbl % I.nkb) * kBK;
+                            if (lane == 0) {
+                                mbar_arrive_expect_tx(&rfull_bar[ls], kRawCodes);
+                                tma_load_3d(&I.codes, &rfull_bar[ls], raw + ls * kRawBytes, col, tok, 0);
+                            }
+#pragma unroll
+                            for (int h = 0; h < 2; ++h) {
+                                const long long t = tok + lane + 32 * h;
+                                uint32_t v = 0x7F7F7F7Fu;
+                                if (t < I.rows) {
+                                    const unsigned char* src = I.e + t * I.lde + b0;
+                                    if (words) {
+                                        v = __ldg(reinterpret_cast<const uint32_t*>(src));
+                                    } else {
+#pragma unroll
+                                        for (int j = 0; j < 4; ++j)
+                                            if (b0 + j < nb) v = (v & ~(0xFFu << 8 * j)) | (uint32_t)__ldg(src + j) << 8 * j;
+                                    }
+                                }
+                                e[d][h] = v;
+                            }
+                            if (++ls == kRaw) { ls = 0; lphase ^= 1; }
+                        }
+                    }
                 }
+            }
+        }
+        if (*abort_flag && lane == 0) {
+            const unsigned long long t0 = global_ns();
+            while (global_ns() - t0 < 200000ull) {
             }
         }
     }
@@ -606,7 +671,8 @@ muon_status run_batch(const muon_act8_grad_item* items, int n, int dt, int w_dt,
     for (int i = 0; i < n; ++i) {
         const muon_act8_grad_item& q = items[i];
         GradItem& I = prm.it[i];
-        I.q = q.c.q; I.e = q.c.e; I.ldq = q.c.ldq; I.lde = q.c.lde;
+        I.e = q.c.e; I.lde = q.c.lde;
+        I.e_words = (reinterpret_cast<uintptr_t>(q.c.e) & 3) == 0 && (q.c.lde & 3) == 0;
         I.rows = q.c.rows; I.cols = q.c.cols; I.out = q.out;
         I.nkb = (q.c.rows + kBK - 1) / kBK;
         I.total = I.nkb * parts;
@@ -638,7 +704,8 @@ muon_status run_batch(const muon_act8_grad_item* items, int n, int dt, int w_dt,
             copy_bytes += (double)q.c.rows * q.out * (dt_size(dt) + 2.0 * parts);
         }
         if (!tc::encode_map(&I.map, dt == DT_FP16 ? DT_FP16 : DT_BF16, base, q.out, q.c.rows, parts, ld,
-                            parts == 1 ? ld : stride, 64, kBK))
+                            parts == 1 ? ld : stride, 64, kBK) ||
+            !tc::encode_bytes_map(&I.codes, q.c.q, q.c.cols, q.c.rows, q.c.ldq, kBN / 2, kBK))
             return MUON_ERR_CUDA;
     }
     prm.n = n;

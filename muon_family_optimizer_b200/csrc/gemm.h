@@ -34,6 +34,9 @@ namespace tc {
 // Tensor map over `count` matrices of rows x inner 16-bit elements (gemm_tc.cu).
 bool encode_map(CUtensorMap* map, int dt, const void* base, long long inner, long long rows, long long count,
                 long long ld, long long mstride, int box_inner, int box_rows, bool swizzle = true);
+// The same over one matrix of bytes, boxes not swizzled.
+bool encode_bytes_map(CUtensorMap* map, const void* base, long long inner, long long rows, long long ld, int box_inner,
+                      int box_rows);
 // tcgen05 back end for 16-bit operands (dt = DT_BF16 or DT_FP16); all ops of
 // one call must have the same `sym` and are run by one launch.
 muon_status tc_run(const GemmOp* ops, int nops, int dt, const FinalCtx& fc, const FinalEntry* fin,

@@ -1174,6 +1174,19 @@ bool encode_map(CUtensorMap* map, int dt, const void* base, long long inner, lon
     return r == CUDA_SUCCESS;
 }
 
+bool encode_bytes_map(CUtensorMap* map, const void* base, long long inner, long long rows, long long ld, int box_inner,
+                      int box_rows) {
+    auto enc = get_encode();
+    if (!enc) return false;
+    cuuint64_t dims[3] = {(cuuint64_t)inner, (cuuint64_t)rows, 1};
+    cuuint64_t strides[2] = {(cuuint64_t)ld, (cuuint64_t)ld};
+    cuuint32_t box[3] = {(cuuint32_t)box_inner, (cuuint32_t)box_rows, 1};
+    cuuint32_t estr[3] = {1, 1, 1};
+    return enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(base), dims, strides, box, estr,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 template <int BN, bool B_MN, bool PAIR, bool FIN, bool TRX, typename T, bool S1 = false>
 static cudaError_t launch_one(const TcParams& prm, int grid, cudaStream_t stream) {
     using C = Cfg<BN, PAIR, B_MN, FIN, S1>;
