@@ -18,7 +18,7 @@
 //   warps 10-17 converters: 16 codes and their exponent byte from a ring of raw
 //               stages to two 16-byte pieces of the swizzled operand;
 //   warp 18     fills the raw ring: codes by TMA (128 columns x 64 tokens), exponent
-//               bytes (any alignment) through registers, kAhead k-blocks in flight.
+//               bytes (any alignment) as the aligned words that hold them by cp.async.
 // A stage is full when both CTAs' boxes have landed and the converters of
 // both have arrived on the leader's barrier.  The converters touch no global memory: the
 // fence that shows their stores to the tensor cores waits for every access of
@@ -41,15 +41,14 @@ namespace {
 constexpr int kItems = 48;              // layers per launch
 constexpr int kBM = 128, kBN = 256;     // rows of a CTA, columns of a pair's tile
 constexpr int kBK = 64;                 // tokens per stage
-constexpr int kStages = 5;
-constexpr int kRaw = 6;                 // raw stages: more than kAhead (see the raw producer)
+constexpr int kStages = 4;
+constexpr int kRaw = 10;                // raw stages
 constexpr int kABytes = kBM * kBK * 2, kBBytes = kBN / 2 * kBK * 2;
 constexpr int kStageBytes = kABytes + kBBytes;
 constexpr int kEpiWarps = 8, kConvWarps = 8;
 constexpr int kGroupWarps = 2, kConvGroups = kConvWarps / kGroupWarps;     // converters of one k-block; k-blocks at once
 constexpr int kThreads = 96 + 32 * (kEpiWarps + kConvWarps);
-constexpr int kAhead = 4;               // k-blocks whose exponent bytes are in flight
-constexpr int kRawCodes = kBN / 2 * kBK, kRawBytes = kRawCodes + 4 * kBK;
+constexpr int kRawCodes = kBN / 2 * kBK, kRawBytes = kRawCodes + 8 * kBK;
 constexpr int kGroup = 8;               // tile rows walked together
 constexpr int kSmem = 1024 + kStages * kStageBytes + kRaw * kRawBytes + 256;
 constexpr int kPlanSms = 148;           // work lists are planned for a whole B200, so a size query needs no device
@@ -59,7 +58,6 @@ struct GradItem {
     CUtensorMap codes;                  // q: boxes of 128 columns x 64 tokens
     const unsigned char* e;
     long long lde;
-    int e_words;                        // rows of e may be read in aligned 4-byte words
     int rows, cols, out;
     int nkb;                            // k-blocks of one part
     int splits, len;                    // ranges of tokens, k-blocks (over all parts) of one range
@@ -213,7 +211,7 @@ __global__ void __launch_bounds__(kThreads, 1) act8_grad_kernel(const __grid_con
             mbar_init(&empty_bar[s], 1);
         }
         for (int s = 0; s < kRaw; ++s) {
-            mbar_init(&rfull_bar[s], 2);                    // the armed byte count, the exponent bytes
+            mbar_init(&rfull_bar[s], 33);                   // the armed byte count, each lane's exponent bytes
             mbar_init(&rempty_bar[s], kGroupWarps);
         }
         for (int b = 0; b < 2; ++b) {
@@ -343,28 +341,37 @@ __global__ void __launch_bounds__(kThreads, 1) act8_grad_kernel(const __grid_con
         const int tid = (cw % kGroupWarps) * 32 + lane;
         const int piece = tid & 7, tok0 = tid >> 3;         // 16 columns, tokens tok0 + 8 i of a k-block
         // the two 16-byte pieces of 16 columns in a 64-column box: row = token, pieces XORed with the token's low bits
+        // Threads of the second box store their upper piece first: the eight pieces that go out together then
+        // cover the eight bank groups.
         const int pc = (piece & 3) * 2, at = (piece >> 2) * (64 * kBK * 2) + tok0 * 128;
-        const int at0 = at + ((pc ^ tok0) << 4), at1 = at + (((pc + 1) ^ tok0) << 4);
+        const bool swap = piece >= 4;
+        const int at0 = at + (((pc + swap) ^ tok0) << 4), at1 = at + (((pc + !swap) ^ tok0) << 4);
         uint32_t n = 0;                                     // k-blocks of this CTA before this work item
         bool ok = true;
         for (long long w = unit; ok && w < p.works; w += nunits) {
             const Work k = decode_work(p, w);
             const GradItem& I = p.it[k.item];
-            const uint32_t len = (uint32_t)(min(I.total, (k.split + 1) * I.len) - k.split * I.len);
+            const uint32_t kb0 = (uint32_t)(k.split * I.len), len = (uint32_t)min(I.total, (k.split + 1) * I.len) - kb0;
+            const uint32_t elde = (uint32_t)I.lde & 3u;
+            const uint32_t ebase = (uint32_t)reinterpret_cast<uintptr_t>(I.e) + (uint32_t)(k.tj * (kBN / kActBlock)) +
+                                   rank * (kBN / 2 / kActBlock);
             for (uint32_t j = n + (((uint32_t)group - n) & (kConvGroups - 1)); j < n + len; j += kConvGroups) {
                 const uint32_t rs = j % kRaw, stage = j % kStages;
                 if (!mbar_wait(&rfull_bar[rs], (j / kRaw) & 1, abort_flag, d_status)) { ok = false; break; }
                 const uint8_t* r = raw + rs * kRawBytes;
+                // byte offset of a token's first exponent in its aligned word
+                const uint32_t e0 = ebase + (uint32_t)((int)((kb0 + (j - n)) % (uint32_t)I.nkb) * kBK) * elde;
                 if (!mbar_wait(&empty_bar[stage], ((j / kStages) & 1) ^ 1, abort_flag, d_status)) { ok = false; break; }
                 uint8_t* sb = smem + stage * kStageBytes + kABytes;
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
                     const uint4 q = *reinterpret_cast<const uint4*>(r + (tok0 + 8 * i) * (kBN / 2) + piece * 16);
-                    const int e = r[kRawCodes + (tok0 + 8 * i) * 4 + (piece >> 1)];
-                    uint4 lo, hi;
-                    convert16<T>(q, e, lo, hi);
-                    *reinterpret_cast<uint4*>(sb + at0 + i * 1024) = lo;
-                    *reinterpret_cast<uint4*>(sb + at1 + i * 1024) = hi;
+                    const int t = tok0 + 8 * i;
+                    const int e = r[kRawCodes + t * 8 + ((e0 + t * elde) & 3) + (piece >> 1)];
+                    uint4 first, second;
+                    convert16<T>(swap ? make_uint4(q.z, q.w, q.x, q.y) : q, e, first, second);
+                    *reinterpret_cast<uint4*>(sb + at0 + i * 1024) = first;
+                    *reinterpret_cast<uint4*>(sb + at1 + i * 1024) = second;
                 }
                 fence_proxy_async_smem();                   // the tensor cores read what was stored here
                 __syncwarp();
@@ -377,62 +384,43 @@ __global__ void __launch_bounds__(kThreads, 1) act8_grad_kernel(const __grid_con
         }
     } else {
         // ---------------------------------------------------- raw producer
-        // Issues k-block kb's codes and loads its exponent bytes, and stores those of kb - kAhead: they have
-        // arrived by then.  A raw stage is waited for only after every k-block kAhead or more back has been
-        // handed over, so kRaw > kAhead stages cannot lock.
-        int ls = 0, ss = 0;         // stages of the next load and the next store
-        uint32_t lphase = 0;
+        uint32_t n = 0;
         bool ok = true;
         for (long long w = unit; ok && w < p.works; w += nunits) {
             const Work k = decode_work(p, w);
             const GradItem& I = p.it[k.item];
-            const int col = k.tj * kBN + (int)rank * (kBN / 2), b0 = col / kActBlock, nb = act8_blocks(I.cols);
-            const bool words = I.e_words && b0 + 4 <= nb;
+            const int col = k.tj * kBN + (int)rank * (kBN / 2), b0 = col / kActBlock, nb = act8_blocks(I.cols) - b0;
             const int kb0 = k.split * I.len, kb1 = min(I.total, kb0 + I.len);
-            uint32_t e[kAhead][2];
-            for (int base = kb0; ok && base < kb1 + kAhead; base += kAhead) {
-#pragma unroll
-                for (int d = 0; d < kAhead; ++d) {
-                    const int kbs = base + d - kAhead, kbl = base + d;
-                    if (kbs >= kb0 && kbs < kb1) {
-                        uint32_t* dst = reinterpret_cast<uint32_t*>(raw + ss * kRawBytes + kRawCodes);
-                        dst[lane] = e[d][0];
-                        dst[lane + 32] = e[d][1];
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(&rfull_bar[ss]);
-                        if (++ss == kRaw) ss = 0;
-                    }
-                    if (kbl < kb1 && ok) {
-                        if (!mbar_wait(&rempty_bar[ls], lphase ^ 1, abort_flag, d_status)) ok = false;
-                        ok = __all_sync(0xFFFFFFFFu, ok);
-                        if (ok) {
-                            const int tok = (kbl % I.nkb) * kBK;
-                            if (lane == 0) {
-                                mbar_arrive_expect_tx(&rfull_bar[ls], kRawCodes);
-                                tma_load_3d(&I.codes, &rfull_bar[ls], raw + ls * kRawBytes, col, tok, 0);
-                            }
-#pragma unroll
-                            for (int h = 0; h < 2; ++h) {
-                                const long long t = tok + lane + 32 * h;
-                                uint32_t v = 0x7F7F7F7Fu;
-                                if (t < I.rows) {
-                                    const unsigned char* src = I.e + t * I.lde + b0;
-                                    if (words) {
-                                        v = __ldg(reinterpret_cast<const uint32_t*>(src));
-                                    } else {
-#pragma unroll
-                                        for (int j = 0; j < 4; ++j)
-                                            if (b0 + j < nb) v = (v & ~(0xFFu << 8 * j)) | (uint32_t)__ldg(src + j) << 8 * j;
-                                    }
-                                }
-                                e[d][h] = v;
-                            }
-                            if (++ls == kRaw) { ls = 0; lphase ^= 1; }
-                        }
-                    }
+            for (int kb = kb0; kb < kb1; ++kb, ++n) {
+                const uint32_t rs = n % kRaw;
+                if (!mbar_wait(&rempty_bar[rs], ((n / kRaw) & 1) ^ 1, abort_flag, d_status)) ok = false;
+                ok = __all_sync(0xFFFFFFFFu, ok);
+                if (!ok) break;
+                uint8_t* r = raw + rs * kRawBytes;
+                const int tok = (kb % I.nkb) * kBK;
+                if (lane == 0) {
+                    mbar_arrive_expect_tx(&rfull_bar[rs], kRawCodes);
+                    tma_load_3d(&I.codes, &rfull_bar[rs], r, col, tok, 0);
                 }
+                // The aligned words that hold a token's four bytes (the second only where they cross into it);
+                // tokens and columns past the end get zeros, which stand for finite values times zero codes.
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const long long t = tok + lane + 32 * h;
+                    const bool in = t < I.rows && nb > 0;
+                    const uintptr_t src = reinterpret_cast<uintptr_t>(I.e) + (in ? t * I.lde + b0 : 0);
+                    const int off = (int)(src & 3);
+                    const char* word = reinterpret_cast<const char*>(src - off);
+                    uint8_t* dst = r + kRawCodes + (lane + 32 * h) * 8;
+                    cp_async4(dst, word, in ? 4u : 0u);
+                    if (!in) cp_async4(dst + 4, word, 0u);
+                    else if (off + min(4, nb) > 4) cp_async4(dst + 4, word + 4, 4u);
+                }
+                cp_async_mbar_arrive(&rfull_bar[rs]);
             }
         }
+        cp_async_commit();
+        cp_async_wait<0>();
         if (*abort_flag && lane == 0) {
             const unsigned long long t0 = global_ns();
             while (global_ns() - t0 < 200000ull) {
@@ -672,7 +660,6 @@ muon_status run_batch(const muon_act8_grad_item* items, int n, int dt, int w_dt,
         const muon_act8_grad_item& q = items[i];
         GradItem& I = prm.it[i];
         I.e = q.c.e; I.lde = q.c.lde;
-        I.e_words = (reinterpret_cast<uintptr_t>(q.c.e) & 3) == 0 && (q.c.lde & 3) == 0;
         I.rows = q.c.rows; I.cols = q.c.cols; I.out = q.out;
         I.nkb = (q.c.rows + kBK - 1) / kBK;
         I.total = I.nkb * parts;
