@@ -41,16 +41,19 @@ namespace {
 constexpr int kItems = 48;              // layers per launch
 constexpr int kBM = 128, kBN = 256;     // rows of a CTA, columns of a pair's tile
 constexpr int kBK = 64;                 // tokens per stage
-constexpr int kStages = 4;
-constexpr int kRaw = 10;                // raw stages
+constexpr int kAStages = 7;             // dY: as many as fit, its loads come from HBM and L2
+constexpr int kBStages = 3;             // converted X^: its stores come from registers
+constexpr int kRaw = 7;                 // codes
+static_assert(kBStages <= kAStages, "converters wait on the A stages' barriers");
 constexpr int kABytes = kBM * kBK * 2, kBBytes = kBN / 2 * kBK * 2;
-constexpr int kStageBytes = kABytes + kBBytes;
 constexpr int kEpiWarps = 8, kConvWarps = 8;
-constexpr int kGroupWarps = 2, kConvGroups = kConvWarps / kGroupWarps;     // converters of one k-block; k-blocks at once
+constexpr int kGroupWarps = 4, kConvGroups = kConvWarps / kGroupWarps;     // converters of one k-block; k-blocks at once
+constexpr int kPieces = 16 / kGroupWarps;                                  // 16-code pieces of a thread
 constexpr int kThreads = 96 + 32 * (kEpiWarps + kConvWarps);
 constexpr int kRawCodes = kBN / 2 * kBK, kRawBytes = kRawCodes + 8 * kBK;
 constexpr int kGroup = 8;               // tile rows walked together
-constexpr int kSmem = 1024 + kStages * kStageBytes + kRaw * kRawBytes + 256;
+constexpr int kBOffset = kAStages * kABytes, kRawOffset = kBOffset + kBStages * kBBytes;
+constexpr int kSmem = 1024 + kRawOffset + kRaw * kRawBytes + 512;
 constexpr int kPlanSms = 148;           // work lists are planned for a whole B200, so a size query needs no device
 
 struct GradItem {
@@ -190,10 +193,11 @@ template <typename T>
 __global__ void __launch_bounds__(kThreads, 1) act8_grad_kernel(const __grid_constant__ GradParams p) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    uint8_t* raw = smem + kStages * kStageBytes;
-    uint64_t* full_bar = reinterpret_cast<uint64_t*>(raw + kRaw * kRawBytes);
-    uint64_t* empty_bar = full_bar + kStages;
-    uint64_t* rfull_bar = empty_bar + kStages;
+    uint8_t* raw = smem + kRawOffset;
+    uint64_t* afull_bar = reinterpret_cast<uint64_t*>(raw + kRaw * kRawBytes);
+    uint64_t* done_bar = afull_bar + kAStages;          // k-block j's MMAs are complete: barrier j % kAStages
+    uint64_t* bfull_bar = done_bar + kAStages;
+    uint64_t* rfull_bar = bfull_bar + kBStages;
     uint64_t* rempty_bar = rfull_bar + kRaw;
     uint64_t* tfull_bar = rempty_bar + kRaw;
     uint64_t* tempty_bar = tfull_bar + 2;
@@ -206,10 +210,11 @@ __global__ void __launch_bounds__(kThreads, 1) act8_grad_kernel(const __grid_con
     int* d_status = p.d_status;
 
     if (threadIdx.x == 0) {
-        for (int s = 0; s < kStages; ++s) {
-            mbar_init(&full_bar[s], 1 + 2 * kGroupWarps);   // the armed byte count, both CTAs' converter warps
-            mbar_init(&empty_bar[s], 1);
+        for (int s = 0; s < kAStages; ++s) {
+            mbar_init(&afull_bar[s], 1);
+            mbar_init(&done_bar[s], 1);
         }
+        for (int s = 0; s < kBStages; ++s) mbar_init(&bfull_bar[s], 2 * kGroupWarps);   // both CTAs' converter warps
         for (int s = 0; s < kRaw; ++s) {
             mbar_init(&rfull_bar[s], 33);                   // the armed byte count, each lane's exponent bytes
             mbar_init(&rempty_bar[s], kGroupWarps);
@@ -243,14 +248,14 @@ __global__ void __launch_bounds__(kThreads, 1) act8_grad_kernel(const __grid_con
                 const int col = k.ti * 2 * kBM + (int)rank * kBM;
                 const int kb1 = min(I.total, (k.split + 1) * I.len);
                 for (int kb = k.split * I.len; kb < kb1; ++kb) {
-                    if (!mbar_wait(&empty_bar[stage], phase ^ 1, abort_flag, d_status)) break;
-                    uint8_t* sa = smem + stage * kStageBytes;
-                    if (rank == 0) mbar_arrive_expect_tx(&full_bar[stage], 2 * kABytes);
-                    const uint32_t fb = mapa_shared(smem_u32(&full_bar[stage]), 0);
+                    if (!mbar_wait(&done_bar[stage], phase ^ 1, abort_flag, d_status)) break;
+                    uint8_t* sa = smem + stage * kABytes;
+                    if (rank == 0) mbar_arrive_expect_tx(&afull_bar[stage], 2 * kABytes);
+                    const uint32_t fb = mapa_shared(smem_u32(&afull_bar[stage]), 0);
                     const int part = kb / I.nkb, tok = (kb - part * I.nkb) * kBK;
                     tma_load_3d_pair(&I.map, fb, sa, col, tok, part);
                     tma_load_3d_pair(&I.map, fb, sa + 64 * kBK * 2, col + 64, tok, part);
-                    if (++stage == kStages) { stage = 0; phase ^= 1; }
+                    if (++stage == kAStages) { stage = 0; phase ^= 1; }
                 }
             }
             if (*abort_flag) {      // give the copies in flight time to land before the CTA exits
@@ -263,8 +268,11 @@ __global__ void __launch_bounds__(kThreads, 1) act8_grad_kernel(const __grid_con
         if (lane == 0 && rank == 0) {
             // ------------------------------------------------ MMA issuer
             constexpr uint32_t idesc = make_idesc_f16(IsBf16<T>::value ? 1 : 0, 1, 2 * kBM, kBN) | 1u << 15;
-            int stage = 0, it = 0;
-            uint32_t phase = 0;
+            // start addresses stay below the descriptor's 14-bit address field, so stages are plain additions
+            const uint64_t desc_a = smem_desc_sw128(smem_u32(smem), 64 * kBK * 2, 1024);
+            const uint64_t desc_b = smem_desc_sw128(smem_u32(smem + kBOffset), 64 * kBK * 2, 1024);
+            int as = 0, bs = 0, it = 0;
+            uint32_t aphase = 0, bphase = 0;
             bool ok = true;
             for (long long w = unit; ok && w < p.works; w += nunits, ++it) {
                 const Work k = decode_work(p, w);
@@ -275,21 +283,24 @@ __global__ void __launch_bounds__(kThreads, 1) act8_grad_kernel(const __grid_con
                 const uint32_t d_tmem = tmem_base + (uint32_t)(buf * kBN);
                 const int kb0 = k.split * I.len, kb1 = min(I.total, kb0 + I.len);
                 for (int kb = kb0; kb < kb1; ++kb) {
-                    if (!mbar_wait(&full_bar[stage], phase, abort_flag, d_status)) { ok = false; break; }
+                    if (!mbar_wait(&afull_bar[as], aphase, abort_flag, d_status) ||
+                        !mbar_wait(&bfull_bar[bs], bphase, abort_flag, d_status)) {
+                        ok = false;
+                        break;
+                    }
                     tc_fence_after();
-                    const uint32_t sa = smem_u32(smem + stage * kStageBytes), sb = sa + kABytes;
+                    // 16 tokens of an MMA: 16 rows of 128 bytes in each 64-wide box
+                    const uint64_t da = desc_a + (uint64_t)(as * (kABytes >> 4)), db = desc_b + (uint64_t)(bs * (kBBytes >> 4));
 #pragma unroll
-                    for (int s = 0; s < kBK / 16; ++s)      // 16 tokens: 16 rows of 128 bytes in each 64-wide box
-                        tc_mma_f16_pair(d_tmem, smem_desc_sw128(sa + s * 2048, 64 * kBK * 2, 1024),
-                                        smem_desc_sw128(sb + s * 2048, 64 * kBK * 2, 1024), idesc,
+                    for (int s = 0; s < kBK / 16; ++s)
+                        tc_mma_f16_pair(d_tmem, da + s * (2048 >> 4), db + s * (2048 >> 4), idesc,
                                         kb > kb0 || s > 0 ? 1u : 0u);
-                    tc_commit_pair(smem_u32(&empty_bar[stage]));
-                    tc_commit_pair(mapa_shared(smem_u32(&empty_bar[stage]), 1));
-                    if (++stage == kStages) { stage = 0; phase ^= 1; }
+                    tc_commit_pair_multicast(smem_u32(&done_bar[as]), 3);
+                    if (++as == kAStages) { as = 0; aphase ^= 1; }
+                    if (++bs == kBStages) { bs = 0; bphase ^= 1; }
                 }
                 if (!ok) break;
-                tc_commit_pair(smem_u32(&tfull_bar[buf]));
-                tc_commit_pair(mapa_shared(smem_u32(&tfull_bar[buf]), 1));
+                tc_commit_pair_multicast(smem_u32(&tfull_bar[buf]), 3);
             }
             // no MMA may still be writing tensor memory when it is freed
             tc_commit_pair(smem_u32(drain_bar));
@@ -335,17 +346,18 @@ __global__ void __launch_bounds__(kThreads, 1) act8_grad_kernel(const __grid_con
         }
     } else if (warp < 2 + kEpiWarps + kConvWarps) {
         // ---------------------------------------------------- converters
-        // Pairs of warps take k-blocks in turn, so that the latencies of kConvGroups of them (barrier, shared
-        // memory, fence) overlap.
+        // Groups of kGroupWarps warps take k-blocks in turn.  A k-block is converted in registers before its operand
+        // stage is waited for, so a stage is only held for the stores and the MMAs.
         const int cw = warp - 2 - kEpiWarps, group = cw / kGroupWarps;
         const int tid = (cw % kGroupWarps) * 32 + lane;
-        const int piece = tid & 7, tok0 = tid >> 3;         // 16 columns, tokens tok0 + 8 i of a k-block
-        // the two 16-byte pieces of 16 columns in a 64-column box: row = token, pieces XORed with the token's low bits
+        constexpr int kTokStep = kGroupWarps * 4;
+        const int piece = tid & 7, tok0 = tid >> 3;         // 16 columns, tokens tok0 + kTokStep i of a k-block
+        // The two 16-byte pieces of 16 columns in a 64-column box: row = token, pieces XORed with the token's low bits.
         // Threads of the second box store their upper piece first: the eight pieces that go out together then
         // cover the eight bank groups.
         const int pc = (piece & 3) * 2, at = (piece >> 2) * (64 * kBK * 2) + tok0 * 128;
         const bool swap = piece >= 4;
-        const int at0 = at + (((pc + swap) ^ tok0) << 4), at1 = at + (((pc + !swap) ^ tok0) << 4);
+        const int at0 = at + (((pc + swap) ^ (tok0 & 7)) << 4), at1 = at + (((pc + !swap) ^ (tok0 & 7)) << 4);
         uint32_t n = 0;                                     // k-blocks of this CTA before this work item
         bool ok = true;
         for (long long w = unit; ok && w < p.works; w += nunits) {
@@ -356,29 +368,36 @@ __global__ void __launch_bounds__(kThreads, 1) act8_grad_kernel(const __grid_con
             const uint32_t ebase = (uint32_t)reinterpret_cast<uintptr_t>(I.e) + (uint32_t)(k.tj * (kBN / kActBlock)) +
                                    rank * (kBN / 2 / kActBlock);
             for (uint32_t j = n + (((uint32_t)group - n) & (kConvGroups - 1)); j < n + len; j += kConvGroups) {
-                const uint32_t rs = j % kRaw, stage = j % kStages;
+                const uint32_t rs = j % kRaw, bs = j % kBStages;
                 if (!mbar_wait(&rfull_bar[rs], (j / kRaw) & 1, abort_flag, d_status)) { ok = false; break; }
                 const uint8_t* r = raw + rs * kRawBytes;
                 // byte offset of a token's first exponent in its aligned word
                 const uint32_t e0 = ebase + (uint32_t)((int)((kb0 + (j - n)) % (uint32_t)I.nkb) * kBK) * elde;
-                if (!mbar_wait(&empty_bar[stage], ((j / kStages) & 1) ^ 1, abort_flag, d_status)) { ok = false; break; }
-                uint8_t* sb = smem + stage * kStageBytes + kABytes;
+                uint4 first[kPieces], second[kPieces];
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const uint4 q = *reinterpret_cast<const uint4*>(r + (tok0 + 8 * i) * (kBN / 2) + piece * 16);
-                    const int t = tok0 + 8 * i;
+                for (int i = 0; i < kPieces; ++i) {
+                    const int t = tok0 + kTokStep * i;
+                    const uint4 q = *reinterpret_cast<const uint4*>(r + t * (kBN / 2) + piece * 16);
                     const int e = r[kRawCodes + t * 8 + ((e0 + t * elde) & 3) + (piece >> 1)];
-                    uint4 first, second;
-                    convert16<T>(swap ? make_uint4(q.z, q.w, q.x, q.y) : q, e, first, second);
-                    *reinterpret_cast<uint4*>(sb + at0 + i * 1024) = first;
-                    *reinterpret_cast<uint4*>(sb + at1 + i * 1024) = second;
+                    convert16<T>(swap ? make_uint4(q.z, q.w, q.x, q.y) : q, e, first[i], second[i]);
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&rempty_bar[rs]);
+                // the MMAs that read this operand stage last, k-block j - kBStages
+                const uint32_t last = j - kBStages;
+                if (j >= kBStages && !mbar_wait(&done_bar[last % kAStages], (last / kAStages) & 1, abort_flag, d_status)) {
+                    ok = false;
+                    break;
+                }
+                uint8_t* sb = smem + kBOffset + bs * kBBytes;
+#pragma unroll
+                for (int i = 0; i < kPieces; ++i) {
+                    *reinterpret_cast<uint4*>(sb + at0 + i * (kTokStep * 128)) = first[i];
+                    *reinterpret_cast<uint4*>(sb + at1 + i * (kTokStep * 128)) = second[i];
                 }
                 fence_proxy_async_smem();                   // the tensor cores read what was stored here
                 __syncwarp();
-                if (lane == 0) {
-                    mbar_arrive_cluster(mapa_shared(smem_u32(&full_bar[stage]), 0));
-                    mbar_arrive(&rempty_bar[rs]);
-                }
+                if (lane == 0) mbar_arrive_cluster_cta(mapa_shared(smem_u32(&bfull_bar[bs]), 0));
             }
             n += len;
         }

@@ -361,6 +361,19 @@ __device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar_cluster) {
     asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar_cluster) : "memory");
 }
 
+// The same on the mbarrier at one shared-memory offset in every CTA of `cta_mask`.
+__device__ __forceinline__ void tc_commit_pair_multicast(uint32_t bar_cluster, uint16_t cta_mask) {
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;"
+        ::"r"(bar_cluster), "h"(cta_mask) : "memory");
+}
+// Arrive on an mbarrier of any CTA of the cluster, releasing at CTA scope only: for
+// data that this CTA's tensor core reads after a proxy fence.  A release at cluster
+// scope waits for the SM's memory traffic, about 1300 cycles each.
+__device__ __forceinline__ void mbar_arrive_cluster_cta(uint32_t bar_cluster) {
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar_cluster) : "memory");
+}
+
 // Shared-memory matrix descriptor (sm_100 layout): start address, leading and
 // stride byte offsets (all >> 4), version 1, layout type 2 = 128-byte swizzle.
 __device__ __forceinline__ uint64_t smem_desc_sw128(uint32_t saddr, uint32_t lbo_bytes,
