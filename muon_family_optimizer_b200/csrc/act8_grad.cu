@@ -15,9 +15,9 @@
 //   warps 2-9   epilogue: tcgen05.ld, gain, shift, beta, store (or the fp32 part of a
 //               range of tokens), overlapped with the next tile through two
 //               accumulator buffers;
-//   warps 10-17 converters: 16 codes and their exponent byte from a ring of raw
+//   warps 10-21 converters: 16 codes and their exponent byte from a ring of raw
 //               stages to two 16-byte pieces of the swizzled operand;
-//   warp 18     fills the raw ring: codes by TMA (128 columns x 64 tokens), exponent
+//   warps 22-23 fill the raw ring: codes by TMA (128 columns x 64 tokens), exponent
 //               bytes (any alignment) as the aligned words that hold them by cp.async.
 // A stage is full when both CTAs' boxes have landed and the converters of
 // both have arrived on the leader's barrier.  The converters touch no global memory: the
@@ -46,10 +46,10 @@ constexpr int kBStages = 3;             // converted X^: its stores come from re
 constexpr int kRaw = 7;                 // codes
 static_assert(kBStages <= kAStages, "converters wait on the A stages' barriers");
 constexpr int kABytes = kBM * kBK * 2, kBBytes = kBN / 2 * kBK * 2;
-constexpr int kEpiWarps = 8, kConvWarps = 8;
+constexpr int kEpiWarps = 8, kConvWarps = 12, kRawWarps = 2;
 constexpr int kGroupWarps = 4, kConvGroups = kConvWarps / kGroupWarps;     // converters of one k-block; k-blocks at once
 constexpr int kPieces = 16 / kGroupWarps;                                  // 16-code pieces of a thread
-constexpr int kThreads = 96 + 32 * (kEpiWarps + kConvWarps);
+constexpr int kThreads = 32 * (2 + kEpiWarps + kConvWarps + kRawWarps);
 constexpr int kRawCodes = kBN / 2 * kBK, kRawBytes = kRawCodes + 8 * kBK;
 constexpr int kGroup = 8;               // tile rows walked together
 constexpr int kBOffset = kAStages * kABytes, kRawOffset = kBOffset + kBStages * kBBytes;
@@ -367,7 +367,7 @@ __global__ void __launch_bounds__(kThreads, 1) act8_grad_kernel(const __grid_con
             const uint32_t elde = (uint32_t)I.lde & 3u;
             const uint32_t ebase = (uint32_t)reinterpret_cast<uintptr_t>(I.e) + (uint32_t)(k.tj * (kBN / kActBlock)) +
                                    rank * (kBN / 2 / kActBlock);
-            for (uint32_t j = n + (((uint32_t)group - n) & (kConvGroups - 1)); j < n + len; j += kConvGroups) {
+            for (uint32_t j = n + (group + kConvGroups - n % kConvGroups) % kConvGroups; j < n + len; j += kConvGroups) {
                 const uint32_t rs = j % kRaw, bs = j % kBStages;
                 if (!mbar_wait(&rfull_bar[rs], (j / kRaw) & 1, abort_flag, d_status)) { ok = false; break; }
                 const uint8_t* r = raw + rs * kRawBytes;
@@ -402,41 +402,55 @@ __global__ void __launch_bounds__(kThreads, 1) act8_grad_kernel(const __grid_con
             n += len;
         }
     } else {
-        // ---------------------------------------------------- raw producer
+        // ---------------------------------------------------- raw producers
+        // kRawWarps warps take k-blocks in turn: the 64 rows' exponent bytes are scattered words, whose requests
+        // take one warp about as long as a k-block's MMAs.
+        const uint32_t mine = warp - 2 - kEpiWarps - kConvWarps;
         uint32_t n = 0;
         bool ok = true;
         for (long long w = unit; ok && w < p.works; w += nunits) {
             const Work k = decode_work(p, w);
             const GradItem& I = p.it[k.item];
-            const int col = k.tj * kBN + (int)rank * (kBN / 2), b0 = col / kActBlock, nb = act8_blocks(I.cols) - b0;
-            const int kb0 = k.split * I.len, kb1 = min(I.total, kb0 + I.len);
-            for (int kb = kb0; kb < kb1; ++kb, ++n) {
-                const uint32_t rs = n % kRaw;
-                if (!mbar_wait(&rempty_bar[rs], ((n / kRaw) & 1) ^ 1, abort_flag, d_status)) ok = false;
+            const int col = k.tj * kBN + (int)rank * (kBN / 2), b0 = col / kActBlock;
+            const int nb = min(4, act8_blocks(I.cols) - b0);            // exponent bytes of a token, if any
+            const int kb0 = k.split * I.len;
+            const uint32_t len = (uint32_t)(min(I.total, kb0 + I.len) - kb0);
+            uint32_t j = n + (mine + kRawWarps - n % kRawWarps) % kRawWarps;
+            int tok = ((kb0 + (int)(j - n)) % I.nkb) * kBK;
+            const unsigned char* src = I.e + (long long)(tok + lane) * I.lde + b0;
+            const long long half = 32 * I.lde, wrap = (long long)I.nkb * kBK * I.lde;
+            for (; j < n + len; j += kRawWarps) {
+                const uint32_t rs = j % kRaw;
+                if (!mbar_wait(&rempty_bar[rs], ((j / kRaw) & 1) ^ 1, abort_flag, d_status)) ok = false;
                 ok = __all_sync(0xFFFFFFFFu, ok);
                 if (!ok) break;
                 uint8_t* r = raw + rs * kRawBytes;
-                const int tok = (kb % I.nkb) * kBK;
                 if (lane == 0) {
                     mbar_arrive_expect_tx(&rfull_bar[rs], kRawCodes);
                     tma_load_3d(&I.codes, &rfull_bar[rs], r, col, tok, 0);
                 }
-                // The aligned words that hold a token's four bytes (the second only where they cross into it);
+                // The aligned words that hold a token's bytes (the second only where they cross into it);
                 // tokens and columns past the end get zeros, which stand for finite values times zero codes.
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                    const long long t = tok + lane + 32 * h;
-                    const bool in = t < I.rows && nb > 0;
-                    const uintptr_t src = reinterpret_cast<uintptr_t>(I.e) + (in ? t * I.lde + b0 : 0);
-                    const int off = (int)(src & 3);
-                    const char* word = reinterpret_cast<const char*>(src - off);
+                    const bool in = tok + lane + 32 * h < I.rows && nb > 0;
+                    const uintptr_t at = reinterpret_cast<uintptr_t>(src + h * half);
+                    const int off = (int)(at & 3);
+                    const char* word = reinterpret_cast<const char*>(in ? at - off : reinterpret_cast<uintptr_t>(I.e) & ~uintptr_t(3));
                     uint8_t* dst = r + kRawCodes + (lane + 32 * h) * 8;
                     cp_async4(dst, word, in ? 4u : 0u);
                     if (!in) cp_async4(dst + 4, word, 0u);
-                    else if (off + min(4, nb) > 4) cp_async4(dst + 4, word + 4, 4u);
+                    else if (off + nb > 4) cp_async4(dst + 4, word + 4, 4u);
                 }
                 cp_async_mbar_arrive(&rfull_bar[rs]);
+                tok += kRawWarps * kBK;
+                src += kRawWarps * 2 * half;
+                while (tok >= I.nkb * kBK) {                            // the next part of an fp32 dY
+                    tok -= I.nkb * kBK;
+                    src -= wrap;
+                }
             }
+            n += len;
         }
         cp_async_commit();
         cp_async_wait<0>();
