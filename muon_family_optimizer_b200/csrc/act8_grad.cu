@@ -204,8 +204,10 @@ __global__ void __launch_bounds__(kThreads, 1) act8_grad_kernel(const __grid_con
     uint64_t* drain_bar = tempty_bar + 2;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain_bar + 1);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const uint32_t rank = cluster_ctarank();
+    // warp and rank in forms the compiler knows to be uniform: the MMA issuer's descriptors then stay in uniform
+    // registers
+    const int warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
+    const uint32_t rank = blockIdx.x & 1u;      // rank in the cluster of two
     const long long unit = blockIdx.x >> 1, nunits = gridDim.x >> 1;
     int* d_status = p.d_status;
 
@@ -265,8 +267,11 @@ __global__ void __launch_bounds__(kThreads, 1) act8_grad_kernel(const __grid_con
             }
         }
     } else if (warp == 1) {
-        if (lane == 0 && rank == 0) {
+        if (rank == 0) {
             // ------------------------------------------------ MMA issuer
+            // The whole warp walks the loop and one lane issues, so that descriptors are uniform values: with a
+            // single thread in the loop each MMA took about 90 cycles to issue and a k-block about 900 of the 512
+            // that its MMAs run.
             constexpr uint32_t idesc = make_idesc_f16(IsBf16<T>::value ? 1 : 0, 1, 2 * kBM, kBN) | 1u << 15;
             // start addresses stay below the descriptor's 14-bit address field, so stages are plain additions
             const uint64_t desc_a = smem_desc_sw128(smem_u32(smem), 64 * kBK * 2, 1024);
@@ -278,32 +283,39 @@ __global__ void __launch_bounds__(kThreads, 1) act8_grad_kernel(const __grid_con
                 const Work k = decode_work(p, w);
                 const GradItem& I = p.it[k.item];
                 const int buf = it & 1;
-                if (!mbar_wait(&tempty_bar[buf], ((it >> 1) & 1) ^ 1, abort_flag, d_status)) break;
+                ok = __all_sync(0xFFFFFFFFu, mbar_wait(&tempty_bar[buf], ((it >> 1) & 1) ^ 1, abort_flag, d_status));
+                if (!ok) break;
                 tc_fence_after();
                 const uint32_t d_tmem = tmem_base + (uint32_t)(buf * kBN);
-                const int kb0 = k.split * I.len, kb1 = min(I.total, kb0 + I.len);
-                for (int kb = kb0; kb < kb1; ++kb) {
-                    if (!mbar_wait(&afull_bar[as], aphase, abort_flag, d_status) ||
-                        !mbar_wait(&bfull_bar[bs], bphase, abort_flag, d_status)) {
-                        ok = false;
-                        break;
+                const int len = min(I.total - k.split * I.len, I.len);
+                for (int kb = 0; kb < len; ++kb) {
+                    bool ready = mbar_try_wait(&afull_bar[as], aphase) && mbar_try_wait(&bfull_bar[bs], bphase);
+                    if (!__all_sync(0xFFFFFFFFu, ready)) {
+                        ready = mbar_wait(&afull_bar[as], aphase, abort_flag, d_status) &&
+                                mbar_wait(&bfull_bar[bs], bphase, abort_flag, d_status);
+                        if (!__all_sync(0xFFFFFFFFu, ready)) { ok = false; break; }
                     }
                     tc_fence_after();
                     // 16 tokens of an MMA: 16 rows of 128 bytes in each 64-wide box
                     const uint64_t da = desc_a + (uint64_t)(as * (kABytes >> 4)), db = desc_b + (uint64_t)(bs * (kBBytes >> 4));
+                    if (elect_one()) {
 #pragma unroll
-                    for (int s = 0; s < kBK / 16; ++s)
-                        tc_mma_f16_pair(d_tmem, da + s * (2048 >> 4), db + s * (2048 >> 4), idesc,
-                                        kb > kb0 || s > 0 ? 1u : 0u);
-                    tc_commit_pair_multicast(smem_u32(&done_bar[as]), 3);
+                        for (int s = 0; s < kBK / 16; ++s)
+                            tc_mma_f16_pair(d_tmem, da + s * (2048 >> 4), db + s * (2048 >> 4), idesc,
+                                            kb > 0 || s > 0 ? 1u : 0u);
+                        tc_commit_pair_multicast(smem_u32(&done_bar[as]), 3);
+                    }
+                    __syncwarp();
                     if (++as == kAStages) { as = 0; aphase ^= 1; }
                     if (++bs == kBStages) { bs = 0; bphase ^= 1; }
                 }
                 if (!ok) break;
-                tc_commit_pair_multicast(smem_u32(&tfull_bar[buf]), 3);
+                if (elect_one()) tc_commit_pair_multicast(smem_u32(&tfull_bar[buf]), 3);
+                __syncwarp();
             }
             // no MMA may still be writing tensor memory when it is freed
-            tc_commit_pair(smem_u32(drain_bar));
+            if (elect_one()) tc_commit_pair(smem_u32(drain_bar));
+            __syncwarp();
             const unsigned long long t0 = global_ns();
             while (!mbar_try_wait(drain_bar, 0) && global_ns() - t0 < kWaitLimitNs) {
             }

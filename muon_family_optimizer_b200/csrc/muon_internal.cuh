@@ -367,6 +367,12 @@ __device__ __forceinline__ void tc_commit_pair_multicast(uint32_t bar_cluster, u
         "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;"
         ::"r"(bar_cluster), "h"(cta_mask) : "memory");
 }
+// One lane of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+    return r != 0;
+}
 // Arrive on an mbarrier of any CTA of the cluster, releasing at CTA scope only: for
 // data that this CTA's tensor core reads after a proxy fence.  A release at cluster
 // scope waits for the SM's memory traffic, about 1300 cycles each.
