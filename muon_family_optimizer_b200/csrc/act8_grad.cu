@@ -39,21 +39,28 @@ namespace muon {
 namespace {
 
 constexpr int kItems = 48;              // layers per launch
-constexpr int kBM = 128, kBN = 256;     // rows of a CTA, columns of a pair's tile
+constexpr int kBM = 128, kBN = 256;     // rows of one MMA in a CTA, columns of a pair's tile
 constexpr int kBK = 64;                 // tokens per stage
-constexpr int kAStages = 7;             // dY: as many as fit, its loads come from HBM and L2
-constexpr int kBStages = 3;             // converted X^: its stores come from registers
-constexpr int kRaw = 7;                 // codes
-static_assert(kBStages <= kAStages, "converters wait on the A stages' barriers");
-constexpr int kABytes = kBM * kBK * 2, kBBytes = kBN / 2 * kBK * 2;
-constexpr int kEpiWarps = 8, kConvWarps = 12, kRawWarps = 2;
+constexpr int kBBytes = kBN / 2 * kBK * 2, kRawBytes = kBN / 2 * kBK, kExpBytes = 8 * kBK;
+constexpr int kEpiWarps = 8, kConvWarps = 8, kRawWarps = 2;
 constexpr int kGroupWarps = 4, kConvGroups = kConvWarps / kGroupWarps;     // converters of one k-block; k-blocks at once
-constexpr int kPieces = 16 / kGroupWarps;                                  // 16-code pieces of a thread
+constexpr int kTokens = 8 / kGroupWarps;                                   // 32-code blocks of a thread
 constexpr int kThreads = 32 * (2 + kEpiWarps + kConvWarps + kRawWarps);
-constexpr int kRawCodes = kBN / 2 * kBK, kRawBytes = kRawCodes + 8 * kBK;
 constexpr int kGroup = 8;               // tile rows walked together
-constexpr int kBOffset = kAStages * kABytes, kRawOffset = kBOffset + kBStages * kBBytes;
-constexpr int kSmem = 1024 + kRawOffset + kRaw * kRawBytes + 512;
+
+// MH MMAs of 256 rows share a converted operand: tiles of 256 MH x 256.
+template <int MH>
+struct Cfg {
+    static constexpr int kABytes = MH * kBM * kBK * 2;
+    static constexpr int kAStages = MH == 2 ? 4 : 7;        // dY: as many as fit, its loads come from HBM and L2
+    static constexpr int kBStages = 2;                      // converted X^: its stores come from registers
+    static constexpr int kRaw = MH == 2 ? 6 : 8;            // codes
+    static constexpr int kBufs = 2 / MH;                    // accumulators in the 512 columns
+    static constexpr int kBOffset = kAStages * kABytes, kRawOffset = kBOffset + kBStages * kBBytes;
+    static constexpr int kExpOffset = kRawOffset + kRaw * kRawBytes;
+    static constexpr int kSmem = 1024 + kExpOffset + kRaw * kExpBytes + 512;
+    static_assert(kConvGroups == kBStages && kBStages <= kAStages && kConvGroups < kRaw, "see the converters");
+};
 constexpr int kPlanSms = 148;           // work lists are planned for a whole B200, so a size query needs no device
 
 struct GradItem {
@@ -104,97 +111,74 @@ __device__ __forceinline__ Work decode_work(const GradParams& p, long long w) {
     return k;
 }
 
-// Two codes of `h` (each byte doubled into a 16-bit half) as bfloat16 values.
-// 0x4300 | (b & 127) is 128 + the low seven bits; q = that - 128, or - 256 for a
-// negative code, whose sign bit 7 raises the subtrahend's exponent by one.
-// (128 + low) 2^e - 128 2^e in one fused operation is exact.
-__device__ __forceinline__ uint32_t codes_bf16(uint32_t h, uint32_t scale2, uint32_t sub2) {
-    const uint32_t v = (h & 0x007F007Fu) | 0x43004300u;
-    const uint32_t c = (h & 0x00800080u) + sub2;
-    const __nv_bfloat162 r = __hfma2(*reinterpret_cast<const __nv_bfloat162*>(&v),
-                                     *reinterpret_cast<const __nv_bfloat162*>(&scale2),
-                                     *reinterpret_cast<const __nv_bfloat162*>(&c));
-    return *reinterpret_cast<const uint32_t*>(&r);
-}
-
-// Sixteen codes under one exponent byte to sixteen 16-bit values, lower columns first.
+// A block's 32 codes to 32 16-bit values in four 16-byte pieces.
+//
+// The bytes of a word (four columns) are taken as two pairs of halves, columns (0, 2)
+// and (1, 3), without reordering them.  Piece g of the block holds pair g of each of its
+// four groups of eight columns (pairs: columns (0, 2), (1, 3), (4, 6), (5, 7) of the
+// group).  That order of the operand's columns costs nothing and is the one in which a
+// thread of the epilogue's 16 x 256-bit reads of the accumulator gets a whole group.
+//
+// Per four codes, in bfloat16: a shift and four logical operations make
+// 128 + (q & 127) and the 128 or 256 to subtract (a code's sign bit is the exponent's
+// lowest bit there), the difference is q and its product with 2^e is exact; in fp16
+// the biased code fits the significand (1152 + q).  A bad block's codes are zeros and
+// its byte the exponent of infinity: 0 * inf makes the NaNs.
 template <typename T>
-__device__ __forceinline__ void convert16(const uint4& q, int byte, uint4& lo, uint4& hi) {
-    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
-    uint32_t o[8];
+__device__ __forceinline__ void convert32(const uint4& a, const uint4& b, int byte, uint4 (&o)[4]) {
+    const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+    uint32_t r[4][4];
     if constexpr (IsBf16<T>::value) {
-        // 2^e has the byte as its exponent field; a bad block's NaN goes through the product
-        const uint32_t scale2 = byte == kActBad ? 0x7FC07FC0u : (uint32_t)byte * 0x00800080u;
-        const uint32_t sub2 = 0x80008000u + (uint32_t)(byte == kActBad ? 0 : byte + 7) * 0x00800080u;
+        const uint32_t scale2 = (uint32_t)byte * 0x00800080u;
+        const __nv_bfloat162 s2 = *reinterpret_cast<const __nv_bfloat162*>(&scale2);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            o[2 * i] = codes_bf16(__byte_perm(w[i], 0, 0x1100), scale2, sub2);
-            o[2 * i + 1] = codes_bf16(__byte_perm(w[i], 0, 0x3322), scale2, sub2);
-        }
+        for (int g = 0; g < 4; ++g)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const uint32_t c = w[2 * i + (g >> 1)] >> (g & 1 ? 8 : 0);
+                const uint32_t v = (c & 0x007F007Fu) | 0x43004300u, d = (c & 0x00800080u) | 0x43004300u;
+                const __nv_bfloat162 x = __hmul2(__hsub2(*reinterpret_cast<const __nv_bfloat162*>(&v),
+                                                         *reinterpret_cast<const __nv_bfloat162*>(&d)), s2);
+                r[g][i] = *reinterpret_cast<const uint32_t*>(&x);
+            }
     } else if (byte >= 127 - 24 && byte <= 127 + 15) {
-        // 2^e is an fp16 value: 0x6400 | (q + 128) is 1152 + q, less 1152 exactly q, times 2^e rounded once
+        // 2^e is an fp16 value; the product is rounded once
         const uint32_t sc = byte >= 127 - 14 ? (uint32_t)(byte - 112) << 10 : 1u << (byte - 103);
         const uint32_t scale2 = sc * 0x00010001u, off2 = 0x64806480u;
         const __half2 s2 = *reinterpret_cast<const __half2*>(&scale2), o2 = *reinterpret_cast<const __half2*>(&off2);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const uint32_t h = __byte_perm(w[i >> 1] ^ 0x80808080u, 0x64646464u, i & 1 ? 0x4342 : 0x4140);
-            const __half2 r = __hmul2(__hsub2(*reinterpret_cast<const __half2*>(&h), o2), s2);
-            o[i] = *reinterpret_cast<const uint32_t*>(&r);
-        }
+        for (int g = 0; g < 4; ++g)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const uint32_t c = w[2 * i + (g >> 1)] >> (g & 1 ? 8 : 0);
+                const uint32_t h = (c & 0x00FF00FFu) ^ 0x64806480u;
+                const __half2 x = __hmul2(__hsub2(*reinterpret_cast<const __half2*>(&h), o2), s2);
+                r[g][i] = *reinterpret_cast<const uint32_t*>(&x);
+            }
     } else {
         // below fp16's smallest step or beyond its range: through fp32, one rounding
         const float s = byte == kActBad ? __uint_as_float(0x7FC00000u) : act8_scale(byte);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const float a = (float)(signed char)(w[i]) * s, b = (float)(signed char)(w[i] >> 8) * s;
-            const float c = (float)(signed char)(w[i] >> 16) * s, d = (float)(signed char)(w[i] >> 24) * s;
-            o[2 * i] = pack2<__half>(a, b);
-            o[2 * i + 1] = pack2<__half>(c, d);
-        }
+        for (int g = 0; g < 4; ++g)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const uint32_t c = w[2 * i + (g >> 1)] >> (g & 1 ? 8 : 0);
+                r[g][i] = pack2<__half>((float)(signed char)c * s, (float)(signed char)(c >> 16) * s);
+            }
     }
-    lo = make_uint4(o[0], o[1], o[2], o[3]);
-    hi = make_uint4(o[4], o[5], o[6], o[7]);
+#pragma unroll
+    for (int g = 0; g < 4; ++g) o[g] = make_uint4(r[g][0], r[g][1], r[g][2], r[g][3]);
 }
 
-// gain, shift and beta on 32 columns of one row, and the store.  gn, sh: this lane's
-// column's gain and shift (lane = column - c0).
-__device__ __forceinline__ void finish32(const GradItem& I, int w_dt, int row, int c0, float gn, float sh, float (&v)[32]) {
-    const bool in = row < I.out;
-    if (I.gain)
-#pragma unroll
-        for (int i = 0; i < 32; ++i) v[i] *= __shfl_sync(0xFFFFFFFFu, gn, i);
-    if (I.shift) {
-        const float d = in ? I.dy_sum[row] : 0.f;
-#pragma unroll
-        for (int i = 0; i < 32; ++i) v[i] = fmaf(d, __shfl_sync(0xFFFFFFFFu, sh, i), v[i]);
-    }
-    if (!in) return;
-    const long long at = (long long)row * I.cols + c0;
-    const int n = min(32, I.cols - c0);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const bool vec = I.vec && 8 * i + 8 <= n;
-        const int nv = max(0, min(8, n - 8 * i));
-        float x[8];
-#pragma unroll
-        for (int j = 0; j < 8; ++j) x[j] = v[8 * i + j];
-        if (I.beta != 0.f) {
-            float g[8];
-            load8_dt(I.G, at + 8 * i, w_dt, vec, nv, g);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) x[j] = fmaf(I.beta, g[j], x[j]);
-        }
-        store8_dt(I.G, at + 8 * i, w_dt, vec, nv, x);
-    }
-}
-
-template <typename T>
+template <typename T, int MH, int WDT>
 __global__ void __launch_bounds__(kThreads, 1) act8_grad_kernel(const __grid_constant__ GradParams p) {
+    using C = Cfg<MH>;
+    constexpr int kABytes = C::kABytes, kAStages = C::kAStages, kBStages = C::kBStages, kRaw = C::kRaw, kBufs = C::kBufs;
+    constexpr int kBOffset = C::kBOffset, kRawOffset = C::kRawOffset, kExpOffset = C::kExpOffset;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint8_t* raw = smem + kRawOffset;
-    uint64_t* afull_bar = reinterpret_cast<uint64_t*>(raw + kRaw * kRawBytes);
+    uint64_t* afull_bar = reinterpret_cast<uint64_t*>(smem + kExpOffset + kRaw * kExpBytes);
     uint64_t* done_bar = afull_bar + kAStages;          // k-block j's MMAs are complete: barrier j % kAStages
     uint64_t* bfull_bar = done_bar + kAStages;
     uint64_t* rfull_bar = bfull_bar + kBStages;
@@ -247,7 +231,7 @@ __global__ void __launch_bounds__(kThreads, 1) act8_grad_kernel(const __grid_con
             for (long long w = unit; w < p.works && !*abort_flag; w += nunits) {
                 const Work k = decode_work(p, w);
                 const GradItem& I = p.it[k.item];
-                const int col = k.ti * 2 * kBM + (int)rank * kBM;
+                const int col = k.ti * MH * 2 * kBM + (int)rank * kBM;
                 const int kb1 = min(I.total, (k.split + 1) * I.len);
                 for (int kb = k.split * I.len; kb < kb1; ++kb) {
                     if (!mbar_wait(&done_bar[stage], phase ^ 1, abort_flag, d_status)) break;
@@ -255,8 +239,9 @@ __global__ void __launch_bounds__(kThreads, 1) act8_grad_kernel(const __grid_con
                     if (rank == 0) mbar_arrive_expect_tx(&afull_bar[stage], 2 * kABytes);
                     const uint32_t fb = mapa_shared(smem_u32(&afull_bar[stage]), 0);
                     const int part = kb / I.nkb, tok = (kb - part * I.nkb) * kBK;
-                    tma_load_3d_pair(&I.map, fb, sa, col, tok, part);
-                    tma_load_3d_pair(&I.map, fb, sa + 64 * kBK * 2, col + 64, tok, part);
+#pragma unroll
+                    for (int h = 0; h < 2 * MH; ++h)     // halves of this CTA's 128 rows of each MMA
+                        tma_load_3d_pair(&I.map, fb, sa + h * (64 * kBK * 2), col + (h >> 1) * (2 * kBM) + (h & 1) * 64, tok, part);
                     if (++stage == kAStages) { stage = 0; phase ^= 1; }
                 }
             }
@@ -282,8 +267,8 @@ __global__ void __launch_bounds__(kThreads, 1) act8_grad_kernel(const __grid_con
             for (long long w = unit; ok && w < p.works; w += nunits, ++it) {
                 const Work k = decode_work(p, w);
                 const GradItem& I = p.it[k.item];
-                const int buf = it & 1;
-                ok = __all_sync(0xFFFFFFFFu, mbar_wait(&tempty_bar[buf], ((it >> 1) & 1) ^ 1, abort_flag, d_status));
+                const int buf = it % kBufs;
+                ok = __all_sync(0xFFFFFFFFu, mbar_wait(&tempty_bar[buf], ((it / kBufs) & 1) ^ 1, abort_flag, d_status));
                 if (!ok) break;
                 tc_fence_after();
                 const uint32_t d_tmem = tmem_base + (uint32_t)(buf * kBN);
@@ -301,8 +286,10 @@ __global__ void __launch_bounds__(kThreads, 1) act8_grad_kernel(const __grid_con
                     if (elect_one()) {
 #pragma unroll
                         for (int s = 0; s < kBK / 16; ++s)
-                            tc_mma_f16_pair(d_tmem, da + s * (2048 >> 4), db + s * (2048 >> 4), idesc,
-                                            kb > 0 || s > 0 ? 1u : 0u);
+#pragma unroll
+                            for (int h = 0; h < MH; ++h)
+                                tc_mma_f16_pair(d_tmem + h * kBN, da + (h * kBM * kBK * 2 >> 4) + s * (2048 >> 4),
+                                                db + s * (2048 >> 4), idesc, kb > 0 || s > 0 ? 1u : 0u);
                         tc_commit_pair_multicast(smem_u32(&done_bar[as]), 3);
                     }
                     __syncwarp();
@@ -327,91 +314,111 @@ __global__ void __launch_bounds__(kThreads, 1) act8_grad_kernel(const __grid_con
         for (long long w = unit; w < p.works; w += nunits, ++it) {
             const Work k = decode_work(p, w);
             const GradItem& I = p.it[k.item];
-            const int buf = it & 1;
-            if (!mbar_wait(&tfull_bar[buf], (it >> 1) & 1, abort_flag, d_status)) break;
+            const int buf = it % kBufs;
+            if (!mbar_wait(&tfull_bar[buf], (it / kBufs) & 1, abort_flag, d_status)) break;
             tc_fence_after();
-            const int row0 = k.ti * 2 * kBM + (int)rank * kBM + quad * 32, row = row0 + lane;
+            // the layer's fields in registers: the loop's fences would have them read again for every row
+            const int out = I.out, cols = I.cols;
+            const bool whole = I.splits == 1, wide = whole ? I.vec != 0 : true;
+            const long long ld = whole ? cols : I.ldp;
+            char* const base = whole ? static_cast<char*>(I.G) : reinterpret_cast<char*>(I.part + (long long)k.split * out * ld);
+            const void *gain = whole ? I.gain : nullptr, *shift = whole ? I.shift : nullptr;
+            const float* dy_sum = I.dy_sum;
+            const float beta = whole ? I.beta : 0.f;
 #pragma unroll 1
-            for (int c = 0; c < kBN / 64; ++c) {
-                const int lc = half * (kBN / 2) + c * 32, c0 = k.tj * kBN + lc;
-                if (c0 >= I.cols || row0 >= I.out) break;            // uniform over the warp
-                float gn = 1.f, sh = 0.f;
-                if (I.splits == 1 && c0 + lane < I.cols) {
-                    if (I.gain) gn = ld_elem(I.gain, c0 + lane, p.w_dt);
-                    if (I.shift) sh = ld_elem(I.shift, c0 + lane, p.w_dt);
-                }
-                float v[32];
-                tmem_ld_32x32b_x32(tmem_base + ((uint32_t)(quad * 32) << 16) + (uint32_t)(buf * kBN + lc), v);
-                if (I.splits == 1) {
-                    finish32(I, p.w_dt, row, c0, gn, sh, v);
-                } else if (row < I.out) {
-                    float* dst = I.part + ((long long)k.split * I.out + row) * I.ldp + c0;
+            for (int c = 0; c < MH * (kBN / 64); ++c) {
+                // a warp's lanes, and every other 32-column chunk of an MMA's columns; a thread has four rows
+                // (row0 + lane / 4 + 8 u) of one group of eight columns (convert32), four lanes 64 bytes or more of a row
+                const int h = c / (kBN / 64), lc = (2 * (c % (kBN / 64)) + half) * 32, c0 = k.tj * kBN + lc;
+                const int row0 = (k.ti * MH + h) * 2 * kBM + (int)rank * kBM + quad * 32;
+                if (c0 >= cols || row0 >= out) continue;             // uniform over the warp
+                const int col = c0 + (lane & 3) * 8, nv = max(0, min(8, (whole ? cols : (int)ld) - col));
+                const bool vec = wide && nv == 8;
+                float v[32], gn[8], sh[8];
+                if (gain) load8_dt(gain, col, WDT, vec, nv, gn);
+                if (shift) load8_dt(shift, col, WDT, false, nv, sh);
+                tmem_ld_16x256b_x4_twice(tmem_base + ((uint32_t)(quad * 32) << 16) + (uint32_t)((buf + h) * kBN + lc), v);
 #pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        if (c0 + 4 * i < I.ldp)
-                            reinterpret_cast<float4*>(dst)[i] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+                for (int u = 0; u < 4; ++u) {
+                    const int row = row0 + 8 * u + (lane >> 2), z = 16 * (u >> 1) + 2 * (u & 1);
+                    float x[8] = {v[z], v[z + 4], v[z + 1], v[z + 5], v[z + 8], v[z + 12], v[z + 9], v[z + 13]};
+                    if (row >= out) continue;
+                    const long long at = row * ld + col;
+                    if (gain)
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) x[i] *= gn[i];
+                    if (shift) {
+                        const float d = dy_sum[row];
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) x[i] = fmaf(d, sh[i], x[i]);
+                    }
+                    if (beta != 0.f) {
+                        float b[8];
+                        load8_dt(base, at, WDT, vec, nv, b);
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) x[i] = fmaf(beta, b[i], x[i]);
+                    }
+                    if (whole) store8_dt(base, at, WDT, vec, nv, x);
+                    else store8_dt(base, at, DT_FP32, vec, nv, x);
                 }
             }
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(&tempty_bar[buf]), 0));
+            // only this warp's accumulator reads have to be over, not its stores
+            if (lane == 0) mbar_arrive_cluster_cta(mapa_shared(smem_u32(&tempty_bar[buf]), 0));
         }
     } else if (warp < 2 + kEpiWarps + kConvWarps) {
         // ---------------------------------------------------- converters
-        // Groups of kGroupWarps warps take k-blocks in turn.  A k-block is converted in registers before its operand
-        // stage is waited for, so a stage is only held for the stores and the MMAs.
-        const int cw = warp - 2 - kEpiWarps, group = cw / kGroupWarps;
-        const int tid = (cw % kGroupWarps) * 32 + lane;
-        constexpr int kTokStep = kGroupWarps * 4;
-        const int piece = tid & 7, tok0 = tid >> 3;         // 16 columns, tokens tok0 + kTokStep i of a k-block
-        // The two 16-byte pieces of 16 columns in a 64-column box: row = token, pieces XORed with the token's low bits.
-        // Threads of the second box store their upper piece first: the eight pieces that go out together then
-        // cover the eight bank groups.
-        const int pc = (piece & 3) * 2, at = (piece >> 2) * (64 * kBK * 2) + tok0 * 128;
-        const bool swap = piece >= 4;
-        const int at0 = at + (((pc + swap) ^ (tok0 & 7)) << 4), at1 = at + (((pc + !swap) ^ (tok0 & 7)) << 4);
-        uint32_t n = 0;                                     // k-blocks of this CTA before this work item
+        // Groups of kGroupWarps warps take k-blocks in turn, as many groups as operand stages, so that a group always
+        // fills the same one.  A k-block is converted in registers before its stage is waited for: the stage is only
+        // held for the stores and the MMAs.
+        const int cw = warp - 2 - kEpiWarps, group = cw / kGroupWarps, sub = cw % kGroupWarps;
+        constexpr int kTokStep = 64 / kTokens;
+        // a warp: two blocks (one 64-column box of the operand), tokens tok0 + kTokStep i
+        // Lanes 8 i .. 8 i + 7 hold both blocks of tokens 0, 1, 6, 7 (or 2, 3, 4, 5) of eight: their 16-byte loads of codes
+        // (row = token, pieces XORed with the token's low bits: pieces {0, 2} ^ token) and their 16-byte stores
+        // (pieces {0, 4} ^ token) each cover the eight bank groups.
+        const int box = sub & 1, blk = lane & 1, tl = (lane >> 1) & 3;
+        const int tok0 = (sub >> 1) * 16 + (lane >> 4) * 8 + ((tl < 2 ? tl : tl + 4) ^ ((lane >> 2) & 2)), x = tok0 & 7;
+        const int at = kBOffset + group * kBBytes + box * (64 * kBK * 2) + tok0 * 128;
+        const int codes_at = tok0 * 128, codes0 = ((box * 4 + blk * 2) ^ x) << 4, codes1 = ((box * 4 + blk * 2 + 1) ^ x) << 4;
+        uint32_t rs = group, rphase = 0;                    // raw stage of the group's next k-block
+        uint32_t ds = (group + kAStages - kBStages) % kAStages, dphase = 1;     // done barrier of the one kBStages before it
+        uint32_t n = 0, j = group;                          // k-blocks of this CTA before this work item; the group's next
         bool ok = true;
         for (long long w = unit; ok && w < p.works; w += nunits) {
             const Work k = decode_work(p, w);
             const GradItem& I = p.it[k.item];
-            const uint32_t kb0 = (uint32_t)(k.split * I.len), len = (uint32_t)min(I.total, (k.split + 1) * I.len) - kb0;
-            const uint32_t elde = (uint32_t)I.lde & 3u;
-            const uint32_t ebase = (uint32_t)reinterpret_cast<uintptr_t>(I.e) + (uint32_t)(k.tj * (kBN / kActBlock)) +
-                                   rank * (kBN / 2 / kActBlock);
-            for (uint32_t j = n + (group + kConvGroups - n % kConvGroups) % kConvGroups; j < n + len; j += kConvGroups) {
-                const uint32_t rs = j % kRaw, bs = j % kBStages;
-                if (!mbar_wait(&rfull_bar[rs], (j / kRaw) & 1, abort_flag, d_status)) { ok = false; break; }
-                const uint8_t* r = raw + rs * kRawBytes;
-                // byte offset of a token's first exponent in its aligned word
-                const uint32_t e0 = ebase + (uint32_t)((int)((kb0 + (j - n)) % (uint32_t)I.nkb) * kBK) * elde;
-                uint4 first[kPieces], second[kPieces];
+            n += (uint32_t)(min(I.total, (k.split + 1) * I.len) - k.split * I.len);
+            // byte offset of the tokens' first exponent in its aligned word: kTokStep and kBK are multiples of 4
+            const uint32_t off = ((uint32_t)reinterpret_cast<uintptr_t>(I.e) + (uint32_t)(k.tj * (kBN / kActBlock)) +
+                                  rank * (kBN / 2 / kActBlock) + tok0 * (uint32_t)I.lde) & 3u;
+            const int exp_at = tok0 * 8 + (int)off + box * 2 + blk;
+            for (; j < n; j += kConvGroups) {
+                if (!mbar_wait(&rfull_bar[rs], rphase, abort_flag, d_status)) { ok = false; break; }
+                const uint8_t *r = raw + rs * kRawBytes, *e = smem + kExpOffset + rs * kExpBytes;
+                uint4 o[kTokens][4];
 #pragma unroll
-                for (int i = 0; i < kPieces; ++i) {
-                    const int t = tok0 + kTokStep * i;
-                    const uint4 q = *reinterpret_cast<const uint4*>(r + t * (kBN / 2) + piece * 16);
-                    const int e = r[kRawCodes + t * 8 + ((e0 + t * elde) & 3) + (piece >> 1)];
-                    convert16<T>(swap ? make_uint4(q.z, q.w, q.x, q.y) : q, e, first[i], second[i]);
+                for (int i = 0; i < kTokens; ++i) {
+                    const uint8_t* q = r + codes_at + i * (kTokStep * 128);
+                    convert32<T>(*reinterpret_cast<const uint4*>(q + codes0), *reinterpret_cast<const uint4*>(q + codes1),
+                                 e[exp_at + i * (kTokStep * 8)], o[i]);
                 }
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&rempty_bar[rs]);
-                // the MMAs that read this operand stage last, k-block j - kBStages
-                const uint32_t last = j - kBStages;
-                if (j >= kBStages && !mbar_wait(&done_bar[last % kAStages], (last / kAStages) & 1, abort_flag, d_status)) {
-                    ok = false;
-                    break;
-                }
-                uint8_t* sb = smem + kBOffset + bs * kBBytes;
+                if ((rs += kConvGroups) >= kRaw) { rs -= kRaw; rphase ^= 1; }
+                // the MMAs that read this operand stage last (none before the group's first k-block)
+                if (j >= kBStages && !mbar_wait(&done_bar[ds], dphase, abort_flag, d_status)) { ok = false; break; }
+                if ((ds += kConvGroups) >= kAStages) { ds -= kAStages; dphase ^= 1; }
 #pragma unroll
-                for (int i = 0; i < kPieces; ++i) {
-                    *reinterpret_cast<uint4*>(sb + at0 + i * (kTokStep * 128)) = first[i];
-                    *reinterpret_cast<uint4*>(sb + at1 + i * (kTokStep * 128)) = second[i];
-                }
+                for (int i = 0; i < kTokens; ++i)
+#pragma unroll
+                    for (int g = 0; g < 4; ++g)
+                        *reinterpret_cast<uint4*>(smem + at + i * (kTokStep * 128) + (((blk * 4 + g) ^ x) << 4)) = o[i][g];
                 fence_proxy_async_smem();                   // the tensor cores read what was stored here
                 __syncwarp();
-                if (lane == 0) mbar_arrive_cluster_cta(mapa_shared(smem_u32(&bfull_bar[bs]), 0));
+                if (lane == 0) mbar_arrive_cluster_cta(mapa_shared(smem_u32(&bfull_bar[group]), 0));
             }
-            n += len;
         }
     } else {
         // ---------------------------------------------------- raw producers
@@ -438,7 +445,7 @@ __global__ void __launch_bounds__(kThreads, 1) act8_grad_kernel(const __grid_con
                 if (!ok) break;
                 uint8_t* r = raw + rs * kRawBytes;
                 if (lane == 0) {
-                    mbar_arrive_expect_tx(&rfull_bar[rs], kRawCodes);
+                    mbar_arrive_expect_tx(&rfull_bar[rs], kRawBytes);
                     tma_load_3d(&I.codes, &rfull_bar[rs], r, col, tok, 0);
                 }
                 // The aligned words that hold a token's bytes (the second only where they cross into it);
@@ -449,7 +456,7 @@ __global__ void __launch_bounds__(kThreads, 1) act8_grad_kernel(const __grid_con
                     const uintptr_t at = reinterpret_cast<uintptr_t>(src + h * half);
                     const int off = (int)(at & 3);
                     const char* word = reinterpret_cast<const char*>(in ? at - off : reinterpret_cast<uintptr_t>(I.e) & ~uintptr_t(3));
-                    uint8_t* dst = r + kRawCodes + (lane + 32 * h) * 8;
+                    uint8_t* dst = smem + kExpOffset + rs * kExpBytes + (lane + 32 * h) * 8;
                     cp_async4(dst, word, in ? 4u : 0u);
                     if (!in) cp_async4(dst + 4, word, 0u);
                     else if (off + nb > 4) cp_async4(dst + 4, word + 4, 4u);
@@ -614,6 +621,7 @@ struct Plan {
     int splits[kItems], len[kItems];
     long long copy_at[kItems], part_at[kItems];   // workspace offsets (-1: none)
     long long bytes;
+    int mh;                                       // MMAs per converted operand
 };
 
 // Ranges of tokens.  Without splits every work item is a whole sum of nkb
@@ -622,14 +630,15 @@ struct Plan {
 // and read again.  The estimate in k-blocks' time (about 0.3 us: 256 x 256 x 64
 // multiply-adds on a pair) is compared for ranges of 1/1, 1/2, ... of the longest sum.
 void plan_batch(const muon_act8_grad_item* items, int n, int dt, Plan& P) {
+    P.mh = getenv("MH") ? atoi(getenv("MH")) : 2;
     const int parts = dt == DT_FP32 ? 3 : 1;
-    const double pairs = kPlanSms / 2, kb_us = 0.3, gbs = 4e6 /* bytes per us: parts through L2 and HBM */, fixed_us = 4.0;
+    const double pairs = kPlanSms / 2, kb_us = 0.3 * P.mh, gbs = 4e6 /* bytes per us: parts through L2 and HBM */, fixed_us = 4.0;
     int total[kItems];
     long long tiles[kItems];
     int longest = 0;
     for (int i = 0; i < n; ++i) {
         total[i] = (items[i].c.rows + kBK - 1) / kBK * parts;
-        tiles[i] = (long long)((items[i].out + 2 * kBM - 1) / (2 * kBM)) * ((items[i].c.cols + kBN - 1) / kBN);
+        tiles[i] = (long long)((items[i].out + P.mh * 2 * kBM - 1) / (P.mh * 2 * kBM)) * ((items[i].c.cols + kBN - 1) / kBN);
         longest = std::max(longest, total[i]);
     }
     int best_len = std::max(1, longest);
@@ -664,9 +673,10 @@ void plan_batch(const muon_act8_grad_item* items, int n, int dt, Plan& P) {
     }
 }
 
-template <typename T>
-cudaError_t launch_grad(const GradParams& prm, cudaStream_t stream) {
-    auto kern = act8_grad_kernel<T>;
+template <typename T, int MH, int WDT>
+cudaError_t launch_one(const GradParams& prm, cudaStream_t stream) {
+    constexpr int kSmem = Cfg<MH>::kSmem;
+    auto kern = act8_grad_kernel<T, MH, WDT>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
     if (e != cudaSuccess) return e;
     int dev = 0, nsm = kPlanSms;
@@ -686,6 +696,15 @@ cudaError_t launch_grad(const GradParams& prm, cudaStream_t stream) {
     cfg.numAttrs = 1;
     e = cudaLaunchKernelEx(&cfg, kern, prm);
     return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+cudaError_t launch_grad(const GradParams& prm, int dt, int mh, cudaStream_t s) {
+#define ACT8_GRAD(T, MH)                                                            \
+    (prm.w_dt == DT_BF16   ? launch_one<T, MH, DT_BF16>(prm, s)                     \
+     : prm.w_dt == DT_FP16 ? launch_one<T, MH, DT_FP16>(prm, s) : launch_one<T, MH, DT_FP32>(prm, s))
+    if (dt == DT_FP16) return mh == 2 ? ACT8_GRAD(__half, 2) : ACT8_GRAD(__half, 1);
+    return mh == 2 ? ACT8_GRAD(__nv_bfloat16, 2) : ACT8_GRAD(__nv_bfloat16, 1);
+#undef ACT8_GRAD
 }
 
 muon_status run_batch(const muon_act8_grad_item* items, int n, int dt, int w_dt, uint8_t* ws, int* d_status,
@@ -710,7 +729,7 @@ muon_status run_batch(const muon_act8_grad_item* items, int n, int dt, int w_dt,
         I.total = I.nkb * parts;
         I.splits = P.splits[i];
         I.len = P.len[i];
-        I.tiles_m = (q.out + 2 * kBM - 1) / (2 * kBM);
+        I.tiles_m = (q.out + P.mh * 2 * kBM - 1) / (P.mh * 2 * kBM);
         I.tiles_n = (q.c.cols + kBN - 1) / kBN;
         I.begin = prm.works;
         prm.works += (long long)I.tiles_m * I.tiles_n * I.splits;
@@ -756,7 +775,7 @@ muon_status run_batch(const muon_act8_grad_item* items, int n, int dt, int w_dt,
     }
     if (prm.works > 0) {
         trace_begin(MUON_KERNEL_ACT8_GRAD, flops, stream);
-        const cudaError_t e = dt == DT_FP16 ? launch_grad<__half>(prm, stream) : launch_grad<__nv_bfloat16>(prm, stream);
+        const cudaError_t e = launch_grad(prm, dt, P.mh, stream);
         trace_end(stream);
         if (e != cudaSuccess) return MUON_ERR_CUDA;
     }

@@ -34,7 +34,7 @@ namespace tc {
 // Tensor map over `count` matrices of rows x inner 16-bit elements (gemm_tc.cu).
 bool encode_map(CUtensorMap* map, int dt, const void* base, long long inner, long long rows, long long count,
                 long long ld, long long mstride, int box_inner, int box_rows, bool swizzle = true);
-// The same over one matrix of bytes, boxes not swizzled.
+// The same over one matrix of bytes (128-byte swizzle).
 bool encode_bytes_map(CUtensorMap* map, const void* base, long long inner, long long rows, long long ld, int box_inner,
                       int box_rows);
 // tcgen05 back end for 16-bit operands (dt = DT_BF16 or DT_FP16); all ops of

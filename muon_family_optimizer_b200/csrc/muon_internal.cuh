@@ -301,6 +301,26 @@ __device__ __forceinline__ void tmem_ld_32x32b_x32(uint32_t taddr, float (&v)[32
     for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
 }
 
+// 32 lanes x 32 columns of 32-bit accumulator as 16 x 256-bit pieces: thread t of the
+// warp gets, of the rows t / 4 + 8 u (u = 0..3), the columns 8 k + 2 (t % 4) and the next
+// (k = 0..3) in v[16 (u / 2) + 4 k + 2 (u % 2)] and the one behind it.
+__device__ __forceinline__ void tmem_ld_16x256b_x4_twice(uint32_t taddr, float (&v)[32]) {
+    uint32_t r[32];
+#pragma unroll
+    for (int l = 0; l < 2; ++l)
+        asm volatile(
+            "tcgen05.ld.sync.aligned.16x256b.x4.b32 "
+            "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+            : "=r"(r[16 * l]), "=r"(r[16 * l + 1]), "=r"(r[16 * l + 2]), "=r"(r[16 * l + 3]), "=r"(r[16 * l + 4]),
+              "=r"(r[16 * l + 5]), "=r"(r[16 * l + 6]), "=r"(r[16 * l + 7]), "=r"(r[16 * l + 8]), "=r"(r[16 * l + 9]),
+              "=r"(r[16 * l + 10]), "=r"(r[16 * l + 11]), "=r"(r[16 * l + 12]), "=r"(r[16 * l + 13]),
+              "=r"(r[16 * l + 14]), "=r"(r[16 * l + 15])
+            : "r"(taddr + ((uint32_t)(16 * l) << 16)));
+    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+    for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+}
+
 // ----------------------------------------------------------------------------
 // CTA pairs (clusters of two CTAs sharing one tcgen05 MMA, cta_group::2)
 // ----------------------------------------------------------------------------
@@ -374,8 +394,9 @@ __device__ __forceinline__ bool elect_one() {
     return r != 0;
 }
 // Arrive on an mbarrier of any CTA of the cluster, releasing at CTA scope only: for
-// data that this CTA's tensor core reads after a proxy fence.  A release at cluster
-// scope waits for the SM's memory traffic, about 1300 cycles each.
+// shared memory that this CTA's tensor core reads after a proxy fence, and for
+// accumulator reads that are over.  A release at cluster scope waits for the
+// thread's stores to reach memory, 1300 cycles and more.
 __device__ __forceinline__ void mbar_arrive_cluster_cta(uint32_t bar_cluster) {
     asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar_cluster) : "memory");
 }
