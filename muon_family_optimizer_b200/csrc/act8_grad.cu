@@ -170,6 +170,48 @@ __device__ __forceinline__ void convert32(const uint4& a, const uint4& b, int by
     for (int g = 0; g < 4; ++g) o[g] = make_uint4(r[g][0], r[g][1], r[g][2], r[g][3]);
 }
 
+// gain, shift and beta on a thread's four rows (row + 8 u) of eight columns, in the
+// accumulator's register order (tmem_ld_16x256b_x4_twice, convert32).
+template <int WDT>
+__device__ __forceinline__ void edit_rows(const GradItem& I, int row, int col, bool vec, int nv, float (&v)[32]) {
+    constexpr int at[8] = {0, 4, 1, 5, 8, 12, 9, 13};
+    const int out = I.out;
+    if (I.gain) {
+        float g[8];
+        load8_dt(I.gain, col, WDT, vec, nv, g);
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[16 * (u >> 1) + 2 * (u & 1) + at[i]] *= g[i];
+    }
+    if (I.shift) {
+        float s[8];
+        load8_dt(I.shift, col, WDT, false, nv, s);
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            const float d = row + 8 * u < out ? I.dy_sum[row + 8 * u] : 0.f;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                float& x = v[16 * (u >> 1) + 2 * (u & 1) + at[i]];
+                x = fmaf(d, s[i], x);
+            }
+        }
+    }
+    const float beta = I.beta;
+    if (beta != 0.f)
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            if (row + 8 * u >= out) continue;
+            float g[8];
+            load8_dt(I.G, (long long)(row + 8 * u) * I.cols + col, WDT, vec, nv, g);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                float& x = v[16 * (u >> 1) + 2 * (u & 1) + at[i]];
+                x = fmaf(beta, g[i], x);
+            }
+        }
+}
+
 template <typename T, int MH, int WDT>
 __global__ void __launch_bounds__(kThreads, 1) act8_grad_kernel(const __grid_constant__ GradParams p) {
     using C = Cfg<MH>;
@@ -319,12 +361,12 @@ __global__ void __launch_bounds__(kThreads, 1) act8_grad_kernel(const __grid_con
             tc_fence_after();
             // the layer's fields in registers: the loop's fences would have them read again for every row
             const int out = I.out, cols = I.cols;
-            const bool whole = I.splits == 1, wide = whole ? I.vec != 0 : true;
-            const long long ld = whole ? cols : I.ldp;
-            char* const base = whole ? static_cast<char*>(I.G) : reinterpret_cast<char*>(I.part + (long long)k.split * out * ld);
-            const void *gain = whole ? I.gain : nullptr, *shift = whole ? I.shift : nullptr;
-            const float* dy_sum = I.dy_sum;
-            const float beta = whole ? I.beta : 0.f;
+            const bool whole = I.splits == 1;
+            const bool edit = whole && (I.gain || I.shift || I.beta != 0.f), wide = !whole || I.vec;
+            const int width = whole ? cols : (int)I.ldp;             // columns that are written, and the row stride
+            const int esz = whole ? (WDT == DT_FP32 ? 4 : 2) : 4;
+            char* const base = whole ? static_cast<char*>(I.G) : reinterpret_cast<char*>(I.part + (long long)k.split * out * width);
+            const long long step = 8LL * width * esz;
 #pragma unroll 1
             for (int c = 0; c < MH * (kBN / 64); ++c) {
                 // a warp's lanes, and every other 32-column chunk of an MMA's columns; a thread has four rows
@@ -332,34 +374,19 @@ __global__ void __launch_bounds__(kThreads, 1) act8_grad_kernel(const __grid_con
                 const int h = c / (kBN / 64), lc = (2 * (c % (kBN / 64)) + half) * 32, c0 = k.tj * kBN + lc;
                 const int row0 = (k.ti * MH + h) * 2 * kBM + (int)rank * kBM + quad * 32;
                 if (c0 >= cols || row0 >= out) continue;             // uniform over the warp
-                const int col = c0 + (lane & 3) * 8, nv = max(0, min(8, (whole ? cols : (int)ld) - col));
+                const int col = c0 + (lane & 3) * 8, nv = max(0, min(8, width - col)), rows = out - row0 - (lane >> 2);
                 const bool vec = wide && nv == 8;
-                float v[32], gn[8], sh[8];
-                if (gain) load8_dt(gain, col, WDT, vec, nv, gn);
-                if (shift) load8_dt(shift, col, WDT, false, nv, sh);
+                char* dst = base + ((long long)(row0 + (lane >> 2)) * width + col) * esz;
+                float v[32];
                 tmem_ld_16x256b_x4_twice(tmem_base + ((uint32_t)(quad * 32) << 16) + (uint32_t)((buf + h) * kBN + lc), v);
+                if (edit) edit_rows<WDT>(I, row0 + (lane >> 2), col, vec, nv, v);
 #pragma unroll
-                for (int u = 0; u < 4; ++u) {
-                    const int row = row0 + 8 * u + (lane >> 2), z = 16 * (u >> 1) + 2 * (u & 1);
-                    float x[8] = {v[z], v[z + 4], v[z + 1], v[z + 5], v[z + 8], v[z + 12], v[z + 9], v[z + 13]};
-                    if (row >= out) continue;
-                    const long long at = row * ld + col;
-                    if (gain)
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) x[i] *= gn[i];
-                    if (shift) {
-                        const float d = dy_sum[row];
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) x[i] = fmaf(d, sh[i], x[i]);
-                    }
-                    if (beta != 0.f) {
-                        float b[8];
-                        load8_dt(base, at, WDT, vec, nv, b);
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) x[i] = fmaf(beta, b[i], x[i]);
-                    }
-                    if (whole) store8_dt(base, at, WDT, vec, nv, x);
-                    else store8_dt(base, at, DT_FP32, vec, nv, x);
+                for (int u = 0; u < 4; ++u, dst += step) {
+                    const int z = 16 * (u >> 1) + 2 * (u & 1);
+                    const float x[8] = {v[z], v[z + 4], v[z + 1], v[z + 5], v[z + 8], v[z + 12], v[z + 9], v[z + 13]};
+                    if (8 * u >= rows) continue;
+                    if (whole) store8_dt(dst, 0, WDT, vec, nv, x);
+                    else store8_dt(dst, 0, DT_FP32, vec, nv, x);
                 }
             }
             tc_fence_before();
