@@ -384,7 +384,7 @@ typedef struct {
 /* Bytes of workspace act8_grad_batched needs for these items (pointers are
  * only inspected for their alignment). */
 MUON_API muon_status act8_grad_workspace_size(const muon_act8_grad_item* items, int n, muon_dtype dy_dtype,
-                                              size_t* bytes);
+                                              muon_dtype w_dtype, size_t* bytes);
 
 /*
  * The gradients of n layers (any mix of shapes; two items may share a

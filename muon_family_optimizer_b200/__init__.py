@@ -203,7 +203,8 @@ def lib():
         L.act8_decode_batched.restype = st
         L.act8_decode_batched.argtypes = [ctypes.POINTER(Act8Item), ctypes.c_int, ctypes.c_int, vp]
         L.act8_grad_workspace_size.restype = st
-        L.act8_grad_workspace_size.argtypes = [ctypes.POINTER(Act8GradItem), ctypes.c_int, ctypes.c_int, sz]
+        L.act8_grad_workspace_size.argtypes = [ctypes.POINTER(Act8GradItem), ctypes.c_int, ctypes.c_int, ctypes.c_int,
+                                               sz]
         L.act8_grad_batched.restype = st
         L.act8_grad_batched.argtypes = [ctypes.POINTER(Act8GradItem), ctypes.c_int, ctypes.c_int, ctypes.c_int, vp,
                                         ctypes.c_size_t, vp, vp]
@@ -565,7 +566,7 @@ def act8_grad_workspace_size(items):
     """Workspace bytes of act8_grad_batched for these items."""
     arr = items if isinstance(items, ctypes.Array) else make_act8_grads(items)
     out = ctypes.c_size_t(0)
-    _check(lib().act8_grad_workspace_size(arr, len(arr), arr.dy_dtype, ctypes.byref(out)),
+    _check(lib().act8_grad_workspace_size(arr, len(arr), arr.dy_dtype, arr.w_dtype, ctypes.byref(out)),
            "act8_grad_workspace_size")
     return out.value
 

@@ -70,39 +70,52 @@ struct GradItem {
     long long lde;
     int rows, cols, out;
     int nkb;                            // k-blocks of one part
-    int splits, len;                    // ranges of tokens, k-blocks (over all parts) of one range
     int total;                          // nkb * parts
+    int whole, tail;                    // tiles summed by one work item; tiles whose tokens are split into ranges
+    int splits, len;                    // ranges of a tail tile (0: no tokens), k-blocks (over all parts) of one
     int tiles_m, tiles_n;
-    long long begin;                    // first entry of the work list
+    long long begin, tail_begin;        // first entries of the work list
     void* G;
     const void *gain, *shift;
     const float* dy_sum;
     float beta;
     int vec;                            // G (and gain) rows may be accessed in 16-byte pieces
-    float* part;                        // splits != 1: [splits][out][ldp] fp32
-    long long ldp;
+    float* part;                        // [splits][tail][256 MH][256] fp32
 };
 
 struct GradParams {
     GradItem it[kItems];
     int n, w_dt;
-    long long works;
+    long long whole_works, works;       // whole tiles of every layer, then the ranges of the tail tiles
     int* d_status;
 };
 
 struct Work {
-    int item, split, ti, tj;
+    int item, ti, tj;
+    int kb0, kb1;                       // k-blocks
+    int slot;                           // -1: a whole tile; else its part's place
 };
 
 __device__ __forceinline__ Work decode_work(const GradParams& p, long long w) {
     Work k;
     k.item = 0;
-    while (k.item + 1 < p.n && w >= p.it[k.item + 1].begin) ++k.item;
+    int r;
+    if (w < p.whole_works) {
+        while (k.item + 1 < p.n && w >= p.it[k.item + 1].begin) ++k.item;
+        r = (int)(w - p.it[k.item].begin);
+        k.slot = -1;
+        k.kb0 = 0;
+        k.kb1 = p.it[k.item].total;
+    } else {
+        while (k.item + 1 < p.n && w >= p.it[k.item + 1].tail_begin) ++k.item;
+        const GradItem& I = p.it[k.item];
+        k.slot = (int)(w - I.tail_begin);
+        const int split = k.slot / I.tail;
+        r = I.whole + k.slot - split * I.tail;
+        k.kb0 = split * I.len;
+        k.kb1 = min(I.total, k.kb0 + I.len);
+    }
     const GradItem& I = p.it[k.item];
-    const int tiles = I.tiles_m * I.tiles_n;
-    const long long local = w - I.begin;
-    k.split = (int)(local / tiles);
-    const int r = (int)(local - (long long)k.split * tiles);
     const int g = r / (kGroup * I.tiles_n);                 // tile rows in groups: concurrent tiles form a block
     const int gm = min(kGroup, I.tiles_m - g * kGroup);
     const int in = r - g * kGroup * I.tiles_n;
@@ -274,8 +287,7 @@ __global__ void __launch_bounds__(kThreads, 1) act8_grad_kernel(const __grid_con
                 const Work k = decode_work(p, w);
                 const GradItem& I = p.it[k.item];
                 const int col = k.ti * MH * 2 * kBM + (int)rank * kBM;
-                const int kb1 = min(I.total, (k.split + 1) * I.len);
-                for (int kb = k.split * I.len; kb < kb1; ++kb) {
+                for (int kb = k.kb0; kb < k.kb1; ++kb) {
                     if (!mbar_wait(&done_bar[stage], phase ^ 1, abort_flag, d_status)) break;
                     uint8_t* sa = smem + stage * kABytes;
                     if (rank == 0) mbar_arrive_expect_tx(&afull_bar[stage], 2 * kABytes);
@@ -308,14 +320,12 @@ __global__ void __launch_bounds__(kThreads, 1) act8_grad_kernel(const __grid_con
             bool ok = true;
             for (long long w = unit; ok && w < p.works; w += nunits, ++it) {
                 const Work k = decode_work(p, w);
-                const GradItem& I = p.it[k.item];
                 const int buf = it % kBufs;
                 ok = __all_sync(0xFFFFFFFFu, mbar_wait(&tempty_bar[buf], ((it / kBufs) & 1) ^ 1, abort_flag, d_status));
                 if (!ok) break;
                 tc_fence_after();
                 const uint32_t d_tmem = tmem_base + (uint32_t)(buf * kBN);
-                const int len = min(I.total - k.split * I.len, I.len);
-                for (int kb = 0; kb < len; ++kb) {
+                for (int kb = k.kb0; kb < k.kb1; ++kb) {
                     bool ready = mbar_try_wait(&afull_bar[as], aphase) && mbar_try_wait(&bfull_bar[bs], bphase);
                     if (!__all_sync(0xFFFFFFFFu, ready)) {
                         ready = mbar_wait(&afull_bar[as], aphase, abort_flag, d_status) &&
@@ -331,7 +341,7 @@ __global__ void __launch_bounds__(kThreads, 1) act8_grad_kernel(const __grid_con
 #pragma unroll
                             for (int h = 0; h < MH; ++h)
                                 tc_mma_f16_pair(d_tmem + h * kBN, da + (h * kBM * kBK * 2 >> 4) + s * (2048 >> 4),
-                                                db + s * (2048 >> 4), idesc, kb > 0 || s > 0 ? 1u : 0u);
+                                                db + s * (2048 >> 4), idesc, kb > k.kb0 || s > 0 ? 1u : 0u);
                         tc_commit_pair_multicast(smem_u32(&done_bar[as]), 3);
                     }
                     __syncwarp();
@@ -351,7 +361,7 @@ __global__ void __launch_bounds__(kThreads, 1) act8_grad_kernel(const __grid_con
         }
     } else if (warp < 2 + kEpiWarps) {
         // ---------------------------------------------------- epilogue
-        const int quad = warp & 3, half = (warp - 2) >> 2;
+        const int quad = warp & 3, part = (warp - 2) >> 2;
         int it = 0;
         for (long long w = unit; w < p.works; w += nunits, ++it) {
             const Work k = decode_work(p, w);
@@ -361,25 +371,27 @@ __global__ void __launch_bounds__(kThreads, 1) act8_grad_kernel(const __grid_con
             tc_fence_after();
             // the layer's fields in registers: the loop's fences would have them read again for every row
             const int out = I.out, cols = I.cols;
-            const bool whole = I.splits == 1;
+            const bool whole = k.slot < 0;
             const bool edit = whole && (I.gain || I.shift || I.beta != 0.f), wide = !whole || I.vec;
-            const int width = whole ? cols : (int)I.ldp;             // columns that are written, and the row stride
-            const int esz = whole ? (WDT == DT_FP32 ? 4 : 2) : 4;
-            char* const base = whole ? static_cast<char*>(I.G) : reinterpret_cast<char*>(I.part + (long long)k.split * out * width);
+            // G, or the part's own 256 MH x 256 tile
+            const int width = whole ? cols : kBN, esz = whole ? (WDT == DT_FP32 ? 4 : 2) : 4;
+            const int row_at = whole ? k.ti * MH * 2 * kBM : 0, col_at = whole ? k.tj * kBN : 0;
+            char* const base = whole ? static_cast<char*>(I.G)
+                                     : reinterpret_cast<char*>(I.part + (long long)k.slot * (MH * 2 * kBM * kBN));
             const long long step = 8LL * width * esz;
 #pragma unroll 1
-            for (int c = 0; c < MH * (kBN / 64); ++c) {
-                // a warp's lanes, and every other 32-column chunk of an MMA's columns; a thread has four rows
-                // (row0 + lane / 4 + 8 u) of one group of eight columns (convert32), four lanes 64 bytes or more of a row
-                const int h = c / (kBN / 64), lc = (2 * (c % (kBN / 64)) + half) * 32, c0 = k.tj * kBN + lc;
-                const int row0 = (k.ti * MH + h) * 2 * kBM + (int)rank * kBM + quad * 32;
+            for (int c = part; c < MH * (kBN / 32); c += kEpiWarps / 4) {
+                // 32 rows and 32 columns; a thread has four rows (row0 + lane / 4 + 8 u) of one group of eight columns
+                // (convert32), four lanes 64 bytes or more of a row
+                const int h = c / (kBN / 32), lc = c % (kBN / 32) * 32, c0 = k.tj * kBN + lc;
+                const int lr = h * 2 * kBM + (int)rank * kBM + quad * 32, row0 = k.ti * MH * 2 * kBM + lr;
                 if (c0 >= cols || row0 >= out) continue;             // uniform over the warp
-                const int col = c0 + (lane & 3) * 8, nv = max(0, min(8, width - col)), rows = out - row0 - (lane >> 2);
+                const int rows = out - row0 - (lane >> 2), nv = whole ? max(0, min(8, cols - c0 - (lane & 3) * 8)) : 8;
                 const bool vec = wide && nv == 8;
-                char* dst = base + ((long long)(row0 + (lane >> 2)) * width + col) * esz;
+                char* dst = base + ((long long)(row_at + lr + (lane >> 2)) * width + col_at + lc + (lane & 3) * 8) * esz;
                 float v[32];
                 tmem_ld_16x256b_x4_twice(tmem_base + ((uint32_t)(quad * 32) << 16) + (uint32_t)((buf + h) * kBN + lc), v);
-                if (edit) edit_rows<WDT>(I, row0 + (lane >> 2), col, vec, nv, v);
+                if (edit) edit_rows<WDT>(I, row0 + (lane >> 2), c0 + (lane & 3) * 8, vec, nv, v);
 #pragma unroll
                 for (int u = 0; u < 4; ++u, dst += step) {
                     const int z = 16 * (u >> 1) + 2 * (u & 1);
@@ -416,7 +428,7 @@ __global__ void __launch_bounds__(kThreads, 1) act8_grad_kernel(const __grid_con
         for (long long w = unit; ok && w < p.works; w += nunits) {
             const Work k = decode_work(p, w);
             const GradItem& I = p.it[k.item];
-            n += (uint32_t)(min(I.total, (k.split + 1) * I.len) - k.split * I.len);
+            n += (uint32_t)(k.kb1 - k.kb0);
             // byte offset of the tokens' first exponent in its aligned word: kTokStep and kBK are multiples of 4
             const uint32_t off = ((uint32_t)reinterpret_cast<uintptr_t>(I.e) + (uint32_t)(k.tj * (kBN / kActBlock)) +
                                   rank * (kBN / 2 / kActBlock) + tok0 * (uint32_t)I.lde) & 3u;
@@ -459,8 +471,8 @@ __global__ void __launch_bounds__(kThreads, 1) act8_grad_kernel(const __grid_con
             const GradItem& I = p.it[k.item];
             const int col = k.tj * kBN + (int)rank * (kBN / 2), b0 = col / kActBlock;
             const int nb = min(4, act8_blocks(I.cols) - b0);            // exponent bytes of a token, if any
-            const int kb0 = k.split * I.len;
-            const uint32_t len = (uint32_t)(min(I.total, kb0 + I.len) - kb0);
+            const int kb0 = k.kb0;
+            const uint32_t len = (uint32_t)(k.kb1 - kb0);
             uint32_t j = n + (mine + kRawWarps - n % kRawWarps) % kRawWarps;
             int tok = ((kb0 + (int)(j - n)) % I.nkb) * kBK;
             const unsigned char* src = I.e + (long long)(tok + lane) * I.lde + b0;
@@ -577,46 +589,67 @@ __global__ void __launch_bounds__(256) act8_copy_kernel(const __grid_constant__ 
     }
 }
 
-// G from the parts of the token ranges (none: no tokens), added in order.
-__global__ void __launch_bounds__(256) act8_join_kernel(const __grid_constant__ GradParams p) {
+// G of the tail tiles from the parts of their token ranges (none: no tokens), added in
+// order.  A warp takes a row of a tile: eight columns per lane where G's rows allow
+// 16-byte accesses, else every 32nd column, so that its accesses stay together.
+__global__ void __launch_bounds__(256) act8_join_kernel(const __grid_constant__ GradParams p, int tile_rows) {
+    const int lane = threadIdx.x & 31;
+    const long long nwarps = (long long)gridDim.x * 8;
     for (int i = 0; i < p.n; ++i) {
         const GradItem& I = p.it[i];
-        if (I.splits == 1) continue;
-        const int segs = (I.cols + 7) / 8;
-        const long long units = (long long)I.out * segs;
-        for (long long u = (long long)blockIdx.x * blockDim.x + threadIdx.x; u < units;
-             u += (long long)gridDim.x * blockDim.x) {
-            const long long row = u / segs;
-            const int col = (int)(u - row * segs) * 8;
-            const int nv = min(8, I.cols - col);
-            const bool vec = I.vec && nv == 8;
-            float s[8] = {};
-            const float* src = I.part + row * I.ldp + col;
-            const long long step = (long long)I.out * I.ldp;
+        const long long tile_size = (long long)tile_rows * kBN, step = I.tail * tile_size;
+        const int w_dt = p.w_dt;
+        for (long long u = (long long)blockIdx.x * 8 + (threadIdx.x >> 5); u < (long long)I.tail * tile_rows; u += nwarps) {
+            const int t = (int)(u / tile_rows), lr = (int)(u - (long long)t * tile_rows), r = I.whole + t;
+            const int g = r / (kGroup * I.tiles_n), gm = min(kGroup, I.tiles_m - g * kGroup), in = r - g * kGroup * I.tiles_n;
+            const int row = (g * kGroup + in % gm) * tile_rows + lr, col0 = in / gm * kBN;
+            if (row >= I.out) continue;
+            const float* src = I.part + t * tile_size + (long long)lr * kBN;
+            const float d = I.shift ? I.dy_sum[row] : 0.f;
+            const long long at = (long long)row * I.cols;
+            if (I.vec) {
+                const int col = col0 + lane * 8;
+                if (col >= I.cols) continue;
+                float s[8] = {};
 #pragma unroll 4
-            for (int k = 0; k < I.splits; ++k) {
-                const float4 a = *reinterpret_cast<const float4*>(src + k * step);
-                const float4 b = *reinterpret_cast<const float4*>(src + k * step + 4);
-                s[0] += a.x; s[1] += a.y; s[2] += a.z; s[3] += a.w;
-                s[4] += b.x; s[5] += b.y; s[6] += b.z; s[7] += b.w;
-            }
-            float g[8];
-            if (I.gain) {
-                load8_dt(I.gain, col, p.w_dt, vec, nv, g);
+                for (int k = 0; k < I.splits; ++k) {
+                    const float4 a = *reinterpret_cast<const float4*>(src + k * step + lane * 8);
+                    const float4 b = *reinterpret_cast<const float4*>(src + k * step + lane * 8 + 4);
+                    s[0] += a.x; s[1] += a.y; s[2] += a.z; s[3] += a.w;
+                    s[4] += b.x; s[5] += b.y; s[6] += b.z; s[7] += b.w;
+                }
+                float g8[8];
+                if (I.gain) {
+                    load8_dt(I.gain, col, w_dt, true, 8, g8);
 #pragma unroll
-                for (int j = 0; j < 8; ++j) s[j] *= g[j];
-            }
-            if (I.shift) {
-                const float d = I.dy_sum[row];
+                    for (int j = 0; j < 8; ++j) s[j] *= g8[j];
+                }
+                if (I.shift)
 #pragma unroll
-                for (int j = 0; j < 8; ++j) s[j] = fmaf(d, j < nv ? ld_elem(I.shift, col + j, p.w_dt) : 0.f, s[j]);
-            }
-            if (I.beta != 0.f) {
-                load8_dt(I.G, row * I.cols + col, p.w_dt, vec, nv, g);
+                    for (int j = 0; j < 8; ++j) s[j] = fmaf(d, ld_elem(I.shift, col + j, w_dt), s[j]);
+                if (I.beta != 0.f) {
+                    load8_dt(I.G, at + col, w_dt, true, 8, g8);
 #pragma unroll
-                for (int j = 0; j < 8; ++j) s[j] = fmaf(I.beta, g[j], s[j]);
+                    for (int j = 0; j < 8; ++j) s[j] = fmaf(I.beta, g8[j], s[j]);
+                }
+                store8_dt(I.G, at + col, w_dt, true, 8, s);
+            } else {
+                float s[8] = {};
+#pragma unroll 2
+                for (int k = 0; k < I.splits; ++k)
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) s[j] += src[k * step + j * 32 + lane];
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const int col = col0 + j * 32 + lane;
+                    if (col >= I.cols) continue;
+                    float x = s[j];
+                    if (I.gain) x *= ld_elem(I.gain, col, w_dt);
+                    if (I.shift) x = fmaf(d, ld_elem(I.shift, col, w_dt), x);
+                    if (I.beta != 0.f) x = fmaf(I.beta, ld_elem(I.G, at + col, w_dt), x);
+                    st_elem(I.G, at + col, w_dt, x);
+                }
             }
-            store8_dt(I.G, row * I.cols + col, p.w_dt, vec, nv, s);
         }
     }
 }
@@ -644,58 +677,76 @@ bool direct(const muon_act8_grad_item& q, int dt) {
     return dt != DT_FP32 && rows_aligned(q.dY, q.lddy, 2) && q.lddy < (1LL << 38);
 }
 
+// Whether G's rows (and the gain) can be accessed in 16-byte pieces.
+bool aligned_G(const muon_act8_grad_item& q, int w_dt) {
+    return rows_aligned(q.G, q.c.cols, dt_size(w_dt)) && (reinterpret_cast<uintptr_t>(q.gain) & 15) == 0;
+}
+
 struct Plan {
-    int splits[kItems], len[kItems];
+    int mh;                                       // MMAs that share a converted operand: tiles of 256 mh x 256
+    int whole[kItems], tail[kItems], splits[kItems], len;
     long long copy_at[kItems], part_at[kItems];   // workspace offsets (-1: none)
     long long bytes;
-    int mh;                                       // MMAs per converted operand
 };
 
-// Ranges of tokens.  Without splits every work item is a whole sum of nkb
-// k-blocks and the pairs run ceil(tiles / pairs) rounds of them; with ranges of
-// `len` k-blocks the rounds are shorter and fuller, for fp32 parts that are written
-// and read again.  The estimate in k-blocks' time (about 0.3 us: 256 x 256 x 64
-// multiply-adds on a pair) is compared for ranges of 1/1, 1/2, ... of the longest sum.
-void plan_batch(const muon_act8_grad_item* items, int n, int dt, Plan& P) {
-    P.mh = getenv("MH") ? atoi(getenv("MH")) : 2;
+// The work list.  A pair that sums a whole tile takes nkb k-blocks; the tiles run in
+// rounds of 74 pairs, and a last round that is not full (or a call with fewer tiles
+// than pairs) leaves pairs idle.  The tiles of that round can be split into ranges of
+// tokens, shorter and fuller rounds, for fp32 parts that are written and read
+// again.  Both tile sizes and every number of ranges are compared by these
+// times, measured at 4096 x 4096 over 8192 tokens and 14336 x 4096 over 2048: a k-block 0.73 us with two
+// MMAs per operand, 0.48 us with one (whose operand traffic per MMA is the higher), 2 us
+// and 1 us per tile around its sum, parts through L2 at 3 TB/s and 4 us for the second launch.
+// G whose rows cannot be written in 16-byte pieces always goes through parts: its stores are then
+// whole rows of lanes instead of single elements 16 bytes apart (1000 x 777 over 300 tokens 59 us without).
+void plan_batch(const muon_act8_grad_item* items, int n, int dt, int w_dt, Plan& P) {
     const int parts = dt == DT_FP32 ? 3 : 1;
-    const double pairs = kPlanSms / 2, kb_us = 0.3 * P.mh, gbs = 4e6 /* bytes per us: parts through L2 and HBM */, fixed_us = 4.0;
-    int total[kItems];
-    long long tiles[kItems];
-    int longest = 0;
+    const long long pairs = kPlanSms / 2;
+    bool any_unaligned = false;
+    int total[kItems], longest = 0;
     for (int i = 0; i < n; ++i) {
         total[i] = (items[i].c.rows + kBK - 1) / kBK * parts;
-        tiles[i] = (long long)((items[i].out + P.mh * 2 * kBM - 1) / (P.mh * 2 * kBM)) * ((items[i].c.cols + kBN - 1) / kBN);
         longest = std::max(longest, total[i]);
+        any_unaligned |= !aligned_G(items[i], w_dt);
     }
-    int best_len = std::max(1, longest);
     double best = -1.0;
-    for (int s = 1; s <= 74 && s <= longest; ++s) {
-        const int len = (longest + s - 1) / s;
-        double works = 0.0, bytes = 0.0;
-        for (int i = 0; i < n; ++i) {
-            const int k = (total[i] + len - 1) / len;
-            works += (double)tiles[i] * k;
-            if (k > 1) bytes += 8.0 * k * items[i].out * items[i].c.cols;
-        }
-        const double us = std::ceil(works / pairs) * len * kb_us + (bytes > 0 ? bytes / gbs + fixed_us : 0.0);
-        if (best < 0.0 || us < best) {
-            best = us;
-            best_len = len;
+    long long best_whole = 0;
+    int best_s = 1;
+    P.mh = 2;
+    for (int mh = 1; mh <= 2; ++mh) {
+        long long tiles = 0;
+        for (int i = 0; i < n; ++i)
+            tiles += (long long)((items[i].out + mh * 2 * kBM - 1) / (mh * 2 * kBM)) * ((items[i].c.cols + kBN - 1) / kBN);
+        const double kb_us = mh == 2 ? 0.73 : 0.48, tile_us = mh, part_us = mh * 4.0 * 2 * kBM * kBN * 2 / 3e6;
+        for (int s = 1; s <= (int)pairs && s <= std::max(1, longest); ++s) {
+            const int len = std::max(1, (longest + s - 1) / s);
+            long long whole = s == 1 ? tiles : tiles / pairs * pairs;
+            if (any_unaligned) whole = 0;
+            const long long tail = tiles - whole;
+            const double us = std::ceil((double)whole / pairs) * (longest * kb_us + tile_us) +
+                              (tail ? std::ceil((double)(tail * s) / pairs) * (len * kb_us + tile_us) + tail * s * part_us + 4.0 : 0.0);
+            if (best < 0.0 || us < best) {
+                best = us; best_whole = whole; best_s = s; P.mh = mh;
+            }
         }
     }
+    P.len = std::max(1, (longest + best_s - 1) / best_s);
     P.bytes = 0;
     for (int i = 0; i < n; ++i) {
-        P.len[i] = best_len;
-        P.splits[i] = (total[i] + best_len - 1) / best_len;
+        const long long tiles = (long long)((items[i].out + P.mh * 2 * kBM - 1) / (P.mh * 2 * kBM)) *
+                                ((items[i].c.cols + kBN - 1) / kBN);
+        P.whole[i] = total[i] == 0 ? 0 : (int)std::min(tiles, best_whole);
+        P.tail[i] = (int)(tiles - P.whole[i]);
+        best_whole -= std::min(tiles, best_whole);
+        P.splits[i] = (total[i] + P.len - 1) / P.len;
         P.copy_at[i] = P.part_at[i] = -1;
         if (items[i].c.rows > 0 && !direct(items[i], dt)) {
             P.copy_at[i] = P.bytes;
             P.bytes += align256(2LL * parts * items[i].c.rows * ((items[i].out + 7) / 8 * 8));
         }
-        if (P.splits[i] > 1) {
+        if (P.tail[i] > 0 && P.splits[i] > 0) {
             P.part_at[i] = P.bytes;
-            P.bytes += align256(4LL * P.splits[i] * items[i].out * ((items[i].c.cols + 7) / 8 * 8));
+            P.bytes += 4LL * P.splits[i] * P.tail[i] * P.mh * 2 * kBM * kBN;
         }
     }
 }
@@ -741,7 +792,7 @@ muon_status run_batch(const muon_act8_grad_item* items, int n, int dt, int w_dt,
     static std::mutex mu;
     std::lock_guard<std::mutex> lock(mu);
     Plan P;
-    plan_batch(items, n, dt, P);
+    plan_batch(items, n, dt, w_dt, P);
     memset(&prm, 0, sizeof(prm));
     memset(&cp, 0, sizeof(cp));
     const int parts = dt == DT_FP32 ? 3 : 1;
@@ -754,18 +805,19 @@ muon_status run_batch(const muon_act8_grad_item* items, int n, int dt, int w_dt,
         I.rows = q.c.rows; I.cols = q.c.cols; I.out = q.out;
         I.nkb = (q.c.rows + kBK - 1) / kBK;
         I.total = I.nkb * parts;
+        I.whole = P.whole[i];
+        I.tail = P.tail[i];
         I.splits = P.splits[i];
-        I.len = P.len[i];
+        I.len = P.len;
         I.tiles_m = (q.out + P.mh * 2 * kBM - 1) / (P.mh * 2 * kBM);
         I.tiles_n = (q.c.cols + kBN - 1) / kBN;
-        I.begin = prm.works;
-        prm.works += (long long)I.tiles_m * I.tiles_n * I.splits;
+        I.begin = prm.whole_works;
+        prm.whole_works += I.whole;
         I.G = q.G; I.gain = q.gain; I.shift = q.shift; I.dy_sum = q.dy_sum; I.beta = q.beta;
-        I.vec = rows_aligned(q.G, q.c.cols, dt_size(w_dt)) && (reinterpret_cast<uintptr_t>(q.gain) & 15) == 0;
-        I.ldp = (q.c.cols + 7) / 8 * 8;
+        I.vec = aligned_G(q, w_dt);
         I.part = P.part_at[i] < 0 ? nullptr : reinterpret_cast<float*>(ws + P.part_at[i]);
-        join |= I.splits != 1;
-        if (I.splits != 1) join_bytes += (double)q.out * q.c.cols * (4.0 * I.splits + dt_size(w_dt));
+        join |= I.tail > 0;
+        join_bytes += (double)I.tail * P.mh * 2 * kBM * kBN * (4.0 * I.splits + dt_size(w_dt));
         if (q.c.rows == 0) continue;
         flops += 2.0 * q.c.rows * q.out * q.c.cols;
         const void* base = q.dY;
@@ -785,6 +837,11 @@ muon_status run_batch(const muon_act8_grad_item* items, int n, int dt, int w_dt,
                             parts == 1 ? ld : stride, 64, kBK) ||
             !tc::encode_bytes_map(&I.codes, q.c.q, q.c.cols, q.c.rows, q.c.ldq, kBN / 2, kBK))
             return MUON_ERR_CUDA;
+    }
+    prm.works = prm.whole_works;
+    for (int i = 0; i < n; ++i) {
+        prm.it[i].tail_begin = prm.works;
+        prm.works += (long long)prm.it[i].tail * prm.it[i].splits;
     }
     prm.n = n;
     prm.w_dt = w_dt;
@@ -808,18 +865,18 @@ muon_status run_batch(const muon_act8_grad_item* items, int n, int dt, int w_dt,
     }
     if (join) {
         trace_begin(MUON_KERNEL_ACT8, join_bytes, stream);
-        act8_join_kernel<<<nsm * 4, 256, 0, stream>>>(prm);
+        act8_join_kernel<<<nsm * 4, 256, 0, stream>>>(prm, P.mh * 2 * kBM);
         trace_end(stream);
         if (cudaGetLastError() != cudaSuccess) return MUON_ERR_CUDA;
     }
     return MUON_OK;
 }
 
-size_t workspace_bytes(const muon_act8_grad_item* items, int n, int dt) {
+size_t workspace_bytes(const muon_act8_grad_item* items, int n, int dt, int w_dt) {
     long long most = 0;
     Plan P;
     for (int b = 0; b < n; b += kItems) {
-        plan_batch(items + b, std::min(kItems, n - b), dt, P);
+        plan_batch(items + b, std::min(kItems, n - b), dt, w_dt, P);
         most = std::max(most, P.bytes);
     }
     return (size_t)most;
@@ -832,11 +889,12 @@ using namespace muon;
 
 extern "C" {
 
-muon_status act8_grad_workspace_size(const muon_act8_grad_item* items, int n, muon_dtype dy_dtype, size_t* bytes) {
-    if (!bytes || !valid(dy_dtype)) return MUON_ERR_INVALID_ARG;
+muon_status act8_grad_workspace_size(const muon_act8_grad_item* items, int n, muon_dtype dy_dtype, muon_dtype w_dtype,
+                                     size_t* bytes) {
+    if (!bytes || !valid(dy_dtype) || !valid(w_dtype)) return MUON_ERR_INVALID_ARG;
     const muon_status st = check_items(items, n);
     if (st != MUON_OK) return st;
-    *bytes = workspace_bytes(items, n, dy_dtype);
+    *bytes = workspace_bytes(items, n, dy_dtype, w_dtype);
     return MUON_OK;
 }
 
@@ -845,7 +903,7 @@ muon_status act8_grad_batched(const muon_act8_grad_item* items, int n, muon_dtyp
     if (!valid(dy_dtype) || !valid(w_dtype)) return MUON_ERR_INVALID_ARG;
     muon_status st = check_items(items, n);
     if (st != MUON_OK) return st;
-    const size_t need = workspace_bytes(items, n, dy_dtype);
+    const size_t need = workspace_bytes(items, n, dy_dtype, w_dtype);
     if (need && (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255) || ws_bytes < need))
         return MUON_ERR_WORKSPACE;
     st = check_device();

@@ -82,17 +82,18 @@ def _grad(**kw):
 def test_grad_refusals(L, bad):
     arr = (mo.Act8GradItem * 2)(_grad(), _grad(**bad))
     out = ctypes.c_size_t(7)
-    assert L.act8_grad_workspace_size(arr, 2, mo.BF16, ctypes.byref(out)) == mo.ERR_INVALID_ARG
+    assert L.act8_grad_workspace_size(arr, 2, mo.BF16, mo.BF16, ctypes.byref(out)) == mo.ERR_INVALID_ARG
     assert L.act8_grad_batched(arr, 2, mo.BF16, mo.BF16, P, 1 << 40, None, None) == mo.ERR_INVALID_ARG
 
 
 def test_grad_refusals_of_the_call(L):
     arr = (mo.Act8GradItem * 1)(_grad())
     out = ctypes.c_size_t(0)
-    assert L.act8_grad_workspace_size(arr, 1, 3, ctypes.byref(out)) == mo.ERR_INVALID_ARG
-    assert L.act8_grad_workspace_size(arr, 1, mo.BF16, None) == mo.ERR_INVALID_ARG
-    assert L.act8_grad_workspace_size(arr, 0, mo.BF16, ctypes.byref(out)) == mo.ERR_INVALID_ARG
-    assert L.act8_grad_workspace_size(None, 1, mo.BF16, ctypes.byref(out)) == mo.ERR_INVALID_ARG
+    assert L.act8_grad_workspace_size(arr, 1, 3, mo.BF16, ctypes.byref(out)) == mo.ERR_INVALID_ARG
+    assert L.act8_grad_workspace_size(arr, 1, mo.BF16, 3, ctypes.byref(out)) == mo.ERR_INVALID_ARG
+    assert L.act8_grad_workspace_size(arr, 1, mo.BF16, mo.BF16, None) == mo.ERR_INVALID_ARG
+    assert L.act8_grad_workspace_size(arr, 0, mo.BF16, mo.BF16, ctypes.byref(out)) == mo.ERR_INVALID_ARG
+    assert L.act8_grad_workspace_size(None, 1, mo.BF16, mo.BF16, ctypes.byref(out)) == mo.ERR_INVALID_ARG
     assert L.act8_grad_batched(arr, 1, 3, mo.BF16, None, 0, None, None) == mo.ERR_INVALID_ARG
     assert L.act8_grad_batched(arr, 1, mo.BF16, 5, None, 0, None, None) == mo.ERR_INVALID_ARG
 
