@@ -2,9 +2,10 @@
 // format).
 //
 // Both passes are bound by HBM: 2 + 1 + 1/32 bytes per element for 16-bit
-// data.  A warp takes four rows of a 256-column segment, eight columns per lane
-// (16-byte loads of 16-bit data, 8-byte accesses of codes), every load issued
-// before any use; a block's four lanes find its exponent with two shuffles.
+// data.  A warp takes a segment of up to 256 columns of eight rows (of more rows where
+// they are shorter), eight columns per lane (16-byte accesses of 16-bit data, 8-byte
+// accesses of codes), every load issued before any use; a block's four lanes find its
+// exponent with two shuffles.
 #include <algorithm>
 #include <cstring>
 #include <mutex>
@@ -17,67 +18,145 @@ namespace muon {
 namespace {
 
 constexpr int kMaxItems = 64;
-constexpr int kRowsPerUnit = 4;     // rows a warp has in flight
-constexpr int kSegCols = 256;       // columns a warp covers
+constexpr int kRowsPerUnit = 8;     // rows a warp has in flight
 
 struct Item {
     const signed char* q;
     const unsigned char* e;
     const void* x;
-    long long ldq, lde, ldx, unit_begin;
-    int rows, cols, segs, vec;
+    long long ldq, lde, ldx;
+    uint32_t unit_begin, segs;
+    int rows, cols, vec, lanes_log;
 };
 
 struct ItemParams {
     Item it[kMaxItems];
     int n;
-    long long units;
+    uint32_t units;
     int* d_status;
 };
 
+// Rows of x that cannot be taken in whole 16-byte pieces.  Encoding, a lane loads its
+// eight columns one by one (the codes' rows are aligned all the same); decoding, it
+// takes one column of every block, so that the warp's stores are whole runs of 32
+// (eight single stores per lane, 16 bytes apart, took 2.1 times as long at 16384 x 1003).
+template <int DT>
+__device__ __forceinline__ bool encode_row(const char* x, signed char* q, unsigned char* e, int col, int cols, int lane) {
+    const int nv = min(8, max(0, cols - col));
+    float v[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = i < nv ? ld_elem(x, col + i, DT) : 0.f;
+    return act8_encode8(v, col, nv, q, e, lane);
+}
+
+template <int DT>
+__device__ __forceinline__ void decode_row(char* x, const signed char* q, const unsigned char* e, int col, int cols) {
+    int code[8], byte[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const int c = col + i * 32;
+        code[i] = c < cols ? q[c] : 0;
+        byte[i] = c < cols ? e[c / kActBlock] : 0;
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        if (col + i * 32 < cols)
+            st_elem(x, col + i * 32, DT,
+                    (float)code[i] * (byte[i] == kActBad ? __uint_as_float(0x7FC00000u) : act8_scale(byte[i])));
+}
+
 template <int DT, bool ENCODE>
-__global__ void __launch_bounds__(256) act8_kernel(const __grid_constant__ ItemParams p) {
+__global__ void __launch_bounds__(256, DT != DT_FP32 ? 4 : ENCODE ? 2 : 3) act8_kernel(const __grid_constant__ ItemParams p) {
+    constexpr int esz = DT == DT_FP32 ? 4 : 2;
     const int lane = threadIdx.x & 31;
-    const long long nwarps = (long long)gridDim.x * (blockDim.x >> 5);
+    const uint32_t nwarps = gridDim.x * (blockDim.x >> 5);
     int ei = 0;
     bool bad = false;
-    for (long long u = (long long)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5); u < p.units; u += nwarps) {
+    for (uint32_t u = blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5); u < p.units; u += nwarps) {
         while (ei + 1 < p.n && u >= p.it[ei + 1].unit_begin) ++ei;
         const Item& I = p.it[ei];
-        const long long local = u - I.unit_begin;
-        const long long rg = local / I.segs;
-        const int col = (int)(local - rg * I.segs) * kSegCols + lane * 8;
-        const int row0 = (int)(rg * kRowsPerUnit);
-        const int nvalid = min(8, max(0, I.cols - col));
-        const bool vec = I.vec && nvalid == 8;
-        if (ENCODE) {
-            float x[kRowsPerUnit][8];
-#pragma unroll
-            for (int r = 0; r < kRowsPerUnit; ++r)
-                load8_dt(I.x, (row0 + r) * I.ldx + col, DT, vec && row0 + r < I.rows,
-                         row0 + r < I.rows ? nvalid : 0, x[r]);
-#pragma unroll
+        const uint32_t local = u - I.unit_begin, rg = local / I.segs, seg = local - rg * I.segs;
+        char* x = static_cast<char*>(const_cast<void*>(I.x));
+        signed char* q = const_cast<signed char*>(I.q);
+        unsigned char* e = const_cast<unsigned char*>(I.e);
+        if (!I.vec) {
+#pragma unroll 4
             for (int r = 0; r < kRowsPerUnit; ++r) {
-                const long long row = row0 + r;
-                bad |= !act8_encode8(x[r], col, row < I.rows ? nvalid : 0, const_cast<signed char*>(I.q) + row * I.ldq,
-                                     const_cast<unsigned char*>(I.e) + row * I.lde, lane);
+                const long long row = (long long)rg * kRowsPerUnit + r;
+                if (row >= I.rows) break;
+                if (ENCODE)
+                    bad |= !encode_row<DT>(x + row * I.ldx * esz, q + row * I.ldq, e + row * I.lde, (int)seg * 256 + lane * 8,
+                                           I.cols, lane);
+                else
+                    decode_row<DT>(x + row * I.ldx * esz, q + row * I.ldq, e + row * I.lde, (int)seg * 256 + lane, I.cols);
+            }
+            continue;
+        }
+        // 2^lanes_log lanes per row; kRowsPerUnit rows per lane, 32 >> lanes_log apart
+        const int apart = 32 >> I.lanes_log, col = (int)((seg << I.lanes_log) + (lane & ((1 << I.lanes_log) - 1))) * 8;
+        const long long row0 = (long long)rg * (kRowsPerUnit * apart) + (lane >> I.lanes_log);
+        const int rows = (int)min((long long)kRowsPerUnit, (I.rows - row0 + apart - 1) / apart);     // of this lane; may be 0
+        const bool in = col < I.cols;                          // eight columns or none
+        x += (row0 * I.ldx + col) * esz;
+        q += row0 * I.ldq + col;
+        e += row0 * I.lde + col / kActBlock;
+        const long long xstep = apart * I.ldx * esz, qstep = apart * I.ldq, estep = apart * I.lde;
+        if (ENCODE) {
+            Raw8<DT> raw[kRowsPerUnit];
+#pragma unroll
+            for (int r = 0; r < kRowsPerUnit; ++r, x += xstep) raw[r].load(x, in && r < rows);
+#pragma unroll
+            for (int r = 0; r < kRowsPerUnit; ++r, q += qstep, e += estep) {
+                float v[8];
+                uint2 w;
+                raw[r].get(v);
+                const int byte = act8_quantise8(v, w);
+                if (in && r < rows) {
+                    *reinterpret_cast<uint2*>(q) = w;
+                    if ((lane & 3) == 0) *e = (unsigned char)byte;
+                }
+                bad |= byte == kActBad;
             }
         } else {
+            // fp32: two runs of four columns per lane, so that a warp's 16-byte stores leave no gaps
+            constexpr int kRuns = DT == DT_FP32 ? 2 : 1;
+            const int sub = lane & ((1 << I.lanes_log) - 1);
             uint2 w[kRowsPerUnit];
-            int b[kRowsPerUnit];
+            int b[kRowsPerUnit][kRuns];
+            int c0 = 0, c1 = 0;                                // columns of the runs, from `col` on
+            if (DT == DT_FP32) {
+                c0 = -4 * sub;
+                c1 = c0 + (4 << I.lanes_log);
+            }
+            const bool in0 = col + c0 < I.cols, in1 = col + c1 < I.cols;
+            const int e0 = (col + c0) / kActBlock - col / kActBlock, e1 = (col + c1) / kActBlock - col / kActBlock;
 #pragma unroll
-            for (int r = 0; r < kRowsPerUnit; ++r) {
-                const long long row = row0 + r;
-                const int nv = row < I.rows ? nvalid : 0;
-                w[r] = act8_load8(I.q + row * I.ldq, col, nv);
-                b[r] = nv > 0 ? I.e[row * I.lde + col / kActBlock] : 0;
+            for (int r = 0; r < kRowsPerUnit; ++r, q += qstep, e += estep) {
+                const bool ok = in0 && r < rows, ok1 = in1 && r < rows;
+                if constexpr (DT == DT_FP32) {
+                    w[r].x = ok ? *reinterpret_cast<const uint32_t*>(q + c0) : 0u;
+                    w[r].y = ok1 ? *reinterpret_cast<const uint32_t*>(q + c1) : 0u;
+                    b[r][1] = ok1 ? e[e1] : 0;
+                } else {
+                    w[r] = ok ? *reinterpret_cast<const uint2*>(q) : make_uint2(0u, 0u);
+                }
+                b[r][0] = ok ? e[e0] : 0;
             }
 #pragma unroll
-            for (int r = 0; r < kRowsPerUnit; ++r) {
+            for (int r = 0; r < kRowsPerUnit; ++r, x += xstep) {
                 float v[8];
-                act8_decode8(w[r], b[r], v);
-                store8_dt(const_cast<void*>(I.x), (row0 + r) * I.ldx + col, DT, vec && row0 + r < I.rows,
-                          row0 + r < I.rows ? nvalid : 0, v);
+                if constexpr (DT == DT_FP32) {
+                    float u[8];
+                    act8_decode8(w[r], b[r][0], v);
+                    act8_decode8(w[r], b[r][1], u);
+                    if (in0 && r < rows) reinterpret_cast<float4*>(x + c0 * esz)[0] = make_float4(v[0], v[1], v[2], v[3]);
+                    if (in1 && r < rows) reinterpret_cast<float4*>(x + c1 * esz)[0] = make_float4(u[4], u[5], u[6], u[7]);
+                } else {
+                    Raw8<DT> o;
+                    act8_decode8(w[r], b[r][0], v);
+                    o.set(v);
+                    o.store(x, in && r < rows);
+                }
             }
         }
     }
@@ -106,10 +185,16 @@ muon_status run_items(const muon_act8_item* items, int n, int dt, int* d_status,
             I.q = q.c.q; I.e = q.c.e; I.x = q.x;
             I.ldq = q.c.ldq; I.lde = q.c.lde; I.ldx = q.ldx;
             I.rows = q.c.rows; I.cols = q.c.cols;
-            I.segs = (q.c.cols + kSegCols - 1) / kSegCols;
-            I.vec = rows_aligned(q.x, q.ldx, dt_size(dt));
+            I.vec = rows_aligned(q.x, q.ldx, dt_size(dt)) && q.c.cols % 8 == 0;
+            // lanes of a row: a warp over one row of 256 columns or more, over several shorter ones
+            I.lanes_log = 5;
+            while (I.vec && I.lanes_log > 2 && (8 << (I.lanes_log - 1)) >= q.c.cols) --I.lanes_log;
+            I.segs = (uint32_t)((q.c.cols + (8 << I.lanes_log) - 1) / (8 << I.lanes_log));
+            const int unit_rows = kRowsPerUnit * (32 >> I.lanes_log);
             I.unit_begin = prm.units;
-            prm.units += (long long)I.segs * ((q.c.rows + kRowsPerUnit - 1) / kRowsPerUnit);
+            const unsigned long long u = prm.units + (unsigned long long)I.segs * (((unsigned long long)q.c.rows + unit_rows - 1) / unit_rows);
+            if (u > 0x7FFFFFFFu) return MUON_ERR_UNSUPPORTED;      // over 2^41 elements
+            prm.units = (uint32_t)u;
             bytes += (double)q.c.rows * (q.c.cols * (dt_size(dt) + 1.0) + act8_blocks(q.c.cols));
         }
         if (prm.n == 0) continue;
@@ -117,7 +202,7 @@ muon_status run_items(const muon_act8_item* items, int n, int dt, int* d_status,
         int dev = 0, nsm = 148;
         cudaGetDevice(&dev);
         cudaDeviceGetAttribute(&nsm, cudaDevAttrMultiProcessorCount, dev);
-        const int grid = (int)std::min<long long>((prm.units + 7) / 8, (long long)nsm * 8);
+        const int grid = (int)std::min<long long>((prm.units + 7) / 8, (long long)nsm * 16);
         trace_begin(MUON_KERNEL_ACT8, bytes, stream);
         if (dt == DT_BF16) act8_kernel<DT_BF16, ENCODE><<<grid, 256, 0, stream>>>(prm);
         else if (dt == DT_FP16) act8_kernel<DT_FP16, ENCODE><<<grid, 256, 0, stream>>>(prm);

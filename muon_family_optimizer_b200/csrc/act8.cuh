@@ -21,9 +21,6 @@ constexpr int kActBad = 255;        // exponent byte of a block that stands for 
 
 __host__ __device__ inline int act8_blocks(int cols) { return (cols + kActBlock - 1) / kActBlock; }
 
-// |x| as bits: unsigned integer order is magnitude order, with NaNs above infinity.
-__device__ __forceinline__ uint32_t abs_bits(float x) { return __float_as_uint(x) & 0x7FFFFFFFu; }
-
 // Exponent byte of a block whose largest magnitude has the bits m: with
 // max = f 2^E (1 <= f < 2), 127 2^(E-6) = (127/64) 2^E holds it unless f > 127/64.
 __device__ __forceinline__ int act8_exp_byte(uint32_t m) {
@@ -45,26 +42,90 @@ __device__ __forceinline__ uint32_t act8_codes4(float a, float b, float c, float
     return __byte_perm(__byte_perm(ua, ub, 0x0040), __byte_perm(uc, ud, 0x0040), 0x5410);
 }
 
-// Eight columns col..col+7 of one row (col a multiple of 8; values past the row
-// given as 0), the block's four lanes in step: the block's exponent by two
-// shuffles (every lane of the warp takes part), the codes as two words, and by
-// the block's first lane the exponent byte.  Returns false for a block that
-// cannot be held.
+// Eight consecutive elements as they lie in memory (16-byte aligned): loaded without
+// a branch (zeros where not `ok`), so that loads can be in flight together, and
+// turned into floats where they are used.
+template <int DT> struct Raw8 {
+    static constexpr int N = DT == DT_FP32 ? 2 : 1;
+    uint4 w[N];
+    __device__ __forceinline__ void load(const void* p, bool ok) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) w[i] = ok ? static_cast<const uint4*>(p)[i] : make_uint4(0u, 0u, 0u, 0u);
+    }
+    __device__ __forceinline__ void get(float (&v)[8]) const {
+        if constexpr (DT == DT_FP32) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                v[4 * i] = __uint_as_float(w[i].x); v[4 * i + 1] = __uint_as_float(w[i].y);
+                v[4 * i + 2] = __uint_as_float(w[i].z); v[4 * i + 3] = __uint_as_float(w[i].w);
+            }
+        } else {
+            const uint32_t u[4] = {w[0].x, w[0].y, w[0].z, w[0].w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                if constexpr (DT == DT_BF16) {
+                    v[2 * i] = __uint_as_float(u[i] << 16);
+                    v[2 * i + 1] = __uint_as_float(u[i] & 0xFFFF0000u);
+                } else {
+                    v[2 * i] = unpack_lo<__half>(u[i]);
+                    v[2 * i + 1] = unpack_hi<__half>(u[i]);
+                }
+            }
+        }
+    }
+    __device__ __forceinline__ void set(const float (&v)[8]) {
+        if constexpr (DT == DT_FP32) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+                w[i] = make_uint4(__float_as_uint(v[4 * i]), __float_as_uint(v[4 * i + 1]), __float_as_uint(v[4 * i + 2]),
+                                  __float_as_uint(v[4 * i + 3]));
+        } else {
+            uint32_t u[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                u[i] = DT == DT_BF16 ? pack2<__nv_bfloat16>(v[2 * i], v[2 * i + 1]) : pack2<__half>(v[2 * i], v[2 * i + 1]);
+            w[0] = make_uint4(u[0], u[1], u[2], u[3]);
+        }
+    }
+    __device__ __forceinline__ void store(void* p, bool ok) const {
+        if (ok)
+#pragma unroll
+            for (int i = 0; i < N; ++i) static_cast<uint4*>(p)[i] = w[i];
+    }
+};
+
+// max(m, |a|, |b|), NaN if any is.
+__device__ __forceinline__ float max3_abs(float m, float a, float b) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(m), "f"(fabsf(a)), "f"(fabsf(b)));
+    return r;
+}
+
+// Exponent byte and codes (two words) of eight columns of a block, its four lanes in step (every lane of
+// the warp takes part; columns past the row given as 0): the block's largest
+// magnitude by two shuffles.
+__device__ __forceinline__ int act8_quantise8(const float (&x)[8], uint2& w) {
+    float m = fabsf(x[0]);
+    m = max3_abs(m, x[1], x[2]);
+    m = max3_abs(m, x[3], x[4]);
+    m = max3_abs(m, x[5], x[6]);
+    m = max3_abs(m, x[7], x[7]);
+    m = max3_abs(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1), 0.f);
+    m = max3_abs(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2), 0.f);
+    const int byte = act8_exp_byte(__float_as_uint(m));
+    const float inv = act8_inv(byte);
+    w.x = act8_codes4(x[0], x[1], x[2], x[3], inv);
+    w.y = act8_codes4(x[4], x[5], x[6], x[7], inv);
+    if (byte == kActBad) w = make_uint2(0u, 0u);
+    return byte;
+}
+
+// The same, stored: the codes at qrow + col, and by the block's first lane the
+// exponent byte.  Returns false for a block that cannot be held.
 __device__ __forceinline__ bool act8_encode8(const float (&x)[8], int col, int nvalid, signed char* qrow,
                                              unsigned char* erow, int lane) {
-    uint32_t m = 0;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) m = max(m, abs_bits(x[i]));
-    m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
-    m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
-    const int byte = act8_exp_byte(m);
-    const bool ok = byte != kActBad;
-    uint2 w = make_uint2(0u, 0u);
-    if (ok) {
-        const float inv = act8_inv(byte);
-        w.x = act8_codes4(x[0], x[1], x[2], x[3], inv);
-        w.y = act8_codes4(x[4], x[5], x[6], x[7], inv);
-    }
+    uint2 w;
+    const int byte = act8_quantise8(x, w);
     if (nvalid >= 8) {
         *reinterpret_cast<uint2*>(qrow + col) = w;
     } else {
@@ -73,17 +134,18 @@ __device__ __forceinline__ bool act8_encode8(const float (&x)[8], int col, int n
             if (i < nvalid) qrow[col + i] = (signed char)((i < 4 ? w.x : w.y) >> (8 * (i & 3)));
     }
     if ((lane & 3) == 0 && nvalid > 0) erow[col / kActBlock] = (unsigned char)byte;
-    return ok;
+    return byte != kActBad;
 }
 
-// The values of eight codes (two words) under an exponent byte.
+// The values of eight codes (two words) under an exponent byte.  A code's byte with the
+// sign bit flipped is q + 128, as the low bits of a float 2^23 + 128 + q; the difference
+// is q and q 2^e exact (a conversion instruction per code would take four times the issue time).
 __device__ __forceinline__ void act8_decode8(uint2 w, int byte, float (&v)[8]) {
     const float s = byte == kActBad ? __uint_as_float(0x7FC00000u) : act8_scale(byte);
+    const uint32_t u[2] = {w.x ^ 0x80808080u, w.y ^ 0x80808080u};
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const int q = (int)(signed char)((i < 4 ? w.x : w.y) >> (8 * (i & 3)));
-        v[i] = (float)q * s;
-    }
+    for (int i = 0; i < 8; ++i)
+        v[i] = (__uint_as_float(__byte_perm(u[i >> 2], 0x4B000000u, 0x7440 + (i & 3))) - 8388736.f) * s;
 }
 
 // Codes col..col+7 of a row; those past the row read as 0.
