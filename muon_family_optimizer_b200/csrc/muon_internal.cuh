@@ -236,6 +236,10 @@ __device__ __forceinline__ void cp_async4(void* smem_dst, const void* gmem_src, 
     asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;"
                  ::"r"(smem_u32(smem_dst)), "l"(gmem_src), "r"(src_bytes) : "memory");
 }
+// 8-byte form.
+__device__ __forceinline__ void cp_async8(void* smem_dst, const void* gmem_src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(smem_u32(smem_dst)), "l"(gmem_src) : "memory");
+}
 // Arrive on an mbarrier (one of its expected arrivals) once this thread's earlier cp.async copies have landed.
 __device__ __forceinline__ void cp_async_mbar_arrive(uint64_t* bar) {
     asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");

@@ -3,13 +3,18 @@
 // gradients of all of it from 8-bit checkpoints of the normalised rows
 // (formulas at muon_seam and muon_seam_grad in muon.h).
 //
-// Both passes are bound by HBM.  A row lives in the registers of one group of TPR
-// threads (VPT chunks of 8 consecutive columns each), so that the two norms of a
-// seam, the second of which depends on every element the first has made, cost one
-// read of the inputs.  Sums over a row: warp shuffles, then (TPR > 32) one round
-// through shared memory, in a fixed order.  Sums over tokens (backward): every block
-// takes a run of consecutive rows, keeps its columns' sums in registers and writes
-// them once; a second launch adds the runs in order.
+// Both passes are bound by HBM.  A row lives in the registers of one block (VPT chunks
+// of 8 consecutive columns per thread), so that the two norms of a seam, the second of
+// which depends on every element the first has made, cost one read of the inputs.  Sums
+// over a row: warp shuffles, then one round through shared memory, in a fixed
+// order.  Sums over tokens (backward): every block takes a run of consecutive rows, keeps
+// its columns' sums in registers and writes them once; a second launch adds the runs in
+// order.
+//
+// Two forms of each pass.  Where every row can be read in 16-byte pieces, a block
+// has exactly the warps its rows need, and each thread copies its own pieces of the next
+// rows into shared memory (cp.async, no barrier: nobody else reads them) while it
+// works on this one.  Other rows (seam_*_any) are read element by element.
 #include <algorithm>
 #include <cmath>
 
@@ -24,6 +29,623 @@ template <typename T> struct DtOf;
 template <> struct DtOf<__nv_bfloat16> { static constexpr int v = DT_BF16; };
 template <> struct DtOf<__half> { static constexpr int v = DT_FP16; };
 template <> struct DtOf<float> { static constexpr int v = DT_FP32; };
+
+// Backward: the runs of rows.
+constexpr int kPlanSms = 148;       // runs are planned for a whole B200, so a size query needs no device
+
+enum Vec : int { V_POST_GAIN, V_POST_BIAS, V_PRE_GAIN, V_PRE_BIAS, V_COUNT };
+
+// Rows cut into runs, one per block.  A run holds whole gate groups (direct: their
+// sums are finished in the run), or lies inside one group of which `parts` runs
+// share the rows.
+struct RunPlan {
+    long long runs;
+    int run_rows;      // rows of a run
+    int parts;         // runs per gate group (0: the runs hold whole groups)
+};
+
+RunPlan plan_runs(int rows, int cols, int gate_rows, bool gate_sums) {
+    const int threads = (cols + 255) / 256 * 32, per_sm = std::max(1, std::min(16, 1024 / threads));
+    RunPlan P;
+    const long long want = (long long)kPlanSms * per_sm;
+    P.run_rows = (int)std::max<long long>(1, (rows + want - 1) / want);
+    P.parts = 0;
+    P.runs = (rows + P.run_rows - 1) / P.run_rows;
+    if (gate_sums) {
+        const long long groups = ((long long)rows + gate_rows - 1) / gate_rows;
+        if (gate_rows <= P.run_rows) {
+            P.run_rows = P.run_rows / gate_rows * gate_rows;
+            P.runs = (rows + P.run_rows - 1) / P.run_rows;
+        } else {
+            const int span = std::min(gate_rows, rows);
+            P.parts = (span + P.run_rows - 1) / P.run_rows;
+            P.run_rows = (span + P.parts - 1) / P.parts;
+            P.runs = groups * P.parts;
+        }
+    }
+    return P;
+}
+
+struct BwdParams {
+    muon_seam_grad s;
+    RunPlan plan;
+    float inv_c;
+    int w_dt, vec, wvec, gate_sums;
+    int vecs_in_smem, units;
+    float* part;           // [V_COUNT + 1][runs][cols]: sums of one run (the last: shared gate rows)
+};
+
+// ---------------------------------------------------------------------------
+// Rows in 16-byte pieces
+// ---------------------------------------------------------------------------
+
+// Sums of N values over a block of nw warps; every thread gets them.  `red`: two areas
+// of 2 x 32 floats in turn, so one barrier per call is enough; entries of warps that do
+// not exist stay 0.
+template <int N>
+__device__ __forceinline__ void block_sum(float (&v)[N], float* red, int& slot, int nw) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1)
+#pragma unroll
+        for (int k = 0; k < N; ++k) v[k] += __shfl_xor_sync(0xFFFFFFFFu, v[k], o);
+    if (nw == 1) return;
+    float* s = red + slot * 64;
+    slot ^= 1;
+    if ((threadIdx.x & 31) == 0)
+#pragma unroll
+        for (int k = 0; k < N; ++k) s[k * 32 + (threadIdx.x >> 5)] = v[k];
+    __syncthreads();
+    if (nw <= 8) {
+#pragma unroll
+        for (int k = 0; k < N; ++k) {
+            const float4 a = *reinterpret_cast<const float4*>(s + k * 32);
+            v[k] = (a.x + a.y) + (a.z + a.w);
+            if (nw > 4) {
+                const float4 b = *reinterpret_cast<const float4*>(s + k * 32 + 4);
+                v[k] += (b.x + b.y) + (b.z + b.w);
+            }
+        }
+    } else {
+#pragma unroll
+        for (int k = 0; k < N; ++k) {
+            float t = s[k * 32 + (threadIdx.x & 31)];
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) t += __shfl_xor_sync(0xFFFFFFFFu, t, o);
+            v[k] = t;
+        }
+    }
+}
+
+// Normalise the row in v (columns beyond the row hold 0 and stay 0, `in` tells them):
+// returns the reciprocal deviation.  The two-pass variance keeps rows whose mean is large
+// against their deviation exact; a sum of squares beyond fp32's range is formed again
+// at 2^-100.
+template <int VPT>
+__device__ __forceinline__ float normalise(float (&v)[VPT][8], const bool (&in)[VPT], int kind, float eps, float inv_c,
+                                           float* red, int& slot, int nw) {
+    if (kind == MUON_NORM_LAYER) {
+        float m[1] = {0.f};
+#pragma unroll
+        for (int j = 0; j < VPT; ++j)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) m[0] = fmaf(v[j][i], inv_c, m[0]);
+        block_sum<1>(m, red, slot, nw);
+#pragma unroll
+        for (int j = 0; j < VPT; ++j)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[j][i] = in[j] ? v[j][i] - m[0] : 0.f;
+    }
+    float s[1] = {0.f};
+#pragma unroll
+    for (int j = 0; j < VPT; ++j)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) s[0] = fmaf(v[j][i], v[j][i], s[0]);
+    block_sum<1>(s, red, slot, nw);
+    float r;
+    if (s[0] == __uint_as_float(0x7F800000u)) {      // uniform over the block
+        const float down = __uint_as_float((127u - 100u) << 23);
+        s[0] = 0.f;
+#pragma unroll
+        for (int j = 0; j < VPT; ++j)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) s[0] = fmaf(v[j][i] * down, v[j][i] * down, s[0]);
+        block_sum<1>(s, red, slot, nw);
+        r = __frsqrt_rn(s[0] * inv_c) * down;
+    } else {
+        r = __frsqrt_rn(fmaf(s[0], inv_c, eps));
+    }
+#pragma unroll
+    for (int j = 0; j < VPT; ++j)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[j][i] *= r;
+    return r;
+}
+
+// The gains and biases of a block's columns, in shared memory as fp32 (two planes of
+// four columns of every chunk, so that a warp's 16-byte reads leave no gaps) or, for rows whose
+// vectors do not fit, read from global memory each time.
+struct Vectors {
+    const float* sm;        // NULL: global
+    int chunks, dt;
+    __device__ __forceinline__ void get(int slot, const void* g, int col, bool in, float (&v)[8]) const {
+        if (sm) {
+            const float4 a = *reinterpret_cast<const float4*>(sm + (long long)(2 * slot) * chunks * 4 + col / 2);
+            const float4 b = *reinterpret_cast<const float4*>(sm + (long long)(2 * slot + 1) * chunks * 4 + col / 2);
+            v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+            v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+        } else {
+            load8_dt(g, col, dt, in, 0, v);
+        }
+    }
+    // fill one vector (before a barrier)
+    __device__ __forceinline__ static void fill(float* sm, int slot, const void* g, int chunks, int dt) {
+        for (int c = threadIdx.x; c < chunks; c += blockDim.x) {
+            float v[8];
+            load8_dt(g, c * 8, dt, true, 8, v);
+            *reinterpret_cast<float4*>(sm + (long long)(2 * slot) * chunks * 4 + c * 4) = make_float4(v[0], v[1], v[2], v[3]);
+            *reinterpret_cast<float4*>(sm + (long long)(2 * slot + 1) * chunks * 4 + c * 4) = make_float4(v[4], v[5], v[6], v[7]);
+        }
+    }
+};
+
+// One thread's 16-byte pieces of the next rows: stage d, unit u of the stage's units,
+// chunk j.
+template <int VPT>
+struct Ring {
+    uint8_t* base;          // this thread's first piece
+    int stride, units;      // bytes between pieces (16 x threads); units of a stage
+    __device__ __forceinline__ uint8_t* at(int d, int u, int j) const { return base + ((d * units + u) * VPT + j) * stride; }
+};
+
+// Eight elements of a thread's chunk from the ring.
+template <int DT, int VPT>
+__device__ __forceinline__ void ring_get(const Ring<VPT>& ring, int d, int u, int j, bool in, float (&v)[8]) {
+    Raw8<DT> r;
+#pragma unroll
+    for (int n = 0; n < Raw8<DT>::N; ++n)
+        r.w[n] = in ? *reinterpret_cast<const uint4*>(ring.at(d, u + n, j)) : make_uint4(0u, 0u, 0u, 0u);
+    r.get(v);
+}
+
+struct FwdParams {
+    muon_seam s;
+    float inv_c;
+    int w_dt, vec, wvec;
+    int vecs_in_smem, units;
+    int* d_status;
+};
+
+enum FwdVec : int { F_POST_GAIN, F_POST_BIAS, F_PRE_GAIN, F_PRE_BIAS, F_VECS };
+
+constexpr int kRedBytes = 512;      // block_sum's areas
+
+// D rows are in flight or at work.
+template <typename T, int VPT, int MAXT, int D>
+__global__ void __launch_bounds__(MAXT, 1024 / MAXT) seam_fwd_kernel(const __grid_constant__ FwdParams p) {
+    constexpr int DT = DtOf<T>::v;
+    constexpr int NPC = sizeof(T) == 4 ? 2 : 1;
+    extern __shared__ __align__(16) uint8_t smem[];
+    const muon_seam& S = p.s;
+    float* red = reinterpret_cast<float*>(smem);
+    float* vecs = reinterpret_cast<float*>(smem + kRedBytes);
+    const int threads = blockDim.x, nw = threads >> 5, lane = threadIdx.x & 31, chunks = S.cols / 8;
+    for (int i = threadIdx.x; i < kRedBytes / 4; i += threads) red[i] = 0.f;
+    Vectors V{p.vecs_in_smem ? vecs : nullptr, chunks, p.w_dt};
+    if (p.vecs_in_smem) {
+        if (S.post_gain) Vectors::fill(vecs, F_POST_GAIN, S.post_gain, chunks, p.w_dt);
+        if (S.post_bias) Vectors::fill(vecs, F_POST_BIAS, S.post_bias, chunks, p.w_dt);
+        if (S.pre_gain) Vectors::fill(vecs, F_PRE_GAIN, S.pre_gain, chunks, p.w_dt);
+        if (S.pre_bias) Vectors::fill(vecs, F_PRE_BIAS, S.pre_bias, chunks, p.w_dt);
+    }
+    __syncthreads();
+    const Ring<VPT> ring{smem + kRedBytes + (p.vecs_in_smem ? F_VECS * 32 * chunks : 0) + threadIdx.x * 16, threads * 16,
+                         p.units};
+    int col[VPT], vcol[VPT];        // vcol: a column that exists
+    bool in[VPT];
+#pragma unroll
+    for (int j = 0; j < VPT; ++j) {
+        col[j] = (j * threads + (int)threadIdx.x) * 8;
+        in[j] = col[j] < S.cols;
+        vcol[j] = in[j] ? col[j] : 0;
+    }
+    const int r0 = (int)((long long)S.rows * blockIdx.x / gridDim.x), r1 = (int)((long long)S.rows * (blockIdx.x + 1) / gridDim.x);
+    const bool has_f = S.f != nullptr, has_gate = S.gate != nullptr;
+    const int post = S.post, pre = S.pre;
+    const T *x = static_cast<const T*>(S.x), *f = static_cast<const T*>(S.f), *gate = static_cast<const T*>(S.gate);
+    int grow = has_gate ? r0 / S.gate_rows : 0, gleft = has_gate ? S.gate_rows - r0 % S.gate_rows : 0;   // of the next copy
+    auto copy = [&](int row, int d) {
+        if (row < r1) {
+#pragma unroll
+            for (int j = 0; j < VPT; ++j) {
+                if (!in[j]) continue;
+#pragma unroll
+                for (int n = 0; n < NPC; ++n) {
+                    const int c = col[j] + n * 4;
+                    cp_async16(ring.at(d, n, j), x + row * S.ldx + c, 16);
+                    if (has_f) cp_async16(ring.at(d, NPC + n, j), f + row * S.ldf + c, 16);
+                    if (has_gate) cp_async16(ring.at(d, 2 * NPC + n, j), gate + grow * S.ldgate + c, 16);
+                }
+            }
+            if (has_gate && --gleft == 0) {
+                ++grow;
+                gleft = S.gate_rows;
+            }
+        }
+        cp_async_commit();
+    };
+    int slot = 0, d = 0;
+    bool bad = false;
+#pragma unroll
+    for (int k = 0; k < D - 1; ++k) copy(r0 + k, k);
+    for (int row = r0; row < r1; ++row) {
+        copy(row + D - 1, d == 0 ? D - 1 : d - 1);
+        cp_async_wait<D - 1>();
+        float v[VPT][8], u[VPT][8];
+#pragma unroll
+        for (int j = 0; j < VPT; ++j) ring_get<DT, VPT>(ring, d, 0, j, in[j], v[j]);
+        if (has_f) {
+#pragma unroll
+            for (int j = 0; j < VPT; ++j) ring_get<DT, VPT>(ring, d, NPC, j, in[j], u[j]);
+            if (post != MUON_NORM_NONE) {
+                const float r = normalise<VPT>(u, in, post, S.eps, p.inv_c, red, slot, nw);
+                if (S.post_rstd && threadIdx.x == 0) S.post_rstd[row] = r;
+            }
+#pragma unroll
+            for (int j = 0; j < VPT; ++j) {
+                if (S.post_c.q) {
+                    uint2 w;
+                    const int byte = act8_quantise8(u[j], w);
+                    bad |= byte == kActBad;
+                    if (in[j]) {
+                        *reinterpret_cast<uint2*>(S.post_c.q + row * S.post_c.ldq + col[j]) = w;
+                        if ((lane & 3) == 0) S.post_c.e[row * S.post_c.lde + col[j] / kActBlock] = (unsigned char)byte;
+                    }
+                }
+                float t[8];
+                if (S.post_gain) {
+                    V.get(F_POST_GAIN, S.post_gain, vcol[j], in[j], t);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) u[j][i] *= t[i];
+                }
+                if (S.post_bias) {
+                    V.get(F_POST_BIAS, S.post_bias, vcol[j], in[j], t);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) u[j][i] += t[i];
+                }
+                if (has_gate) {
+                    ring_get<DT, VPT>(ring, d, 2 * NPC, j, in[j], t);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) u[j][i] *= t[i];
+                }
+#pragma unroll
+                for (int i = 0; i < 8; ++i) v[j][i] = fmaf(S.scale, u[j][i], S.skip * v[j][i]);
+                Raw8<DT> o;
+                o.set(v[j]);
+                o.store(static_cast<T*>(S.out) + row * S.ldout + col[j], in[j]);
+                o.get(v[j]);                    // as it was stored
+                if (!in[j])
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) v[j][i] = 0.f;
+            }
+        }
+        if (pre != MUON_NORM_NONE) {
+            const float r = normalise<VPT>(v, in, pre, S.eps, p.inv_c, red, slot, nw);
+            if (S.pre_rstd && threadIdx.x == 0) S.pre_rstd[row] = r;
+#pragma unroll
+            for (int j = 0; j < VPT; ++j) {
+                if (S.pre_c.q) {
+                    uint2 w;
+                    const int byte = act8_quantise8(v[j], w);
+                    bad |= byte == kActBad;
+                    if (in[j]) {
+                        *reinterpret_cast<uint2*>(S.pre_c.q + row * S.pre_c.ldq + col[j]) = w;
+                        if ((lane & 3) == 0) S.pre_c.e[row * S.pre_c.lde + col[j] / kActBlock] = (unsigned char)byte;
+                    }
+                }
+                float t[8];
+                if (S.pre_gain) {
+                    V.get(F_PRE_GAIN, S.pre_gain, vcol[j], in[j], t);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) v[j][i] *= t[i];
+                }
+                if (S.pre_bias) {
+                    V.get(F_PRE_BIAS, S.pre_bias, vcol[j], in[j], t);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) v[j][i] += t[i];
+                }
+                Raw8<DT> o;
+                o.set(v[j]);
+                o.store(static_cast<T*>(S.y) + row * S.ldy + col[j], in[j]);
+            }
+        }
+        d = d + 1 == D ? 0 : d + 1;
+    }
+    cp_async_wait<0>();
+    if (__any_sync(0xFFFFFFFFu, bad) && lane == 0 && p.d_status) atomicOr(p.d_status, MUON_FLAG_NONFINITE);
+}
+
+enum BwdVec : int { B_POST_GAIN, B_POST_BIAS, B_PRE_GAIN, B_VECS };
+
+template <typename T, int VPT, int MAXT, int D, bool ALL>
+__global__ void __launch_bounds__(MAXT, MAXT * VPT >= 1024 ? 1 : (ALL ? 512 : 1024) / MAXT)
+    seam_bwd_kernel(const __grid_constant__ BwdParams p) {
+    constexpr int DT = DtOf<T>::v;
+    constexpr int NPC = sizeof(T) == 4 ? 2 : 1;
+    constexpr int kDout = NPC, kCodes = 2 * NPC, kGate = 2 * NPC + 1;       // units of a stage (dy first)
+    extern __shared__ __align__(16) uint8_t smem[];
+    const muon_seam_grad& S = p.s;
+    float* red = reinterpret_cast<float*>(smem);
+    float* vecs = reinterpret_cast<float*>(smem + kRedBytes);
+    const int threads = blockDim.x, nw = threads >> 5, chunks = S.cols / 8;
+    for (int i = threadIdx.x; i < kRedBytes / 4; i += threads) red[i] = 0.f;
+    Vectors V{p.vecs_in_smem ? vecs : nullptr, chunks, p.w_dt};
+    if (p.vecs_in_smem) {
+        if (S.post_gain) Vectors::fill(vecs, B_POST_GAIN, S.post_gain, chunks, p.w_dt);
+        if (S.post_bias) Vectors::fill(vecs, B_POST_BIAS, S.post_bias, chunks, p.w_dt);
+        if (S.pre_gain) Vectors::fill(vecs, B_PRE_GAIN, S.pre_gain, chunks, p.w_dt);
+    }
+    __syncthreads();
+    const Ring<VPT> ring{smem + kRedBytes + (p.vecs_in_smem ? B_VECS * 32 * chunks : 0) + threadIdx.x * 16, threads * 16,
+                         p.units};
+    int col[VPT], vcol[VPT];
+    bool in[VPT];
+#pragma unroll
+    for (int j = 0; j < VPT; ++j) {
+        col[j] = (j * threads + (int)threadIdx.x) * 8;
+        in[j] = col[j] < S.cols;
+        vcol[j] = in[j] ? col[j] : 0;
+    }
+    int r0, r1;
+    if (p.plan.parts == 0) {
+        r0 = (int)min((long long)S.rows, (long long)blockIdx.x * p.plan.run_rows);
+        r1 = (int)min((long long)S.rows, (long long)r0 + p.plan.run_rows);
+    } else {
+        const long long g = blockIdx.x / p.plan.parts, end = min((long long)S.rows, (g + 1) * S.gate_rows);
+        r0 = (int)min(end, g * S.gate_rows + (long long)(blockIdx.x % p.plan.parts) * p.plan.run_rows);
+        r1 = (int)min(end, (long long)r0 + p.plan.run_rows);
+    }
+    const bool has_pre = S.pre != MUON_NORM_NONE, has_post = S.post != MUON_NORM_NONE, has_f = S.df != nullptr;
+    const bool has_dout = S.dout != nullptr, has_gate = S.gate != nullptr, post_c = S.post_c.q != nullptr;
+    const bool gate_sums = ALL && p.gate_sums;
+    const T *dy = static_cast<const T*>(S.dy), *dout = static_cast<const T*>(S.dout), *gate = static_cast<const T*>(S.gate);
+    const int gr = has_gate ? S.gate_rows : 1;
+    int grow = has_gate ? r0 / gr : 0, gleft = has_gate ? gr - r0 % gr : 0;         // of the next copy
+    int crow = grow, cleft = gleft;                                                // of the row at work
+    auto copy = [&](int row, int d) {
+        if (row < r1) {
+#pragma unroll
+            for (int j = 0; j < VPT; ++j) {
+                if (!in[j]) continue;
+#pragma unroll
+                for (int n = 0; n < NPC; ++n) {
+                    const int c = col[j] + n * 4;
+                    if (has_pre) cp_async16(ring.at(d, n, j), dy + row * S.lddy + c, 16);
+                    if (has_dout) cp_async16(ring.at(d, kDout + n, j), dout + row * S.lddout + c, 16);
+                    if (has_gate) cp_async16(ring.at(d, kGate + n, j), gate + grow * S.ldgate + c, 16);
+                }
+                if (has_pre) cp_async8(ring.at(d, kCodes, j), S.pre_c.q + row * S.pre_c.ldq + col[j]);
+                if (post_c) cp_async8(ring.at(d, kCodes, j) + 8, S.post_c.q + row * S.post_c.ldq + col[j]);
+            }
+            if (has_gate && --gleft == 0) {
+                ++grow;
+                gleft = gr;
+            }
+        }
+        cp_async_commit();
+    };
+    // exponent bytes and deviations of the next row
+    int ep[VPT], eq[VPT];
+    float rp = 0.f, rq = 0.f;
+    auto scalars = [&](int row) {
+        if (row >= r1) return;
+#pragma unroll
+        for (int j = 0; j < VPT; ++j) {
+            if (has_pre) ep[j] = S.pre_c.e[row * S.pre_c.lde + vcol[j] / kActBlock];
+            if (post_c) eq[j] = S.post_c.e[row * S.post_c.lde + vcol[j] / kActBlock];
+        }
+        if (has_pre) rp = S.pre_rstd[row];
+        if (has_post) rq = S.post_rstd[row];
+    };
+    auto decode = [&](int d, int half, int j, int byte, float (&n)[8]) {
+        const uint2 w = in[j] ? *reinterpret_cast<const uint2*>(ring.at(d, kCodes, j) + 8 * half) : make_uint2(0u, 0u);
+        act8_decode8(w, in[j] ? byte : 127, n);
+    };
+    float a_pg[VPT][8] = {}, a_qg[VPT][8] = {};               // d_pre_gain, d_post_gain
+    float a_pb[ALL ? VPT : 1][8] = {}, a_qb[ALL ? VPT : 1][8] = {}, a_gt[ALL ? VPT : 1][8] = {};
+    int slot = 0, d = 0;
+    scalars(r0);
+#pragma unroll
+    for (int k = 0; k < D - 1; ++k) copy(r0 + k, k);
+    for (int row = r0; row < r1; ++row) {
+        copy(row + D - 1, d == 0 ? D - 1 : d - 1);
+        cp_async_wait<D - 1>();
+        const float r_pre = rp, r_post = rq;
+        int b_pre[VPT], b_post[VPT];
+#pragma unroll
+        for (int j = 0; j < VPT; ++j) {
+            b_pre[j] = ep[j];
+            b_post[j] = eq[j];
+        }
+        scalars(row + 1);
+        float x[VPT][8];                                      // d, the gradient of x'
+#pragma unroll
+        for (int j = 0; j < VPT; ++j) {
+            if (has_dout) ring_get<DT, VPT>(ring, d, kDout, j, in[j], x[j]);
+            else
+#pragma unroll
+                for (int i = 0; i < 8; ++i) x[j][i] = 0.f;
+        }
+        if (has_pre) {
+            float g[VPT][8], n[VPT][8], sums[2] = {0.f, 0.f};
+#pragma unroll
+            for (int j = 0; j < VPT; ++j) {
+                ring_get<DT, VPT>(ring, d, 0, j, in[j], g[j]);
+                decode(d, 0, j, b_pre[j], n[j]);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    a_pg[j][i] = fmaf(g[j][i], n[j][i], a_pg[j][i]);
+                    if constexpr (ALL) a_pb[j][i] += g[j][i];
+                }
+                if (S.pre_gain) {
+                    float t[8];
+                    V.get(B_PRE_GAIN, S.pre_gain, vcol[j], in[j], t);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) g[j][i] *= t[i];
+                }
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    sums[0] = fmaf(g[j][i], n[j][i], sums[0]);
+                    sums[1] += g[j][i];
+                }
+            }
+            float s0 = 0.f, s1;
+            if (S.pre == MUON_NORM_LAYER) {
+                block_sum<2>(sums, red, slot, nw);
+                s0 = sums[1] * p.inv_c;
+                s1 = sums[0] * p.inv_c;
+            } else {
+                float one[1] = {sums[0]};
+                block_sum<1>(one, red, slot, nw);
+                s1 = one[0] * p.inv_c;
+            }
+#pragma unroll
+            for (int j = 0; j < VPT; ++j)
+#pragma unroll
+                for (int i = 0; i < 8; ++i)        // columns beyond the row stay out of the sums over it
+                    x[j][i] = in[j] ? fmaf(r_pre, fmaf(-n[j][i], s1, g[j][i] - s0), x[j][i]) : 0.f;
+        }
+        if (has_f) {
+            float n[VPT][8], h[VPT][8], sums[2] = {0.f, 0.f};
+#pragma unroll
+            for (int j = 0; j < VPT; ++j) {
+                float t[8];
+                if (post_c) decode(d, 1, j, b_post[j], n[j]);
+                else
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) n[j][i] = 0.f;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) h[j][i] = S.scale * x[j][i];
+                if (has_gate) {
+                    if (S.dgate) {
+                        float u[8];
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) u[i] = n[j][i];
+                        if (S.post_gain) {
+                            V.get(B_POST_GAIN, S.post_gain, vcol[j], in[j], t);
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) u[i] *= t[i];
+                        }
+                        if (S.post_bias) {
+                            V.get(B_POST_BIAS, S.post_bias, vcol[j], in[j], t);
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) u[i] += t[i];
+                        }
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) u[i] *= h[j][i];
+                        if (!gate_sums) {
+                            Raw8<DT> o;
+                            o.set(u);
+                            o.store(static_cast<T*>(S.dgate) + crow * S.lddgate + col[j], in[j]);
+                        }
+                        if constexpr (ALL)
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) a_gt[j][i] += u[i];
+                    }
+                    ring_get<DT, VPT>(ring, d, kGate, j, in[j], t);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) h[j][i] *= t[i];
+                }
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    a_qg[j][i] = fmaf(h[j][i], n[j][i], a_qg[j][i]);
+                    if constexpr (ALL) a_qb[j][i] += h[j][i];
+                }
+                if (S.post_gain) {
+                    V.get(B_POST_GAIN, S.post_gain, vcol[j], in[j], t);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) h[j][i] *= t[i];
+                }
+                if (has_post)
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        sums[0] = fmaf(h[j][i], n[j][i], sums[0]);
+                        sums[1] += h[j][i];
+                    }
+            }
+            if (has_post) {
+                float s0 = 0.f, s1;
+                if (S.post == MUON_NORM_LAYER) {
+                    block_sum<2>(sums, red, slot, nw);
+                    s0 = sums[1] * p.inv_c;
+                    s1 = sums[0] * p.inv_c;
+                } else {
+                    float one[1] = {sums[0]};
+                    block_sum<1>(one, red, slot, nw);
+                    s1 = one[0] * p.inv_c;
+                }
+#pragma unroll
+                for (int j = 0; j < VPT; ++j)
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) h[j][i] = r_post * fmaf(-n[j][i], s1, h[j][i] - s0);
+            }
+#pragma unroll
+            for (int j = 0; j < VPT; ++j) {
+                Raw8<DT> o;
+                o.set(h[j]);
+                o.store(static_cast<T*>(S.df) + row * S.lddf + col[j], in[j]);
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < VPT; ++j) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) x[j][i] *= S.skip;
+            Raw8<DT> o;
+            o.set(x[j]);
+            o.store(static_cast<T*>(S.dx) + row * S.lddx + col[j], in[j]);
+        }
+        if (has_gate && (--cleft == 0 || row + 1 == S.rows)) {
+            if constexpr (ALL)
+                if (gate_sums && p.plan.parts == 0)
+#pragma unroll
+                    for (int j = 0; j < VPT; ++j) {
+                        Raw8<DT> o;
+                        o.set(a_gt[j]);
+                        o.store(static_cast<T*>(S.dgate) + crow * S.lddgate + col[j], in[j]);
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) a_gt[j][i] = 0.f;
+                    }
+            ++crow;
+            cleft = gr;
+        }
+        d = d + 1 == D ? 0 : d + 1;
+    }
+    cp_async_wait<0>();
+    auto put = [&](int v, const float (&a)[8], int j) {
+        Raw8<DT_FP32> o;
+        o.set(a);
+        o.store(p.part + ((long long)v * p.plan.runs + blockIdx.x) * S.cols + col[j], in[j]);
+    };
+#pragma unroll
+    for (int j = 0; j < VPT; ++j) {
+        if (S.d_pre_gain) put(V_PRE_GAIN, a_pg[j], j);
+        if (S.d_post_gain) put(V_POST_GAIN, a_qg[j], j);
+        if constexpr (ALL) {
+            if (S.d_pre_bias) put(V_PRE_BIAS, a_pb[j], j);
+            if (S.d_post_bias) put(V_POST_BIAS, a_qb[j], j);
+            if (p.gate_sums && p.plan.parts) put(V_COUNT, a_gt[j], j);
+        }
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Any rows: element by element
+// ---------------------------------------------------------------------------
+
+__device__ __forceinline__ float round_dt(float v, int dt) {
+    if (dt == DT_BF16) return __bfloat162float(__float2bfloat16_rn(v));
+    if (dt == DT_FP16) return __half2float(__float2half_rn(v));
+    return v;
+}
 
 // Sums of N values over the TPR threads of a row; every thread gets them.  `slot`
 // alternates between two shared-memory areas, so one barrier per call is enough.
@@ -121,16 +743,8 @@ __device__ __forceinline__ void affine8(float (&v)[8], const void* gain, const v
     }
 }
 
-struct FwdParams {
-    muon_seam s;
-    float inv_c;
-    int w_dt, vec, wvec;
-    int* d_status;
-};
-
-template <typename T, int TPR, int VPT>
-__global__ void __launch_bounds__(TPR == 32 ? 128 : TPR) seam_fwd_kernel(const __grid_constant__ FwdParams p) {
-    constexpr int DT = DtOf<T>::v;
+template <int TPR, int VPT>
+__global__ void __launch_bounds__(TPR == 32 ? 128 : TPR) seam_fwd_any(const __grid_constant__ FwdParams p, int DT) {
     constexpr int RPB = TPR == 32 ? 4 : 1;
     __shared__ float red[TPR > 32 ? 4 * (TPR / 32) : 1];
     const muon_seam& S = p.s;
@@ -171,7 +785,7 @@ __global__ void __launch_bounds__(TPR == 32 ? 128 : TPR) seam_fwd_kernel(const _
                 }
 #pragma unroll
                 for (int i = 0; i < 8; ++i)
-                    x[j][i] = to_float(from_float<T>(fmaf(S.scale, u[j][i], S.skip * x[j][i])));
+                    x[j][i] = round_dt(fmaf(S.scale, u[j][i], S.skip * x[j][i]), DT);
                 if (nv[j] < 8)
 #pragma unroll
                     for (int i = 0; i < 8; ++i) x[j][i] = i < nv[j] ? x[j][i] : 0.f;
@@ -194,55 +808,8 @@ __global__ void __launch_bounds__(TPR == 32 ? 128 : TPR) seam_fwd_kernel(const _
     if (__any_sync(0xFFFFFFFFu, bad) && lane == 0 && p.d_status) atomicOr(p.d_status, MUON_FLAG_NONFINITE);
 }
 
-// ---------------------------------------------------------------------------
-// Backward
-// ---------------------------------------------------------------------------
-constexpr int kPlanSms = 148;       // runs are planned for a whole B200, so a size query needs no device
-
-enum Vec : int { V_POST_GAIN, V_POST_BIAS, V_PRE_GAIN, V_PRE_BIAS, V_COUNT };
-
-// Rows cut into runs, one per block.  A run holds whole gate groups (direct: their
-// sums are finished in the run), or lies inside one group of which `parts` runs
-// share the rows.
-struct RunPlan {
-    long long runs;
-    int run_rows;      // rows of a run
-    int parts;         // runs per gate group (0: the runs hold whole groups)
-};
-
-RunPlan plan_runs(int rows, int cols, int gate_rows, bool gate_sums) {
-    const int per_sm = cols <= 1024 ? 8 : cols <= 2048 ? 4 : cols <= 4096 ? 2 : 1;
-    RunPlan P;
-    const long long want = (long long)kPlanSms * per_sm;
-    P.run_rows = (int)std::max<long long>(1, (rows + want - 1) / want);
-    P.parts = 0;
-    P.runs = (rows + P.run_rows - 1) / P.run_rows;
-    if (gate_sums) {
-        const long long groups = ((long long)rows + gate_rows - 1) / gate_rows;
-        if (gate_rows <= P.run_rows) {
-            P.run_rows = P.run_rows / gate_rows * gate_rows;
-            P.runs = (rows + P.run_rows - 1) / P.run_rows;
-        } else {
-            const int span = std::min(gate_rows, rows);
-            P.parts = (span + P.run_rows - 1) / P.run_rows;
-            P.run_rows = (span + P.parts - 1) / P.parts;
-            P.runs = groups * P.parts;
-        }
-    }
-    return P;
-}
-
-struct BwdParams {
-    muon_seam_grad s;
-    RunPlan plan;
-    float inv_c;
-    int w_dt, vec, wvec, gate_sums;
-    float* part;           // [V_COUNT + 1][runs][cols]: sums of one run (the last: shared gate rows)
-};
-
-template <typename T, int TPR, int VPT, bool ALL>
-__global__ void __launch_bounds__(TPR) seam_bwd_kernel(const __grid_constant__ BwdParams p) {
-    constexpr int DT = DtOf<T>::v;
+template <int TPR, int VPT, bool ALL>
+__global__ void __launch_bounds__(TPR) seam_bwd_any(const __grid_constant__ BwdParams p, int DT) {
     __shared__ float red[TPR > 32 ? 4 * (TPR / 32) : 1];
     const muon_seam_grad& S = p.s;
     const int tr = threadIdx.x;
@@ -301,7 +868,8 @@ __global__ void __launch_bounds__(TPR) seam_bwd_kernel(const __grid_constant__ B
 #pragma unroll
             for (int j = 0; j < VPT; ++j)
 #pragma unroll
-                for (int i = 0; i < 8; ++i) d[j][i] = fmaf(r, fmaf(-n[j][i], s1, g[j][i] - s0), d[j][i]);
+                for (int i = 0; i < 8; ++i)        // columns beyond the row stay out of the sums over it
+                    d[j][i] = i < nv[j] ? fmaf(r, fmaf(-n[j][i], s1, g[j][i] - s0), d[j][i]) : 0.f;
         }
         if (S.df) {
             float n[VPT][8], h[VPT][8];
@@ -424,7 +992,7 @@ __global__ void __launch_bounds__(1024) seam_join_kernel(const __grid_constant__
     float s = 0.f;
     if (c < S.cols) {
         const float* src = p.part + ((long long)v * p.plan.runs + first) * S.cols + c;
-#pragma unroll 4
+#pragma unroll 8
         for (long long r = threadIdx.y; r < count; r += 32) s += src[r * S.cols];
     }
     sm[threadIdx.y][threadIdx.x] = s;
@@ -507,15 +1075,62 @@ int sm_count() {
     return nsm;
 }
 
+// Shared memory of a block whose stages hold `units` 16-byte pieces per thread and chunk, with
+// the vectors as fp32 where that leaves room for the blocks that the kernel's registers allow on
+// an SM.
+template <typename P>
+int seam_smem(P& p, int threads, int vpt, int stages, int vectors, int blocks_per_sm) {
+    const int ring = stages * p.units * vpt * threads * 16, vecs = vectors * 32 * (p.s.cols / 8);
+    const int limit = (227 * 1024 - 1024 * blocks_per_sm) / blocks_per_sm;
+    p.vecs_in_smem = kRedBytes + ring + vecs <= limit;
+    return kRedBytes + ring + (p.vecs_in_smem ? vecs : 0);
+}
+
+template <typename K, typename P>
+cudaError_t seam_launch(K kern, const P& p, unsigned grid, int threads, int smem, cudaStream_t s) {
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    kern<<<grid, threads, smem, s>>>(p);
+    return cudaGetLastError();
+}
+
+int row_threads(int cols) { return (cols + 255) / 256 * 32; }
+
 template <typename T>
-void launch_fwd(const FwdParams& p, cudaStream_t s) {
+cudaError_t launch_fwd(FwdParams& p, cudaStream_t s) {
+    const int c = p.s.cols, t = row_threads(c), npc = sizeof(T) == 4 ? 2 : 1;
+    p.units = npc * (p.s.gate ? 3 : p.s.f ? 2 : 1);
+    const int per_sm = std::max(1, std::min(32, 1024 / std::min(t, 1024)));
+    const unsigned grid = (unsigned)std::min<long long>(p.s.rows, (long long)sm_count() * per_sm);
+    if (c <= 1024) return seam_launch(seam_fwd_kernel<T, 1, 128, 3>, p, grid, t, seam_smem(p, t, 1, 3, F_VECS, per_sm), s);
+    if (c <= 4096) return seam_launch(seam_fwd_kernel<T, 1, 512, 2>, p, grid, t, seam_smem(p, t, 1, 2, F_VECS, per_sm), s);
+    if (c <= 8192) return seam_launch(seam_fwd_kernel<T, 1, 1024, 2>, p, grid, t, seam_smem(p, t, 1, 2, F_VECS, 1), s);
+    return seam_launch(seam_fwd_kernel<T, 2, 1024, 1>, p, grid, 1024, seam_smem(p, 1024, 2, 1, F_VECS, 1), s);
+}
+
+template <typename T, bool ALL>
+cudaError_t launch_bwd(BwdParams& p, cudaStream_t s) {
+    const int c = p.s.cols, t = row_threads(c), npc = sizeof(T) == 4 ? 2 : 1;
+    p.units = 2 * npc + 1 + (p.s.gate ? npc : 0);
+    const unsigned grid = (unsigned)p.plan.runs;
+    const int per_sm = std::max(1, std::min(16, 1024 / std::min(t, 1024)));
+    if (c <= 1024) return seam_launch(seam_bwd_kernel<T, 1, 128, 3, ALL>, p, grid, t, seam_smem(p, t, 1, 3, B_VECS, per_sm), s);
+    if (c <= 4096) return seam_launch(seam_bwd_kernel<T, 1, 512, 2, ALL>, p, grid, t, seam_smem(p, t, 1, 2, B_VECS, per_sm), s);
+    if (c <= 8192) {
+        const int h = (c + 511) / 512 * 32;
+        return seam_launch(seam_bwd_kernel<T, 2, 512, 2, ALL>, p, grid, h, seam_smem(p, h, 2, 2, B_VECS, 1), s);
+    }
+    return seam_launch(seam_bwd_kernel<T, 2, 1024, 1, ALL>, p, grid, 1024, seam_smem(p, 1024, 2, 1, B_VECS, 1), s);
+}
+
+cudaError_t launch_fwd_any(const FwdParams& p, int dt, cudaStream_t s) {
     const int c = p.s.cols;
 #define SEAM_FWD(TPR, VPT)                                                                              \
     do {                                                                                                \
         const int rpb = TPR == 32 ? 4 : 1, threads = TPR == 32 ? 128 : TPR;                             \
         const long long blocks = ((long long)p.s.rows + rpb - 1) / rpb;                                 \
         const int grid = (int)std::min<long long>(blocks, (long long)sm_count() * (2048 / threads));    \
-        seam_fwd_kernel<T, TPR, VPT><<<grid, threads, 0, s>>>(p);                                       \
+        seam_fwd_any<TPR, VPT><<<grid, threads, 0, s>>>(p, dt);                                         \
     } while (0)
     if (c <= 256) SEAM_FWD(32, 1);
     else if (c <= 512) SEAM_FWD(32, 2);
@@ -525,16 +1140,16 @@ void launch_fwd(const FwdParams& p, cudaStream_t s) {
     else if (c <= 8192) SEAM_FWD(512, 2);
     else SEAM_FWD(1024, 2);
 #undef SEAM_FWD
+    return cudaGetLastError();
 }
 
-template <typename T>
-void launch_bwd(const BwdParams& p, bool all, cudaStream_t s) {
+cudaError_t launch_bwd_any(const BwdParams& p, int dt, bool all, cudaStream_t s) {
     const int c = p.s.cols;
     const unsigned grid = (unsigned)p.plan.runs;
 #define SEAM_BWD(TPR, VPT)                                                       \
     do {                                                                         \
-        if (all) seam_bwd_kernel<T, TPR, VPT, true><<<grid, TPR, 0, s>>>(p);     \
-        else seam_bwd_kernel<T, TPR, VPT, false><<<grid, TPR, 0, s>>>(p);        \
+        if (all) seam_bwd_any<TPR, VPT, true><<<grid, TPR, 0, s>>>(p, dt);       \
+        else seam_bwd_any<TPR, VPT, false><<<grid, TPR, 0, s>>>(p, dt);          \
     } while (0)
     if (c <= 256) SEAM_BWD(32, 1);
     else if (c <= 512) SEAM_BWD(64, 1);
@@ -544,6 +1159,7 @@ void launch_bwd(const BwdParams& p, bool all, cudaStream_t s) {
     else if (c <= 8192) SEAM_BWD(1024, 1);
     else SEAM_BWD(1024, 2);
 #undef SEAM_BWD
+    return cudaGetLastError();
 }
 
 bool vec_ok(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
@@ -577,11 +1193,11 @@ muon_status seam_forward(const muon_seam* seam, muon_dtype x_dtype, muon_dtype w
     const double el = (double)q.rows * q.cols;
     trace_begin(MUON_KERNEL_SEAM, el * (esz * (1 + (q.f ? 2 : 0) + (q.y ? 1 : 0) + (q.gate && q.gate_rows == 1 ? 1 : 0)) +
                                         33.0 / 32 * ((q.post_c.q ? 1 : 0) + (q.pre_c.q ? 1 : 0))), s);
-    if (x_dtype == MUON_BF16) launch_fwd<__nv_bfloat16>(p, s);
-    else if (x_dtype == MUON_FP16) launch_fwd<__half>(p, s);
-    else launch_fwd<float>(p, s);
+    const cudaError_t e = !(p.vec && p.wvec && q.cols % 8 == 0) ? launch_fwd_any(p, x_dtype, s)
+                          : x_dtype == MUON_BF16 ? launch_fwd<__nv_bfloat16>(p, s)
+                          : x_dtype == MUON_FP16 ? launch_fwd<__half>(p, s) : launch_fwd<float>(p, s);
     trace_end(s);
-    return cudaGetLastError() == cudaSuccess ? MUON_OK : MUON_ERR_CUDA;
+    return e == cudaSuccess ? MUON_OK : MUON_ERR_CUDA;
 }
 
 muon_status seam_backward_workspace_size(const muon_seam_grad* seam, size_t* bytes) {
@@ -623,11 +1239,13 @@ muon_status seam_backward(const muon_seam_grad* seam, muon_dtype x_dtype, muon_d
         trace_begin(MUON_KERNEL_SEAM, (double)q.rows * q.cols *
                         (esz * (1.0 + (q.dy ? 1 : 0) + (q.dout ? 1 : 0) + (q.df ? 1 : 0) + (tok ? 1 : 0) + (tok && q.dgate ? 1 : 0)) +
                          33.0 / 32 * ((q.dy ? 1 : 0) + (q.post_c.q ? 1 : 0))), s);
-        if (x_dtype == MUON_BF16) launch_bwd<__nv_bfloat16>(p, all, s);
-        else if (x_dtype == MUON_FP16) launch_bwd<__half>(p, all, s);
-        else launch_bwd<float>(p, all, s);
+        cudaError_t e;
+        if (!(p.vec && p.wvec && q.cols % 8 == 0)) e = launch_bwd_any(p, x_dtype, all, s);
+        else if (x_dtype == MUON_BF16) e = all ? launch_bwd<__nv_bfloat16, true>(p, s) : launch_bwd<__nv_bfloat16, false>(p, s);
+        else if (x_dtype == MUON_FP16) e = all ? launch_bwd<__half, true>(p, s) : launch_bwd<__half, false>(p, s);
+        else e = all ? launch_bwd<float, true>(p, s) : launch_bwd<float, false>(p, s);
         trace_end(s);
-        if (cudaGetLastError() != cudaSuccess) return MUON_ERR_CUDA;
+        if (e != cudaSuccess) return MUON_ERR_CUDA;
     }
     const long long groups = p.gate_sums && p.plan.parts ? p.plan.runs / p.plan.parts : 0;
     if (any_vector(q) || groups) {

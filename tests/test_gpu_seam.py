@@ -293,6 +293,18 @@ def test_without_gains_and_vectors():
     _check_back(b, v)
 
 
+@pytest.mark.parametrize("C", [40, 136, 203, 1003, 4104])
+def test_layer_norms_without_gains(C):
+    # no gain to hide what a thread without columns adds to the row's sums
+    s = _build(7, C, FP, FP, "layer", "layer", 0, gain=False, bias=False)
+    mo.seam_forward(s)
+    _check_forward(s)
+    b = _back_of(s, vectors=False)
+    v = _back_inputs(b)
+    _run_back(b)
+    _check_back(b, v)
+
+
 def test_without_checkpoints_or_deviations():
     s = _build(9, 264, BF, FP, "rms", "layer", 1, keep=False)
     full = _build(9, 264, BF, FP, "rms", "layer", 1)
