@@ -150,9 +150,9 @@ __device__ __forceinline__ float normalise(float (&v)[VPT][8], const bool (&in)[
 #pragma unroll
             for (int i = 0; i < 8; ++i) s[0] = fmaf(v[j][i] * down, v[j][i] * down, s[0]);
         block_sum<1>(s, red, slot, nw);
-        r = __frsqrt_rn(s[0] * inv_c) * down;
+        r = rsqrtf(s[0] * inv_c) * down;
     } else {
-        r = __frsqrt_rn(fmaf(s[0], inv_c, eps));
+        r = rsqrtf(fmaf(s[0], inv_c, eps));
     }
 #pragma unroll
     for (int j = 0; j < VPT; ++j)
@@ -161,29 +161,40 @@ __device__ __forceinline__ float normalise(float (&v)[VPT][8], const bool (&in)[
     return r;
 }
 
-// The gains and biases of a block's columns, in shared memory as fp32 (two planes of
-// four columns of every chunk, so that a warp's 16-byte reads leave no gaps) or, for rows whose
+// A gain or bias times a constant (NULL: the constant alone, or nothing) on a thread's
+// chunks, in shared memory as fp32 (two planes of four columns of every chunk, so that a
+// warp's 16-byte reads leave no gaps; columns beyond the row hold 0) or, for rows whose
 // vectors do not fit, read from global memory each time.
 struct Vectors {
-    const float* sm;        // NULL: global
-    int chunks, dt;
-    __device__ __forceinline__ void get(int slot, const void* g, int col, bool in, float (&v)[8]) const {
+    float* sm;              // NULL: global
+    int chunks, dt;         // chunks of a vector in shared memory: those of all threads
+    __device__ __forceinline__ void get(int slot, const void* g, float mul, int col, bool in, float (&v)[8]) const {
         if (sm) {
-            const float4 a = *reinterpret_cast<const float4*>(sm + (long long)(2 * slot) * chunks * 4 + col / 2);
-            const float4 b = *reinterpret_cast<const float4*>(sm + (long long)(2 * slot + 1) * chunks * 4 + col / 2);
+            const float4 a = *reinterpret_cast<const float4*>(sm + 2 * slot * chunks * 4 + col / 2);
+            const float4 b = *reinterpret_cast<const float4*>(sm + (2 * slot + 1) * chunks * 4 + col / 2);
             v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
             v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
         } else {
-            load8_dt(g, col, dt, in, 0, v);
+            load(g, mul, col, in, v);
         }
     }
-    // fill one vector (before a barrier)
-    __device__ __forceinline__ static void fill(float* sm, int slot, const void* g, int chunks, int dt) {
+    __device__ __forceinline__ void load(const void* g, float mul, int col, bool in, float (&v)[8]) const {
+        if (g) {
+            load8_dt(g, col, dt, in, 0, v);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] *= mul;
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] = in ? mul : 0.f;
+        }
+    }
+    // fill one vector of `cols` columns (before a barrier)
+    __device__ __forceinline__ void fill(int slot, const void* g, float mul, int cols) const {
         for (int c = threadIdx.x; c < chunks; c += blockDim.x) {
             float v[8];
-            load8_dt(g, c * 8, dt, true, 8, v);
-            *reinterpret_cast<float4*>(sm + (long long)(2 * slot) * chunks * 4 + c * 4) = make_float4(v[0], v[1], v[2], v[3]);
-            *reinterpret_cast<float4*>(sm + (long long)(2 * slot + 1) * chunks * 4 + c * 4) = make_float4(v[4], v[5], v[6], v[7]);
+            load(g, mul, c * 8, c * 8 < cols, v);
+            *reinterpret_cast<float4*>(sm + 2 * slot * chunks * 4 + c * 4) = make_float4(v[0], v[1], v[2], v[3]);
+            *reinterpret_cast<float4*>(sm + (2 * slot + 1) * chunks * 4 + c * 4) = make_float4(v[4], v[5], v[6], v[7]);
         }
     }
 };
@@ -197,13 +208,13 @@ struct Ring {
     __device__ __forceinline__ uint8_t* at(int d, int u, int j) const { return base + ((d * units + u) * VPT + j) * stride; }
 };
 
-// Eight elements of a thread's chunk from the ring.
+// Eight elements of a thread's chunk from the ring (zeros for a thread without columns: it never copies, and
+// its pieces were cleared).
 template <int DT, int VPT>
-__device__ __forceinline__ void ring_get(const Ring<VPT>& ring, int d, int u, int j, bool in, float (&v)[8]) {
+__device__ __forceinline__ void ring_get(const Ring<VPT>& ring, int d, int u, int j, float (&v)[8]) {
     Raw8<DT> r;
 #pragma unroll
-    for (int n = 0; n < Raw8<DT>::N; ++n)
-        r.w[n] = in ? *reinterpret_cast<const uint4*>(ring.at(d, u + n, j)) : make_uint4(0u, 0u, 0u, 0u);
+    for (int n = 0; n < Raw8<DT>::N; ++n) r.w[n] = *reinterpret_cast<const uint4*>(ring.at(d, u + n, j));
     r.get(v);
 }
 
@@ -219,40 +230,49 @@ enum FwdVec : int { F_POST_GAIN, F_POST_BIAS, F_PRE_GAIN, F_PRE_BIAS, F_VECS };
 
 constexpr int kRedBytes = 512;      // block_sum's areas
 
-// D rows are in flight or at work.
-template <typename T, int VPT, int MAXT, int D>
-__global__ void __launch_bounds__(MAXT, 1024 / MAXT) seam_fwd_kernel(const __grid_constant__ FwdParams p) {
+// D rows are in flight or at work; MINB blocks of MAXT threads per SM bound the registers.
+template <typename T, int VPT, int MAXT, int D, int MINB>
+__global__ void __launch_bounds__(MAXT, MINB) seam_fwd_kernel(const __grid_constant__ FwdParams p) {
     constexpr int DT = DtOf<T>::v;
-    constexpr int NPC = sizeof(T) == 4 ? 2 : 1;
+    constexpr int NPC = sizeof(T) == 4 ? 2 : 1, kF = NPC, kGate = 2 * NPC;        // units of a stage (x first)
     extern __shared__ __align__(16) uint8_t smem[];
     const muon_seam& S = p.s;
     float* red = reinterpret_cast<float*>(smem);
-    float* vecs = reinterpret_cast<float*>(smem + kRedBytes);
-    const int threads = blockDim.x, nw = threads >> 5, lane = threadIdx.x & 31, chunks = S.cols / 8;
+    const int threads = blockDim.x, nw = threads >> 5, lane = threadIdx.x & 31;
+    const bool has_f = S.f != nullptr, has_gate = S.gate != nullptr, has_pb = S.post_bias != nullptr;
+    const bool has_yb = S.pre_bias != nullptr, unit_skip = S.skip == 1.f;
+    const int post = S.post, pre = S.pre;
     for (int i = threadIdx.x; i < kRedBytes / 4; i += threads) red[i] = 0.f;
-    Vectors V{p.vecs_in_smem ? vecs : nullptr, chunks, p.w_dt};
-    if (p.vecs_in_smem) {
-        if (S.post_gain) Vectors::fill(vecs, F_POST_GAIN, S.post_gain, chunks, p.w_dt);
-        if (S.post_bias) Vectors::fill(vecs, F_POST_BIAS, S.post_bias, chunks, p.w_dt);
-        if (S.pre_gain) Vectors::fill(vecs, F_PRE_GAIN, S.pre_gain, chunks, p.w_dt);
-        if (S.pre_bias) Vectors::fill(vecs, F_PRE_BIAS, S.pre_bias, chunks, p.w_dt);
+    // scale rides on the post-norm's vectors
+    const Vectors V{p.vecs_in_smem ? reinterpret_cast<float*>(smem + kRedBytes) : nullptr, threads * VPT, p.w_dt};
+    if (V.sm) {
+        V.fill(F_POST_GAIN, S.post_gain, S.scale, S.cols);
+        V.fill(F_PRE_GAIN, S.pre_gain, 1.f, S.cols);
+        if (has_pb) V.fill(F_POST_BIAS, S.post_bias, S.scale, S.cols);
+        if (has_yb) V.fill(F_PRE_BIAS, S.pre_bias, 1.f, S.cols);
     }
-    __syncthreads();
-    const Ring<VPT> ring{smem + kRedBytes + (p.vecs_in_smem ? F_VECS * 32 * chunks : 0) + threadIdx.x * 16, threads * 16,
-                         p.units};
-    int col[VPT], vcol[VPT];        // vcol: a column that exists
+    const Ring<VPT> ring{smem + kRedBytes + (V.sm ? F_VECS * 32 * V.chunks : 0) + threadIdx.x * 16, threads * 16, p.units};
+    int col[VPT];
     bool in[VPT];
 #pragma unroll
     for (int j = 0; j < VPT; ++j) {
         col[j] = (j * threads + (int)threadIdx.x) * 8;
         in[j] = col[j] < S.cols;
-        vcol[j] = in[j] ? col[j] : 0;
+        if (!in[j])
+            for (int u = 0; u < D * p.units; ++u) *reinterpret_cast<uint4*>(ring.at(0, u, j)) = make_uint4(0u, 0u, 0u, 0u);
     }
+    __syncthreads();
     const int r0 = (int)((long long)S.rows * blockIdx.x / gridDim.x), r1 = (int)((long long)S.rows * (blockIdx.x + 1) / gridDim.x);
-    const bool has_f = S.f != nullptr, has_gate = S.gate != nullptr;
-    const int post = S.post, pre = S.pre;
-    const T *x = static_cast<const T*>(S.x), *f = static_cast<const T*>(S.f), *gate = static_cast<const T*>(S.gate);
-    int grow = has_gate ? r0 / S.gate_rows : 0, gleft = has_gate ? S.gate_rows - r0 % S.gate_rows : 0;   // of the next copy
+    // this thread's first chunk of the next row to copy, and of the row at work
+    const T* x = static_cast<const T*>(S.x) + r0 * S.ldx + threadIdx.x * 8;
+    const T* f = static_cast<const T*>(S.f) + r0 * S.ldf + threadIdx.x * 8;
+    int grow = has_gate ? r0 / S.gate_rows : 0, gleft = has_gate ? S.gate_rows - r0 % S.gate_rows : 0;
+    const T* gate = static_cast<const T*>(S.gate) + grow * S.ldgate + threadIdx.x * 8;
+    T* out = static_cast<T*>(S.out) + r0 * S.ldout + threadIdx.x * 8;
+    T* y = static_cast<T*>(S.y) + r0 * S.ldy + threadIdx.x * 8;
+    signed char *pq = S.post_c.q + r0 * S.post_c.ldq + threadIdx.x * 8, *yq = S.pre_c.q + r0 * S.pre_c.ldq + threadIdx.x * 8;
+    unsigned char *pe = S.post_c.e + r0 * S.post_c.lde, *ye = S.pre_c.e + r0 * S.pre_c.lde;
+    const bool keep_f = S.post_c.q != nullptr, keep_y = S.pre_c.q != nullptr;
     auto copy = [&](int row, int d) {
         if (row < r1) {
 #pragma unroll
@@ -260,14 +280,16 @@ __global__ void __launch_bounds__(MAXT, 1024 / MAXT) seam_fwd_kernel(const __gri
                 if (!in[j]) continue;
 #pragma unroll
                 for (int n = 0; n < NPC; ++n) {
-                    const int c = col[j] + n * 4;
-                    cp_async16(ring.at(d, n, j), x + row * S.ldx + c, 16);
-                    if (has_f) cp_async16(ring.at(d, NPC + n, j), f + row * S.ldf + c, 16);
-                    if (has_gate) cp_async16(ring.at(d, 2 * NPC + n, j), gate + grow * S.ldgate + c, 16);
+                    const int c = j * threads * 8 + n * 4;
+                    cp_async16(ring.at(d, n, j), x + c, 16);
+                    if (has_f) cp_async16(ring.at(d, kF + n, j), f + c, 16);
+                    if (has_gate) cp_async16(ring.at(d, kGate + n, j), gate + c, 16);
                 }
             }
+            x += S.ldx;
+            f += S.ldf;
             if (has_gate && --gleft == 0) {
-                ++grow;
+                gate += S.ldgate;
                 gleft = S.gate_rows;
             }
         }
@@ -280,83 +302,95 @@ __global__ void __launch_bounds__(MAXT, 1024 / MAXT) seam_fwd_kernel(const __gri
     for (int row = r0; row < r1; ++row) {
         copy(row + D - 1, d == 0 ? D - 1 : d - 1);
         cp_async_wait<D - 1>();
-        float v[VPT][8], u[VPT][8];
-#pragma unroll
-        for (int j = 0; j < VPT; ++j) ring_get<DT, VPT>(ring, d, 0, j, in[j], v[j]);
+        float v[VPT][8];
         if (has_f) {
+            float u[VPT][8];
 #pragma unroll
-            for (int j = 0; j < VPT; ++j) ring_get<DT, VPT>(ring, d, NPC, j, in[j], u[j]);
+            for (int j = 0; j < VPT; ++j) ring_get<DT, VPT>(ring, d, kF, j, u[j]);
             if (post != MUON_NORM_NONE) {
                 const float r = normalise<VPT>(u, in, post, S.eps, p.inv_c, red, slot, nw);
                 if (S.post_rstd && threadIdx.x == 0) S.post_rstd[row] = r;
             }
+            if (keep_f) {
 #pragma unroll
-            for (int j = 0; j < VPT; ++j) {
-                if (S.post_c.q) {
+                for (int j = 0; j < VPT; ++j) {
                     uint2 w;
                     const int byte = act8_quantise8(u[j], w);
                     bad |= byte == kActBad;
                     if (in[j]) {
-                        *reinterpret_cast<uint2*>(S.post_c.q + row * S.post_c.ldq + col[j]) = w;
-                        if ((lane & 3) == 0) S.post_c.e[row * S.post_c.lde + col[j] / kActBlock] = (unsigned char)byte;
+                        *reinterpret_cast<uint2*>(pq + j * threads * 8) = w;
+                        if ((lane & 3) == 0) pe[col[j] / kActBlock] = (unsigned char)byte;
                     }
                 }
-                float t[8];
-                if (S.post_gain) {
-                    V.get(F_POST_GAIN, S.post_gain, vcol[j], in[j], t);
+                pq += S.post_c.ldq;
+                pe += S.post_c.lde;
+            }
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) u[j][i] *= t[i];
-                }
-                if (S.post_bias) {
-                    V.get(F_POST_BIAS, S.post_bias, vcol[j], in[j], t);
+            for (int j = 0; j < VPT; ++j) {
+                float t[8];
+                V.get(F_POST_GAIN, S.post_gain, S.scale, col[j], in[j], t);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) u[j][i] *= t[i];
+                if (has_pb) {
+                    V.get(F_POST_BIAS, S.post_bias, S.scale, col[j], in[j], t);
 #pragma unroll
                     for (int i = 0; i < 8; ++i) u[j][i] += t[i];
                 }
+                ring_get<DT, VPT>(ring, d, 0, j, v[j]);
+                if (!unit_skip)
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) v[j][i] *= S.skip;
                 if (has_gate) {
-                    ring_get<DT, VPT>(ring, d, 2 * NPC, j, in[j], t);
+                    ring_get<DT, VPT>(ring, d, kGate, j, t);
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) u[j][i] *= t[i];
+                    for (int i = 0; i < 8; ++i) v[j][i] = fmaf(u[j][i], t[i], v[j][i]);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) v[j][i] += u[j][i];
                 }
-#pragma unroll
-                for (int i = 0; i < 8; ++i) v[j][i] = fmaf(S.scale, u[j][i], S.skip * v[j][i]);
                 Raw8<DT> o;
                 o.set(v[j]);
-                o.store(static_cast<T*>(S.out) + row * S.ldout + col[j], in[j]);
+                o.store(out + j * threads * 8, in[j]);
                 o.get(v[j]);                    // as it was stored
-                if (!in[j])
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) v[j][i] = 0.f;
             }
+            out += S.ldout;
+        } else {
+#pragma unroll
+            for (int j = 0; j < VPT; ++j) ring_get<DT, VPT>(ring, d, 0, j, v[j]);
         }
         if (pre != MUON_NORM_NONE) {
             const float r = normalise<VPT>(v, in, pre, S.eps, p.inv_c, red, slot, nw);
             if (S.pre_rstd && threadIdx.x == 0) S.pre_rstd[row] = r;
+            if (keep_y) {
 #pragma unroll
-            for (int j = 0; j < VPT; ++j) {
-                if (S.pre_c.q) {
+                for (int j = 0; j < VPT; ++j) {
                     uint2 w;
                     const int byte = act8_quantise8(v[j], w);
                     bad |= byte == kActBad;
                     if (in[j]) {
-                        *reinterpret_cast<uint2*>(S.pre_c.q + row * S.pre_c.ldq + col[j]) = w;
-                        if ((lane & 3) == 0) S.pre_c.e[row * S.pre_c.lde + col[j] / kActBlock] = (unsigned char)byte;
+                        *reinterpret_cast<uint2*>(yq + j * threads * 8) = w;
+                        if ((lane & 3) == 0) ye[col[j] / kActBlock] = (unsigned char)byte;
                     }
                 }
-                float t[8];
-                if (S.pre_gain) {
-                    V.get(F_PRE_GAIN, S.pre_gain, vcol[j], in[j], t);
+                yq += S.pre_c.ldq;
+                ye += S.pre_c.lde;
+            }
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) v[j][i] *= t[i];
-                }
-                if (S.pre_bias) {
-                    V.get(F_PRE_BIAS, S.pre_bias, vcol[j], in[j], t);
+            for (int j = 0; j < VPT; ++j) {
+                float t[8];
+                V.get(F_PRE_GAIN, S.pre_gain, 1.f, col[j], in[j], t);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) v[j][i] *= t[i];
+                if (has_yb) {
+                    V.get(F_PRE_BIAS, S.pre_bias, 1.f, col[j], in[j], t);
 #pragma unroll
                     for (int i = 0; i < 8; ++i) v[j][i] += t[i];
                 }
                 Raw8<DT> o;
                 o.set(v[j]);
-                o.store(static_cast<T*>(S.y) + row * S.ldy + col[j], in[j]);
+                o.store(y + j * threads * 8, in[j]);
             }
+            y += S.ldy;
         }
         d = d + 1 == D ? 0 : d + 1;
     }
@@ -366,35 +400,38 @@ __global__ void __launch_bounds__(MAXT, 1024 / MAXT) seam_fwd_kernel(const __gri
 
 enum BwdVec : int { B_POST_GAIN, B_POST_BIAS, B_PRE_GAIN, B_VECS };
 
-template <typename T, int VPT, int MAXT, int D, bool ALL>
-__global__ void __launch_bounds__(MAXT, MAXT * VPT >= 1024 ? 1 : (ALL ? 512 : 1024) / MAXT)
-    seam_bwd_kernel(const __grid_constant__ BwdParams p) {
+template <typename T, int VPT, int MAXT, int D, int MINB, bool ALL>
+__global__ void __launch_bounds__(MAXT, MINB) seam_bwd_kernel(const __grid_constant__ BwdParams p) {
     constexpr int DT = DtOf<T>::v;
     constexpr int NPC = sizeof(T) == 4 ? 2 : 1;
     constexpr int kDout = NPC, kCodes = 2 * NPC, kGate = 2 * NPC + 1;       // units of a stage (dy first)
     extern __shared__ __align__(16) uint8_t smem[];
     const muon_seam_grad& S = p.s;
     float* red = reinterpret_cast<float*>(smem);
-    float* vecs = reinterpret_cast<float*>(smem + kRedBytes);
-    const int threads = blockDim.x, nw = threads >> 5, chunks = S.cols / 8;
+    const int threads = blockDim.x, nw = threads >> 5;
+    const bool has_pre = S.pre != MUON_NORM_NONE, has_post = S.post != MUON_NORM_NONE, has_f = S.df != nullptr;
+    const bool has_dout = S.dout != nullptr, has_gate = S.gate != nullptr, post_c = S.post_c.q != nullptr;
+    const bool has_pb = S.post_bias != nullptr, dgate = S.dgate != nullptr, gate_sums = ALL && p.gate_sums;
     for (int i = threadIdx.x; i < kRedBytes / 4; i += threads) red[i] = 0.f;
-    Vectors V{p.vecs_in_smem ? vecs : nullptr, chunks, p.w_dt};
-    if (p.vecs_in_smem) {
-        if (S.post_gain) Vectors::fill(vecs, B_POST_GAIN, S.post_gain, chunks, p.w_dt);
-        if (S.post_bias) Vectors::fill(vecs, B_POST_BIAS, S.post_bias, chunks, p.w_dt);
-        if (S.pre_gain) Vectors::fill(vecs, B_PRE_GAIN, S.pre_gain, chunks, p.w_dt);
+    // scale rides on the post-norm's vectors
+    const Vectors V{p.vecs_in_smem ? reinterpret_cast<float*>(smem + kRedBytes) : nullptr, threads * VPT, p.w_dt};
+    if (V.sm) {
+        V.fill(B_POST_GAIN, S.post_gain, S.scale, S.cols);
+        V.fill(B_PRE_GAIN, S.pre_gain, 1.f, S.cols);
+        if (has_pb) V.fill(B_POST_BIAS, S.post_bias, S.scale, S.cols);
     }
-    __syncthreads();
-    const Ring<VPT> ring{smem + kRedBytes + (p.vecs_in_smem ? B_VECS * 32 * chunks : 0) + threadIdx.x * 16, threads * 16,
-                         p.units};
-    int col[VPT], vcol[VPT];
+    const Ring<VPT> ring{smem + kRedBytes + (V.sm ? B_VECS * 32 * V.chunks : 0) + threadIdx.x * 16, threads * 16, p.units};
+    int col[VPT], ecol[VPT];
     bool in[VPT];
 #pragma unroll
     for (int j = 0; j < VPT; ++j) {
         col[j] = (j * threads + (int)threadIdx.x) * 8;
         in[j] = col[j] < S.cols;
-        vcol[j] = in[j] ? col[j] : 0;
+        ecol[j] = (in[j] ? col[j] : 0) / kActBlock;
+        if (!in[j])
+            for (int u = 0; u < D * p.units; ++u) *reinterpret_cast<uint4*>(ring.at(0, u, j)) = make_uint4(0u, 0u, 0u, 0u);
     }
+    __syncthreads();
     int r0, r1;
     if (p.plan.parts == 0) {
         r0 = (int)min((long long)S.rows, (long long)blockIdx.x * p.plan.run_rows);
@@ -404,30 +441,38 @@ __global__ void __launch_bounds__(MAXT, MAXT * VPT >= 1024 ? 1 : (ALL ? 512 : 10
         r0 = (int)min(end, g * S.gate_rows + (long long)(blockIdx.x % p.plan.parts) * p.plan.run_rows);
         r1 = (int)min(end, (long long)r0 + p.plan.run_rows);
     }
-    const bool has_pre = S.pre != MUON_NORM_NONE, has_post = S.post != MUON_NORM_NONE, has_f = S.df != nullptr;
-    const bool has_dout = S.dout != nullptr, has_gate = S.gate != nullptr, post_c = S.post_c.q != nullptr;
-    const bool gate_sums = ALL && p.gate_sums;
-    const T *dy = static_cast<const T*>(S.dy), *dout = static_cast<const T*>(S.dout), *gate = static_cast<const T*>(S.gate);
     const int gr = has_gate ? S.gate_rows : 1;
-    int grow = has_gate ? r0 / gr : 0, gleft = has_gate ? gr - r0 % gr : 0;         // of the next copy
-    int crow = grow, cleft = gleft;                                                // of the row at work
+    int gleft = has_gate ? gr - r0 % gr : 0, cleft = gleft;                 // rows left of the gate row: of the next copy, at work
+    // this thread's first chunk of the next row to copy, and of the row at work
+    const T* dy = static_cast<const T*>(S.dy) + r0 * S.lddy + threadIdx.x * 8;
+    const T* dout = static_cast<const T*>(S.dout) + r0 * S.lddout + threadIdx.x * 8;
+    const T* gate = static_cast<const T*>(S.gate) + (r0 / gr) * S.ldgate + threadIdx.x * 8;
+    const signed char* yq = S.pre_c.q + r0 * S.pre_c.ldq + threadIdx.x * 8;
+    const signed char* pq = S.post_c.q + r0 * S.post_c.ldq + threadIdx.x * 8;
+    T* dx = static_cast<T*>(S.dx) + r0 * S.lddx + threadIdx.x * 8;
+    T* df = static_cast<T*>(S.df) + r0 * S.lddf + threadIdx.x * 8;
+    T* dg = static_cast<T*>(S.dgate) + (r0 / gr) * S.lddgate + threadIdx.x * 8;
     auto copy = [&](int row, int d) {
         if (row < r1) {
 #pragma unroll
             for (int j = 0; j < VPT; ++j) {
                 if (!in[j]) continue;
+                const int cj = j * threads * 8;
 #pragma unroll
                 for (int n = 0; n < NPC; ++n) {
-                    const int c = col[j] + n * 4;
-                    if (has_pre) cp_async16(ring.at(d, n, j), dy + row * S.lddy + c, 16);
-                    if (has_dout) cp_async16(ring.at(d, kDout + n, j), dout + row * S.lddout + c, 16);
-                    if (has_gate) cp_async16(ring.at(d, kGate + n, j), gate + grow * S.ldgate + c, 16);
+                    if (has_pre) cp_async16(ring.at(d, n, j), dy + cj + n * 4, 16);
+                    if (has_dout) cp_async16(ring.at(d, kDout + n, j), dout + cj + n * 4, 16);
+                    if (has_gate) cp_async16(ring.at(d, kGate + n, j), gate + cj + n * 4, 16);
                 }
-                if (has_pre) cp_async8(ring.at(d, kCodes, j), S.pre_c.q + row * S.pre_c.ldq + col[j]);
-                if (post_c) cp_async8(ring.at(d, kCodes, j) + 8, S.post_c.q + row * S.post_c.ldq + col[j]);
+                if (has_pre) cp_async8(ring.at(d, kCodes, j), yq + cj);
+                if (post_c) cp_async8(ring.at(d, kCodes, j) + 8, pq + cj);
             }
+            dy += S.lddy;
+            dout += S.lddout;
+            yq += S.pre_c.ldq;
+            pq += S.post_c.ldq;
             if (has_gate && --gleft == 0) {
-                ++grow;
+                gate += S.ldgate;
                 gleft = gr;
             }
         }
@@ -436,21 +481,24 @@ __global__ void __launch_bounds__(MAXT, MAXT * VPT >= 1024 ? 1 : (ALL ? 512 : 10
     // exponent bytes and deviations of the next row
     int ep[VPT], eq[VPT];
     float rp = 0.f, rq = 0.f;
+    const unsigned char *ye = S.pre_c.e + r0 * S.pre_c.lde, *pe = S.post_c.e + r0 * S.post_c.lde;
     auto scalars = [&](int row) {
         if (row >= r1) return;
 #pragma unroll
         for (int j = 0; j < VPT; ++j) {
-            if (has_pre) ep[j] = S.pre_c.e[row * S.pre_c.lde + vcol[j] / kActBlock];
-            if (post_c) eq[j] = S.post_c.e[row * S.post_c.lde + vcol[j] / kActBlock];
+            if (has_pre) ep[j] = ye[ecol[j]];
+            if (post_c) eq[j] = pe[ecol[j]];
         }
+        ye += S.pre_c.lde;
+        pe += S.post_c.lde;
         if (has_pre) rp = S.pre_rstd[row];
         if (has_post) rq = S.post_rstd[row];
     };
+    // codes of a thread without columns are 0 under any finite scale; a bad block's byte must not reach them
     auto decode = [&](int d, int half, int j, int byte, float (&n)[8]) {
-        const uint2 w = in[j] ? *reinterpret_cast<const uint2*>(ring.at(d, kCodes, j) + 8 * half) : make_uint2(0u, 0u);
-        act8_decode8(w, in[j] ? byte : 127, n);
+        act8_decode8(*reinterpret_cast<const uint2*>(ring.at(d, kCodes, j) + 8 * half), in[j] ? byte : 127, n);
     };
-    float a_pg[VPT][8] = {}, a_qg[VPT][8] = {};               // d_pre_gain, d_post_gain
+    float a_pg[VPT][8] = {}, a_qg[VPT][8] = {};               // d_pre_gain, d_post_gain / scale
     float a_pb[ALL ? VPT : 1][8] = {}, a_qb[ALL ? VPT : 1][8] = {}, a_gt[ALL ? VPT : 1][8] = {};
     int slot = 0, d = 0;
     scalars(r0);
@@ -468,51 +516,52 @@ __global__ void __launch_bounds__(MAXT, MAXT * VPT >= 1024 ? 1 : (ALL ? 512 : 10
         }
         scalars(row + 1);
         float x[VPT][8];                                      // d, the gradient of x'
-#pragma unroll
-        for (int j = 0; j < VPT; ++j) {
-            if (has_dout) ring_get<DT, VPT>(ring, d, kDout, j, in[j], x[j]);
-            else
-#pragma unroll
-                for (int i = 0; i < 8; ++i) x[j][i] = 0.f;
-        }
         if (has_pre) {
-            float g[VPT][8], n[VPT][8], sums[2] = {0.f, 0.f};
+            float n[VPT][8], sums[2] = {0.f, 0.f};
 #pragma unroll
             for (int j = 0; j < VPT; ++j) {
-                ring_get<DT, VPT>(ring, d, 0, j, in[j], g[j]);
+                float t[8];
+                ring_get<DT, VPT>(ring, d, 0, j, x[j]);
                 decode(d, 0, j, b_pre[j], n[j]);
+                V.get(B_PRE_GAIN, S.pre_gain, 1.f, col[j], in[j], t);
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
-                    a_pg[j][i] = fmaf(g[j][i], n[j][i], a_pg[j][i]);
-                    if constexpr (ALL) a_pb[j][i] += g[j][i];
+                    const float gn = x[j][i] * n[j][i];
+                    a_pg[j][i] += gn;
+                    if constexpr (ALL) a_pb[j][i] += x[j][i];
+                    sums[0] = fmaf(gn, t[i], sums[0]);
+                    x[j][i] *= t[i];
                 }
-                if (S.pre_gain) {
-                    float t[8];
-                    V.get(B_PRE_GAIN, S.pre_gain, vcol[j], in[j], t);
+                if (S.pre == MUON_NORM_LAYER)
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) g[j][i] *= t[i];
-                }
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    sums[0] = fmaf(g[j][i], n[j][i], sums[0]);
-                    sums[1] += g[j][i];
-                }
+                    for (int i = 0; i < 8; ++i) sums[1] += x[j][i];
             }
             float s0 = 0.f, s1;
             if (S.pre == MUON_NORM_LAYER) {
                 block_sum<2>(sums, red, slot, nw);
-                s0 = sums[1] * p.inv_c;
-                s1 = sums[0] * p.inv_c;
+                s0 = sums[1] * p.inv_c * r_pre;
+                s1 = sums[0];
             } else {
                 float one[1] = {sums[0]};
                 block_sum<1>(one, red, slot, nw);
-                s1 = one[0] * p.inv_c;
+                s1 = one[0];
             }
+            s1 *= p.inv_c * r_pre;
 #pragma unroll
-            for (int j = 0; j < VPT; ++j)
+            for (int j = 0; j < VPT; ++j) {
+                float t[8];
+                if (has_dout) ring_get<DT, VPT>(ring, d, kDout, j, t);
+                else
 #pragma unroll
-                for (int i = 0; i < 8; ++i)        // columns beyond the row stay out of the sums over it
-                    x[j][i] = in[j] ? fmaf(r_pre, fmaf(-n[j][i], s1, g[j][i] - s0), x[j][i]) : 0.f;
+                    for (int i = 0; i < 8; ++i) t[i] = 0.f;
+                // columns beyond the row (t, x and n are 0) stay out of the sums over it
+                const float s0j = in[j] ? s0 : 0.f;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) x[j][i] = fmaf(r_pre, x[j][i], fmaf(-s1, n[j][i], t[i] - s0j));
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < VPT; ++j) ring_get<DT, VPT>(ring, d, kDout, j, x[j]);
         }
         if (has_f) {
             float n[VPT][8], h[VPT][8], sums[2] = {0.f, 0.f};
@@ -523,86 +572,82 @@ __global__ void __launch_bounds__(MAXT, MAXT * VPT >= 1024 ? 1 : (ALL ? 512 : 10
                 else
 #pragma unroll
                     for (int i = 0; i < 8; ++i) n[j][i] = 0.f;
-#pragma unroll
-                for (int i = 0; i < 8; ++i) h[j][i] = S.scale * x[j][i];
+                V.get(B_POST_GAIN, S.post_gain, S.scale, col[j], in[j], t);
                 if (has_gate) {
-                    if (S.dgate) {
+                    float g[8];
+                    ring_get<DT, VPT>(ring, d, kGate, j, g);
+                    if (dgate) {
                         float u[8];
+                        if (has_pb) {
+                            V.get(B_POST_BIAS, S.post_bias, S.scale, col[j], in[j], u);
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) u[i] = n[j][i];
-                        if (S.post_gain) {
-                            V.get(B_POST_GAIN, S.post_gain, vcol[j], in[j], t);
+                            for (int i = 0; i < 8; ++i) u[i] = fmaf(n[j][i], t[i], u[i]) * x[j][i];
+                        } else {
 #pragma unroll
-                            for (int i = 0; i < 8; ++i) u[i] *= t[i];
+                            for (int i = 0; i < 8; ++i) u[i] = n[j][i] * t[i] * x[j][i];
                         }
-                        if (S.post_bias) {
-                            V.get(B_POST_BIAS, S.post_bias, vcol[j], in[j], t);
-#pragma unroll
-                            for (int i = 0; i < 8; ++i) u[i] += t[i];
-                        }
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) u[i] *= h[j][i];
                         if (!gate_sums) {
                             Raw8<DT> o;
                             o.set(u);
-                            o.store(static_cast<T*>(S.dgate) + crow * S.lddgate + col[j], in[j]);
+                            o.store(dg + j * threads * 8, in[j]);
                         }
                         if constexpr (ALL)
 #pragma unroll
                             for (int i = 0; i < 8; ++i) a_gt[j][i] += u[i];
                     }
-                    ring_get<DT, VPT>(ring, d, kGate, j, in[j], t);
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) h[j][i] *= t[i];
+                    for (int i = 0; i < 8; ++i) h[j][i] = x[j][i] * g[i];
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) h[j][i] = x[j][i];
                 }
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
-                    a_qg[j][i] = fmaf(h[j][i], n[j][i], a_qg[j][i]);
+                    const float hn = h[j][i] * n[j][i];
+                    a_qg[j][i] += hn;
                     if constexpr (ALL) a_qb[j][i] += h[j][i];
+                    sums[0] = fmaf(hn, t[i], sums[0]);
+                    h[j][i] *= t[i];
                 }
-                if (S.post_gain) {
-                    V.get(B_POST_GAIN, S.post_gain, vcol[j], in[j], t);
+                if (S.post == MUON_NORM_LAYER)
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) h[j][i] *= t[i];
-                }
-                if (has_post)
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        sums[0] = fmaf(h[j][i], n[j][i], sums[0]);
-                        sums[1] += h[j][i];
-                    }
+                    for (int i = 0; i < 8; ++i) sums[1] += h[j][i];
             }
             if (has_post) {
                 float s0 = 0.f, s1;
                 if (S.post == MUON_NORM_LAYER) {
                     block_sum<2>(sums, red, slot, nw);
-                    s0 = sums[1] * p.inv_c;
-                    s1 = sums[0] * p.inv_c;
+                    s0 = sums[1] * p.inv_c * r_post;
+                    s1 = sums[0];
                 } else {
                     float one[1] = {sums[0]};
                     block_sum<1>(one, red, slot, nw);
-                    s1 = one[0] * p.inv_c;
+                    s1 = one[0];
                 }
+                s1 *= p.inv_c * r_post;
 #pragma unroll
                 for (int j = 0; j < VPT; ++j)
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) h[j][i] = r_post * fmaf(-n[j][i], s1, h[j][i] - s0);
+                    for (int i = 0; i < 8; ++i) h[j][i] = fmaf(r_post, h[j][i], fmaf(-s1, n[j][i], -s0));
             }
 #pragma unroll
             for (int j = 0; j < VPT; ++j) {
                 Raw8<DT> o;
                 o.set(h[j]);
-                o.store(static_cast<T*>(S.df) + row * S.lddf + col[j], in[j]);
+                o.store(df + j * threads * 8, in[j]);
             }
+            df += S.lddf;
         }
 #pragma unroll
         for (int j = 0; j < VPT; ++j) {
+            if (S.skip != 1.f)
 #pragma unroll
-            for (int i = 0; i < 8; ++i) x[j][i] *= S.skip;
+                for (int i = 0; i < 8; ++i) x[j][i] *= S.skip;
             Raw8<DT> o;
             o.set(x[j]);
-            o.store(static_cast<T*>(S.dx) + row * S.lddx + col[j], in[j]);
+            o.store(dx + j * threads * 8, in[j]);
         }
+        dx += S.lddx;
         if (has_gate && (--cleft == 0 || row + 1 == S.rows)) {
             if constexpr (ALL)
                 if (gate_sums && p.plan.parts == 0)
@@ -610,29 +655,31 @@ __global__ void __launch_bounds__(MAXT, MAXT * VPT >= 1024 ? 1 : (ALL ? 512 : 10
                     for (int j = 0; j < VPT; ++j) {
                         Raw8<DT> o;
                         o.set(a_gt[j]);
-                        o.store(static_cast<T*>(S.dgate) + crow * S.lddgate + col[j], in[j]);
+                        o.store(dg + j * threads * 8, in[j]);
 #pragma unroll
                         for (int i = 0; i < 8; ++i) a_gt[j][i] = 0.f;
                     }
-            ++crow;
+            dg += S.lddgate;
             cleft = gr;
         }
         d = d + 1 == D ? 0 : d + 1;
     }
     cp_async_wait<0>();
-    auto put = [&](int v, const float (&a)[8], int j) {
+    auto put = [&](int v, float (&a)[8], float mul, int j) {
         Raw8<DT_FP32> o;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) a[i] *= mul;
         o.set(a);
         o.store(p.part + ((long long)v * p.plan.runs + blockIdx.x) * S.cols + col[j], in[j]);
     };
 #pragma unroll
     for (int j = 0; j < VPT; ++j) {
-        if (S.d_pre_gain) put(V_PRE_GAIN, a_pg[j], j);
-        if (S.d_post_gain) put(V_POST_GAIN, a_qg[j], j);
+        if (S.d_pre_gain) put(V_PRE_GAIN, a_pg[j], 1.f, j);
+        if (S.d_post_gain) put(V_POST_GAIN, a_qg[j], S.scale, j);
         if constexpr (ALL) {
-            if (S.d_pre_bias) put(V_PRE_BIAS, a_pb[j], j);
-            if (S.d_post_bias) put(V_POST_BIAS, a_qb[j], j);
-            if (p.gate_sums && p.plan.parts) put(V_COUNT, a_gt[j], j);
+            if (S.d_pre_bias) put(V_PRE_BIAS, a_pb[j], 1.f, j);
+            if (S.d_post_bias) put(V_POST_BIAS, a_qb[j], S.scale, j);
+            if (p.gate_sums && p.plan.parts) put(V_COUNT, a_gt[j], 1.f, j);
         }
     }
 }
@@ -715,9 +762,9 @@ __device__ __forceinline__ float row_normalise(float (&v)[VPT][8], const int (&n
 #pragma unroll
             for (int i = 0; i < 8; ++i) s[0] = fmaf(v[j][i] * down, v[j][i] * down, s[0]);
         row_sum<TPR, 1>(s, red, slot);
-        r = __frsqrt_rn(s[0] * inv_c) * down;
+        r = rsqrtf(s[0] * inv_c) * down;
     } else {
-        r = __frsqrt_rn(fmaf(s[0], inv_c, eps));
+        r = rsqrtf(fmaf(s[0], inv_c, eps));
     }
 #pragma unroll
     for (int j = 0; j < VPT; ++j)
@@ -1075,52 +1122,65 @@ int sm_count() {
     return nsm;
 }
 
-// Shared memory of a block whose stages hold `units` 16-byte pieces per thread and chunk, with
-// the vectors as fp32 where that leaves room for the blocks that the kernel's registers allow on
-// an SM.
+// One form of a kernel: chunks of 8 columns per thread, most threads, stages, blocks per SM that
+// its registers are bounded for.
+struct Form {
+    int vpt, maxt, stages, per_sm;
+    int threads(int cols) const { return (cols + 256 * vpt - 1) / (256 * vpt) * 32; }
+    // blocks that the registers of an SM take
+    int blocks(int cols) const { return std::min(32, per_sm * maxt / threads(cols)); }
+};
+
+// Shared memory of a block, with the vectors as fp32 where that leaves room for as many blocks as
+// the registers take.
 template <typename P>
-int seam_smem(P& p, int threads, int vpt, int stages, int vectors, int blocks_per_sm) {
-    const int ring = stages * p.units * vpt * threads * 16, vecs = vectors * 32 * (p.s.cols / 8);
-    const int limit = (227 * 1024 - 1024 * blocks_per_sm) / blocks_per_sm;
-    p.vecs_in_smem = kRedBytes + ring + vecs <= limit;
+int seam_smem(P& p, const Form& f, int vectors) {
+    const int t = f.threads(p.s.cols), blocks = f.blocks(p.s.cols);
+    const int ring = f.stages * p.units * f.vpt * t * 16, vecs = vectors * 32 * f.vpt * t;
+    p.vecs_in_smem = kRedBytes + ring + vecs <= 227 * 1024 / blocks - 1024;
     return kRedBytes + ring + (p.vecs_in_smem ? vecs : 0);
 }
 
 template <typename K, typename P>
-cudaError_t seam_launch(K kern, const P& p, unsigned grid, int threads, int smem, cudaStream_t s) {
+cudaError_t seam_launch(K kern, P& p, const Form& f, int vectors, unsigned grid, cudaStream_t s) {
+    const int smem = seam_smem(p, f, vectors);
     const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
-    kern<<<grid, threads, smem, s>>>(p);
+    kern<<<grid, f.threads(p.s.cols), smem, s>>>(p);
     return cudaGetLastError();
 }
 
-int row_threads(int cols) { return (cols + 255) / 256 * 32; }
-
 template <typename T>
 cudaError_t launch_fwd(FwdParams& p, cudaStream_t s) {
-    const int c = p.s.cols, t = row_threads(c), npc = sizeof(T) == 4 ? 2 : 1;
+    const int c = p.s.cols, npc = sizeof(T) == 4 ? 2 : 1;
     p.units = npc * (p.s.gate ? 3 : p.s.f ? 2 : 1);
-    const int per_sm = std::max(1, std::min(32, 1024 / std::min(t, 1024)));
-    const unsigned grid = (unsigned)std::min<long long>(p.s.rows, (long long)sm_count() * per_sm);
-    if (c <= 1024) return seam_launch(seam_fwd_kernel<T, 1, 128, 3>, p, grid, t, seam_smem(p, t, 1, 3, F_VECS, per_sm), s);
-    if (c <= 4096) return seam_launch(seam_fwd_kernel<T, 1, 512, 2>, p, grid, t, seam_smem(p, t, 1, 2, F_VECS, per_sm), s);
-    if (c <= 8192) return seam_launch(seam_fwd_kernel<T, 1, 1024, 2>, p, grid, t, seam_smem(p, t, 1, 2, F_VECS, 1), s);
-    return seam_launch(seam_fwd_kernel<T, 2, 1024, 1>, p, grid, 1024, seam_smem(p, 1024, 2, 1, F_VECS, 1), s);
+#define SEAM_FWD(VPT, MAXT, D, MINB)                                                                              \
+    do {                                                                                                          \
+        const Form f{VPT, MAXT, D, MINB};                                                                         \
+        const unsigned grid = (unsigned)std::min<long long>(p.s.rows, (long long)sm_count() * f.blocks(c));       \
+        return seam_launch(seam_fwd_kernel<T, VPT, MAXT, D, MINB>, p, f, F_VECS, grid, s);                        \
+    } while (0)
+    if (c <= 256) SEAM_FWD(1, 32, 3, 32);
+    if (c <= 512) SEAM_FWD(2, 32, 3, 24);
+    if (c <= 768) SEAM_FWD(3, 32, 3, 20);
+    if (c <= 1024) SEAM_FWD(4, 32, 2, 16);
+    if (c <= 4096) SEAM_FWD(2, 256, 2, 3);
+    if (c <= 8192) SEAM_FWD(2, 512, 2, 1);
+    SEAM_FWD(2, 1024, 1, 1);
+#undef SEAM_FWD
 }
 
 template <typename T, bool ALL>
 cudaError_t launch_bwd(BwdParams& p, cudaStream_t s) {
-    const int c = p.s.cols, t = row_threads(c), npc = sizeof(T) == 4 ? 2 : 1;
+    const int c = p.s.cols, npc = sizeof(T) == 4 ? 2 : 1;
     p.units = 2 * npc + 1 + (p.s.gate ? npc : 0);
-    const unsigned grid = (unsigned)p.plan.runs;
-    const int per_sm = std::max(1, std::min(16, 1024 / std::min(t, 1024)));
-    if (c <= 1024) return seam_launch(seam_bwd_kernel<T, 1, 128, 3, ALL>, p, grid, t, seam_smem(p, t, 1, 3, B_VECS, per_sm), s);
-    if (c <= 4096) return seam_launch(seam_bwd_kernel<T, 1, 512, 2, ALL>, p, grid, t, seam_smem(p, t, 1, 2, B_VECS, per_sm), s);
-    if (c <= 8192) {
-        const int h = (c + 511) / 512 * 32;
-        return seam_launch(seam_bwd_kernel<T, 2, 512, 2, ALL>, p, grid, h, seam_smem(p, h, 2, 2, B_VECS, 1), s);
-    }
-    return seam_launch(seam_bwd_kernel<T, 2, 1024, 1, ALL>, p, grid, 1024, seam_smem(p, 1024, 2, 1, B_VECS, 1), s);
+#define SEAM_BWD(VPT, MAXT, D, MINB)                                                                                    \
+    return seam_launch(seam_bwd_kernel<T, VPT, MAXT, D, MINB, ALL>, p, Form{VPT, MAXT, D, MINB}, B_VECS, (unsigned)p.plan.runs, s)
+    if (c <= 1024) SEAM_BWD(1, 128, 3, ALL ? 4 : 6);
+    if (c <= 4096) SEAM_BWD(2, 256, 2, ALL ? 1 : 2);
+    if (c <= 8192) SEAM_BWD(2, 512, 2, 1);
+    SEAM_BWD(2, 1024, 1, 1);
+#undef SEAM_BWD
 }
 
 cudaError_t launch_fwd_any(const FwdParams& p, int dt, cudaStream_t s) {
