@@ -236,6 +236,10 @@ __device__ __forceinline__ void cp_async4(void* smem_dst, const void* gmem_src, 
     asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;"
                  ::"r"(smem_u32(smem_dst)), "l"(gmem_src), "r"(src_bytes) : "memory");
 }
+// The same through L1: for threads that copy the two halves of a 32-byte sector one after the other.
+__device__ __forceinline__ void cp_async16_l1(void* smem_dst, const void* gmem_src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 16;" ::"r"(smem_u32(smem_dst)), "l"(gmem_src) : "memory");
+}
 // 8-byte form.
 __device__ __forceinline__ void cp_async8(void* smem_dst, const void* gmem_src) {
     asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(smem_u32(smem_dst)), "l"(gmem_src) : "memory");

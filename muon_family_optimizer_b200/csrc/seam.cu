@@ -71,7 +71,7 @@ struct BwdParams {
     RunPlan plan;
     float inv_c;
     int w_dt, vec, wvec, gate_sums;
-    int vecs_in_smem, units;
+    int vecs_in_smem, vectors, units;
     float* part;           // [V_COUNT + 1][runs][cols]: sums of one run (the last: shared gate rows)
 };
 
@@ -208,6 +208,13 @@ struct Ring {
     __device__ __forceinline__ uint8_t* at(int d, int u, int j) const { return base + ((d * units + u) * VPT + j) * stride; }
 };
 
+// One 16-byte copy; an fp32 chunk is two of them, halves of one sector.
+template <int NPC>
+__device__ __forceinline__ void copy16(void* dst, const void* src) {
+    if (NPC == 2) cp_async16_l1(dst, src);
+    else cp_async16(dst, src, 16);
+}
+
 // Eight elements of a thread's chunk from the ring (zeros for a thread without columns: it never copies, and
 // its pieces were cleared).
 template <int DT, int VPT>
@@ -222,11 +229,11 @@ struct FwdParams {
     muon_seam s;
     float inv_c;
     int w_dt, vec, wvec;
-    int vecs_in_smem, units;
+    int vecs_in_smem, vectors, units;
     int* d_status;
 };
 
-enum FwdVec : int { F_POST_GAIN, F_POST_BIAS, F_PRE_GAIN, F_PRE_BIAS, F_VECS };
+enum FwdVec : int { F_POST_GAIN, F_PRE_GAIN, F_POST_BIAS, F_PRE_BIAS, F_VECS };   // the biases only where there is one
 
 constexpr int kRedBytes = 512;      // block_sum's areas
 
@@ -251,7 +258,7 @@ __global__ void __launch_bounds__(MAXT, MINB) seam_fwd_kernel(const __grid_const
         if (has_pb) V.fill(F_POST_BIAS, S.post_bias, S.scale, S.cols);
         if (has_yb) V.fill(F_PRE_BIAS, S.pre_bias, 1.f, S.cols);
     }
-    const Ring<VPT> ring{smem + kRedBytes + (V.sm ? F_VECS * 32 * V.chunks : 0) + threadIdx.x * 16, threads * 16, p.units};
+    const Ring<VPT> ring{smem + kRedBytes + (V.sm ? p.vectors * 32 * V.chunks : 0) + threadIdx.x * 16, threads * 16, p.units};
     int col[VPT];
     bool in[VPT];
 #pragma unroll
@@ -281,9 +288,9 @@ __global__ void __launch_bounds__(MAXT, MINB) seam_fwd_kernel(const __grid_const
 #pragma unroll
                 for (int n = 0; n < NPC; ++n) {
                     const int c = j * threads * 8 + n * 4;
-                    cp_async16(ring.at(d, n, j), x + c, 16);
-                    if (has_f) cp_async16(ring.at(d, kF + n, j), f + c, 16);
-                    if (has_gate) cp_async16(ring.at(d, kGate + n, j), gate + c, 16);
+                    copy16<NPC>(ring.at(d, n, j), x + c);
+                    if (has_f) copy16<NPC>(ring.at(d, kF + n, j), f + c);
+                    if (has_gate) copy16<NPC>(ring.at(d, kGate + n, j), gate + c);
                 }
             }
             x += S.ldx;
@@ -398,9 +405,9 @@ __global__ void __launch_bounds__(MAXT, MINB) seam_fwd_kernel(const __grid_const
     if (__any_sync(0xFFFFFFFFu, bad) && lane == 0 && p.d_status) atomicOr(p.d_status, MUON_FLAG_NONFINITE);
 }
 
-enum BwdVec : int { B_POST_GAIN, B_POST_BIAS, B_PRE_GAIN, B_VECS };
+enum BwdVec : int { B_POST_GAIN, B_PRE_GAIN, B_POST_BIAS, B_VECS };
 
-template <typename T, int VPT, int MAXT, int D, int MINB, bool ALL>
+template <typename T, int VPT, int MAXT, int D, int MINB, bool BIAS, bool GSUM>
 __global__ void __launch_bounds__(MAXT, MINB) seam_bwd_kernel(const __grid_constant__ BwdParams p) {
     constexpr int DT = DtOf<T>::v;
     constexpr int NPC = sizeof(T) == 4 ? 2 : 1;
@@ -411,7 +418,7 @@ __global__ void __launch_bounds__(MAXT, MINB) seam_bwd_kernel(const __grid_const
     const int threads = blockDim.x, nw = threads >> 5;
     const bool has_pre = S.pre != MUON_NORM_NONE, has_post = S.post != MUON_NORM_NONE, has_f = S.df != nullptr;
     const bool has_dout = S.dout != nullptr, has_gate = S.gate != nullptr, post_c = S.post_c.q != nullptr;
-    const bool has_pb = S.post_bias != nullptr, dgate = S.dgate != nullptr, gate_sums = ALL && p.gate_sums;
+    const bool has_pb = S.post_bias != nullptr, dgate = S.dgate != nullptr, gate_sums = GSUM;
     for (int i = threadIdx.x; i < kRedBytes / 4; i += threads) red[i] = 0.f;
     // scale rides on the post-norm's vectors
     const Vectors V{p.vecs_in_smem ? reinterpret_cast<float*>(smem + kRedBytes) : nullptr, threads * VPT, p.w_dt};
@@ -420,7 +427,7 @@ __global__ void __launch_bounds__(MAXT, MINB) seam_bwd_kernel(const __grid_const
         V.fill(B_PRE_GAIN, S.pre_gain, 1.f, S.cols);
         if (has_pb) V.fill(B_POST_BIAS, S.post_bias, S.scale, S.cols);
     }
-    const Ring<VPT> ring{smem + kRedBytes + (V.sm ? B_VECS * 32 * V.chunks : 0) + threadIdx.x * 16, threads * 16, p.units};
+    const Ring<VPT> ring{smem + kRedBytes + (V.sm ? p.vectors * 32 * V.chunks : 0) + threadIdx.x * 16, threads * 16, p.units};
     int col[VPT], ecol[VPT];
     bool in[VPT];
 #pragma unroll
@@ -460,9 +467,9 @@ __global__ void __launch_bounds__(MAXT, MINB) seam_bwd_kernel(const __grid_const
                 const int cj = j * threads * 8;
 #pragma unroll
                 for (int n = 0; n < NPC; ++n) {
-                    if (has_pre) cp_async16(ring.at(d, n, j), dy + cj + n * 4, 16);
-                    if (has_dout) cp_async16(ring.at(d, kDout + n, j), dout + cj + n * 4, 16);
-                    if (has_gate) cp_async16(ring.at(d, kGate + n, j), gate + cj + n * 4, 16);
+                    if (has_pre) copy16<NPC>(ring.at(d, n, j), dy + cj + n * 4);
+                    if (has_dout) copy16<NPC>(ring.at(d, kDout + n, j), dout + cj + n * 4);
+                    if (has_gate) copy16<NPC>(ring.at(d, kGate + n, j), gate + cj + n * 4);
                 }
                 if (has_pre) cp_async8(ring.at(d, kCodes, j), yq + cj);
                 if (post_c) cp_async8(ring.at(d, kCodes, j) + 8, pq + cj);
@@ -499,7 +506,7 @@ __global__ void __launch_bounds__(MAXT, MINB) seam_bwd_kernel(const __grid_const
         act8_decode8(*reinterpret_cast<const uint2*>(ring.at(d, kCodes, j) + 8 * half), in[j] ? byte : 127, n);
     };
     float a_pg[VPT][8] = {}, a_qg[VPT][8] = {};               // d_pre_gain, d_post_gain / scale
-    float a_pb[ALL ? VPT : 1][8] = {}, a_qb[ALL ? VPT : 1][8] = {}, a_gt[ALL ? VPT : 1][8] = {};
+    float a_pb[BIAS ? VPT : 1][8] = {}, a_qb[BIAS ? VPT : 1][8] = {}, a_gt[GSUM ? VPT : 1][8] = {};
     int slot = 0, d = 0;
     scalars(r0);
 #pragma unroll
@@ -528,7 +535,7 @@ __global__ void __launch_bounds__(MAXT, MINB) seam_bwd_kernel(const __grid_const
                 for (int i = 0; i < 8; ++i) {
                     const float gn = x[j][i] * n[j][i];
                     a_pg[j][i] += gn;
-                    if constexpr (ALL) a_pb[j][i] += x[j][i];
+                    if constexpr (BIAS) a_pb[j][i] += x[j][i];
                     sums[0] = fmaf(gn, t[i], sums[0]);
                     x[j][i] *= t[i];
                 }
@@ -591,7 +598,7 @@ __global__ void __launch_bounds__(MAXT, MINB) seam_bwd_kernel(const __grid_const
                             o.set(u);
                             o.store(dg + j * threads * 8, in[j]);
                         }
-                        if constexpr (ALL)
+                        if constexpr (GSUM)
 #pragma unroll
                             for (int i = 0; i < 8; ++i) a_gt[j][i] += u[i];
                     }
@@ -605,7 +612,7 @@ __global__ void __launch_bounds__(MAXT, MINB) seam_bwd_kernel(const __grid_const
                 for (int i = 0; i < 8; ++i) {
                     const float hn = h[j][i] * n[j][i];
                     a_qg[j][i] += hn;
-                    if constexpr (ALL) a_qb[j][i] += h[j][i];
+                    if constexpr (BIAS) a_qb[j][i] += h[j][i];
                     sums[0] = fmaf(hn, t[i], sums[0]);
                     h[j][i] *= t[i];
                 }
@@ -649,8 +656,8 @@ __global__ void __launch_bounds__(MAXT, MINB) seam_bwd_kernel(const __grid_const
         }
         dx += S.lddx;
         if (has_gate && (--cleft == 0 || row + 1 == S.rows)) {
-            if constexpr (ALL)
-                if (gate_sums && p.plan.parts == 0)
+            if constexpr (GSUM)
+                if (p.plan.parts == 0)
 #pragma unroll
                     for (int j = 0; j < VPT; ++j) {
                         Raw8<DT> o;
@@ -676,11 +683,12 @@ __global__ void __launch_bounds__(MAXT, MINB) seam_bwd_kernel(const __grid_const
     for (int j = 0; j < VPT; ++j) {
         if (S.d_pre_gain) put(V_PRE_GAIN, a_pg[j], 1.f, j);
         if (S.d_post_gain) put(V_POST_GAIN, a_qg[j], S.scale, j);
-        if constexpr (ALL) {
+        if constexpr (BIAS) {
             if (S.d_pre_bias) put(V_PRE_BIAS, a_pb[j], 1.f, j);
             if (S.d_post_bias) put(V_POST_BIAS, a_qb[j], S.scale, j);
-            if (p.gate_sums && p.plan.parts) put(V_COUNT, a_gt[j], 1.f, j);
         }
+        if constexpr (GSUM)
+            if (p.plan.parts) put(V_COUNT, a_gt[j], 1.f, j);
     }
 }
 
@@ -1131,22 +1139,20 @@ struct Form {
     int blocks(int cols) const { return std::min(32, per_sm * maxt / threads(cols)); }
 };
 
-// Shared memory of a block, with the vectors as fp32 where that leaves room for as many blocks as
-// the registers take.
-template <typename P>
-int seam_smem(P& p, const Form& f, int vectors) {
-    const int t = f.threads(p.s.cols), blocks = f.blocks(p.s.cols);
-    const int ring = f.stages * p.units * f.vpt * t * 16, vecs = vectors * 32 * f.vpt * t;
-    p.vecs_in_smem = kRedBytes + ring + vecs <= 227 * 1024 / blocks - 1024;
-    return kRedBytes + ring + (p.vecs_in_smem ? vecs : 0);
-}
-
+// Launches a form: its shared memory, with the vectors as fp32 wherever they fit (read from
+// global memory they cost more than the blocks per SM that their space may cost: 16384 x 4096
+// with a gate forward 150 us with three blocks and global vectors); the blocks that are resident then are
+// the grid, unless the runs of rows are given.
 template <typename K, typename P>
-cudaError_t seam_launch(K kern, P& p, const Form& f, int vectors, unsigned grid, cudaStream_t s) {
-    const int smem = seam_smem(p, f, vectors);
+cudaError_t seam_launch(K kern, P& p, const Form& f, long long runs, cudaStream_t s) {
+    const int t = f.threads(p.s.cols), most = f.blocks(p.s.cols), room = 227 * 1024;
+    const int ring = kRedBytes + f.stages * p.units * f.vpt * t * 16, vecs = p.vectors * 32 * f.vpt * t;
+    p.vecs_in_smem = ring + vecs + 1024 <= room;
+    const int smem = ring + (p.vecs_in_smem ? vecs : 0);
     const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
-    kern<<<grid, f.threads(p.s.cols), smem, s>>>(p);
+    const long long resident = (long long)sm_count() * std::max(1, std::min(most, room / (smem + 1024)));
+    kern<<<(unsigned)(runs ? runs : std::min<long long>(p.s.rows, resident)), t, smem, s>>>(p);
     return cudaGetLastError();
 }
 
@@ -1154,12 +1160,9 @@ template <typename T>
 cudaError_t launch_fwd(FwdParams& p, cudaStream_t s) {
     const int c = p.s.cols, npc = sizeof(T) == 4 ? 2 : 1;
     p.units = npc * (p.s.gate ? 3 : p.s.f ? 2 : 1);
-#define SEAM_FWD(VPT, MAXT, D, MINB)                                                                              \
-    do {                                                                                                          \
-        const Form f{VPT, MAXT, D, MINB};                                                                         \
-        const unsigned grid = (unsigned)std::min<long long>(p.s.rows, (long long)sm_count() * f.blocks(c));       \
-        return seam_launch(seam_fwd_kernel<T, VPT, MAXT, D, MINB>, p, f, F_VECS, grid, s);                        \
-    } while (0)
+    p.vectors = p.s.post_bias || p.s.pre_bias ? F_VECS : F_POST_BIAS;
+#define SEAM_FWD(VPT, MAXT, D, MINB) \
+    return seam_launch(seam_fwd_kernel<T, VPT, MAXT, D, MINB>, p, Form{VPT, MAXT, D, MINB}, 0, s)
     if (c <= 256) SEAM_FWD(1, 32, 3, 32);
     if (c <= 512) SEAM_FWD(2, 32, 3, 24);
     if (c <= 768) SEAM_FWD(3, 32, 3, 20);
@@ -1170,17 +1173,25 @@ cudaError_t launch_fwd(FwdParams& p, cudaStream_t s) {
 #undef SEAM_FWD
 }
 
-template <typename T, bool ALL>
-cudaError_t launch_bwd(BwdParams& p, cudaStream_t s) {
+template <typename T, bool BIAS, bool GSUM>
+cudaError_t launch_bwd_form(BwdParams& p, cudaStream_t s) {
     const int c = p.s.cols, npc = sizeof(T) == 4 ? 2 : 1;
     p.units = 2 * npc + 1 + (p.s.gate ? npc : 0);
+    p.vectors = p.s.post_bias ? B_VECS : B_POST_BIAS;
 #define SEAM_BWD(VPT, MAXT, D, MINB)                                                                                    \
-    return seam_launch(seam_bwd_kernel<T, VPT, MAXT, D, MINB, ALL>, p, Form{VPT, MAXT, D, MINB}, B_VECS, (unsigned)p.plan.runs, s)
-    if (c <= 1024) SEAM_BWD(1, 128, 3, ALL ? 4 : 6);
-    if (c <= 4096) SEAM_BWD(2, 256, 2, ALL ? 1 : 2);
+    return seam_launch(seam_bwd_kernel<T, VPT, MAXT, D, MINB, BIAS, GSUM>, p, Form{VPT, MAXT, D, MINB}, p.plan.runs, s)
+    if (c <= 768) SEAM_BWD(1, 96, 3, BIAS || GSUM ? 6 : 8);
+    if (c <= 4096) SEAM_BWD(2, 256, 2, BIAS ? 1 : 2);
     if (c <= 8192) SEAM_BWD(2, 512, 2, 1);
     SEAM_BWD(2, 1024, 1, 1);
 #undef SEAM_BWD
+}
+
+template <typename T>
+cudaError_t launch_bwd(BwdParams& p, cudaStream_t s) {
+    const bool bias = p.s.d_post_bias || p.s.d_pre_bias;
+    if (p.gate_sums) return bias ? launch_bwd_form<T, true, true>(p, s) : launch_bwd_form<T, false, true>(p, s);
+    return bias ? launch_bwd_form<T, true, false>(p, s) : launch_bwd_form<T, false, false>(p, s);
 }
 
 cudaError_t launch_fwd_any(const FwdParams& p, int dt, cudaStream_t s) {
@@ -1301,9 +1312,9 @@ muon_status seam_backward(const muon_seam_grad* seam, muon_dtype x_dtype, muon_d
                          33.0 / 32 * ((q.dy ? 1 : 0) + (q.post_c.q ? 1 : 0))), s);
         cudaError_t e;
         if (!(p.vec && p.wvec && q.cols % 8 == 0)) e = launch_bwd_any(p, x_dtype, all, s);
-        else if (x_dtype == MUON_BF16) e = all ? launch_bwd<__nv_bfloat16, true>(p, s) : launch_bwd<__nv_bfloat16, false>(p, s);
-        else if (x_dtype == MUON_FP16) e = all ? launch_bwd<__half, true>(p, s) : launch_bwd<__half, false>(p, s);
-        else e = all ? launch_bwd<float, true>(p, s) : launch_bwd<float, false>(p, s);
+        else if (x_dtype == MUON_BF16) e = launch_bwd<__nv_bfloat16>(p, s);
+        else if (x_dtype == MUON_FP16) e = launch_bwd<__half>(p, s);
+        else e = launch_bwd<float>(p, s);
         trace_end(s);
         if (e != cudaSuccess) return MUON_ERR_CUDA;
     }
