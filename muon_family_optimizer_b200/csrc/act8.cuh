@@ -137,15 +137,27 @@ __device__ __forceinline__ bool act8_encode8(const float (&x)[8], int col, int n
     return byte != kActBad;
 }
 
-// The values of eight codes (two words) under an exponent byte.  A code's byte with the
-// sign bit flipped is q + 128, as the low bits of a float 2^23 + 128 + q; the difference
-// is q and q 2^e exact (a conversion instruction per code would take four times the issue time).
-__device__ __forceinline__ void act8_decode8(uint2 w, int byte, float (&v)[8]) {
-    const float s = byte == kActBad ? __uint_as_float(0x7FC00000u) : act8_scale(byte);
+// Eight codes (two words) as whole floats.  A code's byte with the sign bit flipped is
+// q + 128, as the low bits of a float 2^23 + 128 + q; the difference is q (a conversion
+// instruction per code would take four times the issue time).
+__device__ __forceinline__ void act8_whole8(uint2 w, float (&q)[8]) {
     const uint32_t u[2] = {w.x ^ 0x80808080u, w.y ^ 0x80808080u};
 #pragma unroll
     for (int i = 0; i < 8; ++i)
-        v[i] = (__uint_as_float(__byte_perm(u[i >> 2], 0x4B000000u, 0x7440 + (i & 3))) - 8388736.f) * s;
+        q[i] = __uint_as_float(__byte_perm(u[i >> 2], 0x4B000000u, 0x7440 + (i & 3))) - 8388736.f;
+}
+
+// 2^e of an exponent byte, NaN for a bad block's.
+__device__ __forceinline__ float act8_step(int byte) {
+    return byte == kActBad ? __uint_as_float(0x7FC00000u) : act8_scale(byte);
+}
+
+// The values of eight codes under an exponent byte.
+__device__ __forceinline__ void act8_decode8(uint2 w, int byte, float (&v)[8]) {
+    const float s = act8_step(byte);
+    act8_whole8(w, v);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] *= s;
 }
 
 // Codes col..col+7 of a row; those past the row read as 0.

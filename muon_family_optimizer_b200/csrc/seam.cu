@@ -237,19 +237,22 @@ enum FwdVec : int { F_POST_GAIN, F_PRE_GAIN, F_POST_BIAS, F_PRE_BIAS, F_VECS }; 
 
 constexpr int kRedBytes = 512;      // block_sum's areas
 
-// D rows are in flight or at work; MINB blocks of MAXT threads per SM bound the registers.
-template <typename T, int VPT, int MAXT, int D, int MINB>
+// D rows are in flight or at work; MINB blocks of MAXT threads per SM bound the registers.  WARP: every
+// warp of the block has rows of its own (rows of up to 1024 columns: no barriers, and the block's
+// warps share its vectors).
+template <typename T, int VPT, int MAXT, int D, int MINB, bool WARP>
 __global__ void __launch_bounds__(MAXT, MINB) seam_fwd_kernel(const __grid_constant__ FwdParams p) {
     constexpr int DT = DtOf<T>::v;
     constexpr int NPC = sizeof(T) == 4 ? 2 : 1, kF = NPC, kGate = 2 * NPC;        // units of a stage (x first)
     extern __shared__ __align__(16) uint8_t smem[];
     const muon_seam& S = p.s;
     float* red = reinterpret_cast<float*>(smem);
-    const int threads = blockDim.x, nw = threads >> 5, lane = threadIdx.x & 31;
+    const int lane = threadIdx.x & 31, threads = WARP ? 32 : blockDim.x, nw = threads >> 5;      // of a row
+    const int tr = WARP ? lane : (int)threadIdx.x;
     const bool has_f = S.f != nullptr, has_gate = S.gate != nullptr, has_pb = S.post_bias != nullptr;
     const bool has_yb = S.pre_bias != nullptr, unit_skip = S.skip == 1.f;
     const int post = S.post, pre = S.pre;
-    for (int i = threadIdx.x; i < kRedBytes / 4; i += threads) red[i] = 0.f;
+    for (int i = threadIdx.x; i < kRedBytes / 4; i += blockDim.x) red[i] = 0.f;
     // scale rides on the post-norm's vectors
     const Vectors V{p.vecs_in_smem ? reinterpret_cast<float*>(smem + kRedBytes) : nullptr, threads * VPT, p.w_dt};
     if (V.sm) {
@@ -258,26 +261,28 @@ __global__ void __launch_bounds__(MAXT, MINB) seam_fwd_kernel(const __grid_const
         if (has_pb) V.fill(F_POST_BIAS, S.post_bias, S.scale, S.cols);
         if (has_yb) V.fill(F_PRE_BIAS, S.pre_bias, 1.f, S.cols);
     }
-    const Ring<VPT> ring{smem + kRedBytes + (V.sm ? p.vectors * 32 * V.chunks : 0) + threadIdx.x * 16, threads * 16, p.units};
+    const Ring<VPT> ring{smem + kRedBytes + (V.sm ? p.vectors * 32 * V.chunks : 0) + threadIdx.x * 16, (int)blockDim.x * 16, p.units};
     int col[VPT];
     bool in[VPT];
 #pragma unroll
     for (int j = 0; j < VPT; ++j) {
-        col[j] = (j * threads + (int)threadIdx.x) * 8;
+        col[j] = (j * threads + tr) * 8;
         in[j] = col[j] < S.cols;
         if (!in[j])
             for (int u = 0; u < D * p.units; ++u) *reinterpret_cast<uint4*>(ring.at(0, u, j)) = make_uint4(0u, 0u, 0u, 0u);
     }
     __syncthreads();
-    const int r0 = (int)((long long)S.rows * blockIdx.x / gridDim.x), r1 = (int)((long long)S.rows * (blockIdx.x + 1) / gridDim.x);
+    const long long worker = WARP ? (long long)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5) : blockIdx.x;
+    const long long workers = WARP ? (long long)gridDim.x * (blockDim.x >> 5) : gridDim.x;
+    const int r0 = (int)(S.rows * worker / workers), r1 = (int)(S.rows * (worker + 1) / workers);
     // this thread's first chunk of the next row to copy, and of the row at work
-    const T* x = static_cast<const T*>(S.x) + r0 * S.ldx + threadIdx.x * 8;
-    const T* f = static_cast<const T*>(S.f) + r0 * S.ldf + threadIdx.x * 8;
+    const T* x = static_cast<const T*>(S.x) + r0 * S.ldx + tr * 8;
+    const T* f = static_cast<const T*>(S.f) + r0 * S.ldf + tr * 8;
     int grow = has_gate ? r0 / S.gate_rows : 0, gleft = has_gate ? S.gate_rows - r0 % S.gate_rows : 0;
-    const T* gate = static_cast<const T*>(S.gate) + grow * S.ldgate + threadIdx.x * 8;
-    T* out = static_cast<T*>(S.out) + r0 * S.ldout + threadIdx.x * 8;
-    T* y = static_cast<T*>(S.y) + r0 * S.ldy + threadIdx.x * 8;
-    signed char *pq = S.post_c.q + r0 * S.post_c.ldq + threadIdx.x * 8, *yq = S.pre_c.q + r0 * S.pre_c.ldq + threadIdx.x * 8;
+    const T* gate = static_cast<const T*>(S.gate) + grow * S.ldgate + tr * 8;
+    T* out = static_cast<T*>(S.out) + r0 * S.ldout + tr * 8;
+    T* y = static_cast<T*>(S.y) + r0 * S.ldy + tr * 8;
+    signed char *pq = S.post_c.q + r0 * S.post_c.ldq + tr * 8, *yq = S.pre_c.q + r0 * S.pre_c.ldq + tr * 8;
     unsigned char *pe = S.post_c.e + r0 * S.post_c.lde, *ye = S.pre_c.e + r0 * S.pre_c.lde;
     const bool keep_f = S.post_c.q != nullptr, keep_y = S.pre_c.q != nullptr;
     auto copy = [&](int row, int d) {
@@ -316,7 +321,7 @@ __global__ void __launch_bounds__(MAXT, MINB) seam_fwd_kernel(const __grid_const
             for (int j = 0; j < VPT; ++j) ring_get<DT, VPT>(ring, d, kF, j, u[j]);
             if (post != MUON_NORM_NONE) {
                 const float r = normalise<VPT>(u, in, post, S.eps, p.inv_c, red, slot, nw);
-                if (S.post_rstd && threadIdx.x == 0) S.post_rstd[row] = r;
+                if (S.post_rstd && tr == 0) S.post_rstd[row] = r;
             }
             if (keep_f) {
 #pragma unroll
@@ -367,7 +372,7 @@ __global__ void __launch_bounds__(MAXT, MINB) seam_fwd_kernel(const __grid_const
         }
         if (pre != MUON_NORM_NONE) {
             const float r = normalise<VPT>(v, in, pre, S.eps, p.inv_c, red, slot, nw);
-            if (S.pre_rstd && threadIdx.x == 0) S.pre_rstd[row] = r;
+            if (S.pre_rstd && tr == 0) S.pre_rstd[row] = r;
             if (keep_y) {
 #pragma unroll
                 for (int j = 0; j < VPT; ++j) {
@@ -1132,9 +1137,12 @@ int sm_count() {
 
 // One form of a kernel: chunks of 8 columns per thread, most threads, stages, blocks per SM that
 // its registers are bounded for.
+// (warp: a row per warp, blocks of maxt threads.)
 struct Form {
     int vpt, maxt, stages, per_sm;
-    int threads(int cols) const { return (cols + 256 * vpt - 1) / (256 * vpt) * 32; }
+    bool warp;
+    int row_threads(int cols) const { return warp ? 32 : (cols + 256 * vpt - 1) / (256 * vpt) * 32; }
+    int threads(int cols) const { return warp ? maxt : row_threads(cols); }
     // blocks that the registers of an SM take
     int blocks(int cols) const { return std::min(32, per_sm * maxt / threads(cols)); }
 };
@@ -1146,13 +1154,14 @@ struct Form {
 template <typename K, typename P>
 cudaError_t seam_launch(K kern, P& p, const Form& f, long long runs, cudaStream_t s) {
     const int t = f.threads(p.s.cols), most = f.blocks(p.s.cols), room = 227 * 1024;
-    const int ring = kRedBytes + f.stages * p.units * f.vpt * t * 16, vecs = p.vectors * 32 * f.vpt * t;
+    const int ring = kRedBytes + f.stages * p.units * f.vpt * t * 16, vecs = p.vectors * 32 * f.vpt * f.row_threads(p.s.cols);
     p.vecs_in_smem = ring + vecs + 1024 <= room;
     const int smem = ring + (p.vecs_in_smem ? vecs : 0);
     const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     const long long resident = (long long)sm_count() * std::max(1, std::min(most, room / (smem + 1024)));
-    kern<<<(unsigned)(runs ? runs : std::min<long long>(p.s.rows, resident)), t, smem, s>>>(p);
+    const long long most_blocks = (p.s.rows + t / f.row_threads(p.s.cols) - 1) / (t / f.row_threads(p.s.cols));
+    kern<<<(unsigned)(runs ? runs : std::min(most_blocks, resident)), t, smem, s>>>(p);
     return cudaGetLastError();
 }
 
@@ -1161,15 +1170,15 @@ cudaError_t launch_fwd(FwdParams& p, cudaStream_t s) {
     const int c = p.s.cols, npc = sizeof(T) == 4 ? 2 : 1;
     p.units = npc * (p.s.gate ? 3 : p.s.f ? 2 : 1);
     p.vectors = p.s.post_bias || p.s.pre_bias ? F_VECS : F_POST_BIAS;
-#define SEAM_FWD(VPT, MAXT, D, MINB) \
-    return seam_launch(seam_fwd_kernel<T, VPT, MAXT, D, MINB>, p, Form{VPT, MAXT, D, MINB}, 0, s)
-    if (c <= 256) SEAM_FWD(1, 32, 3, 32);
-    if (c <= 512) SEAM_FWD(2, 32, 3, 24);
-    if (c <= 768) SEAM_FWD(3, 32, 3, 20);
-    if (c <= 1024) SEAM_FWD(4, 32, 2, 16);
-    if (c <= 4096) SEAM_FWD(2, 256, 2, 3);
-    if (c <= 8192) SEAM_FWD(2, 512, 2, 1);
-    SEAM_FWD(2, 1024, 1, 1);
+#define SEAM_FWD(VPT, MAXT, D, MINB, WARP) \
+    return seam_launch(seam_fwd_kernel<T, VPT, MAXT, D, MINB, WARP>, p, Form{VPT, MAXT, D, MINB, WARP}, 0, s)
+    if (c <= 256) SEAM_FWD(1, 256, 3, 4, true);
+    if (c <= 512) SEAM_FWD(2, 256, 2, 3, true);
+    if (c <= 768) SEAM_FWD(3, 256, 2, 3, true);
+    if (c <= 1024) SEAM_FWD(4, 128, 2, 4, true);
+    if (c <= 4096) SEAM_FWD(2, 256, 2, 3, false);
+    if (c <= 8192) SEAM_FWD(2, 512, 2, 1, false);
+    SEAM_FWD(2, 1024, 1, 1, false);
 #undef SEAM_FWD
 }
 
@@ -1179,7 +1188,7 @@ cudaError_t launch_bwd_form(BwdParams& p, cudaStream_t s) {
     p.units = 2 * npc + 1 + (p.s.gate ? npc : 0);
     p.vectors = p.s.post_bias ? B_VECS : B_POST_BIAS;
 #define SEAM_BWD(VPT, MAXT, D, MINB)                                                                                    \
-    return seam_launch(seam_bwd_kernel<T, VPT, MAXT, D, MINB, BIAS, GSUM>, p, Form{VPT, MAXT, D, MINB}, p.plan.runs, s)
+    return seam_launch(seam_bwd_kernel<T, VPT, MAXT, D, MINB, BIAS, GSUM>, p, Form{VPT, MAXT, D, MINB, false}, p.plan.runs, s)
     if (c <= 768) SEAM_BWD(1, 96, 3, BIAS || GSUM ? 6 : 8);
     if (c <= 4096) SEAM_BWD(2, 256, 2, BIAS ? 1 : 2);
     if (c <= 8192) SEAM_BWD(2, 512, 2, 1);
