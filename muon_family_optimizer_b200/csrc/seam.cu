@@ -698,8 +698,71 @@ __global__ void __launch_bounds__(MAXT, MINB) seam_bwd_kernel(const __grid_const
 }
 
 // ---------------------------------------------------------------------------
-// Any rows: element by element
+// Any rows: element by element.  A lane takes one column of each of eight blocks of 32
+// columns, so that a warp's accesses are whole runs of 32 elements (eight
+// neighbouring columns per lane took 2.2 times as long backward at 16384 x 2900).
 // ---------------------------------------------------------------------------
+
+// (One choice of type around the eight accesses, which are then in flight together.)
+template <typename T>
+__device__ __forceinline__ void load_cols_t(const T* p, int c0, int cols, float (&v)[8]) {
+    T t[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) t[i] = c0 + 32 * i < cols ? p[32 * i] : from_float<T>(0.f);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = to_float(t[i]);
+}
+
+__device__ __forceinline__ void load_cols(const void* p, long long row_at, int c0, int cols, int dt, float (&v)[8]) {
+    if (dt == DT_BF16) load_cols_t(static_cast<const __nv_bfloat16*>(p) + row_at + c0, c0, cols, v);
+    else if (dt == DT_FP16) load_cols_t(static_cast<const __half*>(p) + row_at + c0, c0, cols, v);
+    else load_cols_t(static_cast<const float*>(p) + row_at + c0, c0, cols, v);
+}
+
+template <typename T>
+__device__ __forceinline__ void store_cols_t(T* p, int c0, int cols, const float (&v)[8]) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        if (c0 + 32 * i < cols) p[32 * i] = from_float<T>(v[i]);
+}
+
+__device__ __forceinline__ void store_cols(void* p, long long row_at, int c0, int cols, int dt, const float (&v)[8]) {
+    if (dt == DT_BF16) store_cols_t(static_cast<__nv_bfloat16*>(p) + row_at + c0, c0, cols, v);
+    else if (dt == DT_FP16) store_cols_t(static_cast<__half*>(p) + row_at + c0, c0, cols, v);
+    else store_cols_t(static_cast<float*>(p) + row_at + c0, c0, cols, v);
+}
+
+// Blocks of a checkpoint's row, a lane one column of each; false if one cannot be held.
+__device__ __forceinline__ bool encode_cols(const muon_act8& c, long long row, int c0, int cols, const float (&v)[8]) {
+    const int lane = threadIdx.x & 31;
+    signed char* q = c.q + row * c.ldq + c0;
+    unsigned char* e = c.e + row * c.lde + c0 / kActBlock;
+    bool ok = true;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const int byte = act8_exp_byte(__reduce_max_sync(0xFFFFFFFFu, __float_as_uint(fabsf(v[i]))));
+        const int code = byte == kActBad ? 0 : (int)act8_codes4(v[i], 0.f, 0.f, 0.f, act8_inv(byte));
+        ok = ok && byte != kActBad;
+        if (c0 + 32 * i < cols) {
+            q[32 * i] = (signed char)code;
+            if (lane == 0) e[i] = (unsigned char)byte;
+        }
+    }
+    return ok;
+}
+
+__device__ __forceinline__ void decode_cols(const muon_act8& c, long long row, int c0, int cols, float (&v)[8]) {
+    const signed char* qp = c.q + row * c.ldq + c0;
+    const unsigned char* ep = c.e + row * c.lde + c0 / kActBlock;
+    int q[8], e[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        q[i] = c0 + 32 * i < cols ? qp[32 * i] : 0;
+        e[i] = c0 + 32 * i < cols ? ep[i] : 127;
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = (float)q[i] * act8_step(e[i]);
+}
 
 __device__ __forceinline__ float round_dt(float v, int dt) {
     if (dt == DT_BF16) return __bfloat162float(__float2bfloat16_rn(v));
@@ -746,7 +809,7 @@ __device__ __forceinline__ void row_sum(float (&v)[N], float* red, int& slot) {
 // against their deviation exact; a sum of squares beyond fp32's range is formed
 // again at 2^-100.
 template <int TPR, int VPT>
-__device__ __forceinline__ float row_normalise(float (&v)[VPT][8], const int (&nv)[VPT], int kind, float eps,
+__device__ __forceinline__ float row_normalise(float (&v)[VPT][8], const int (&c0)[VPT], int cols, int kind, float eps,
                                                float inv_c, float* red, int& slot) {
     if (kind == MUON_NORM_LAYER) {
         float m[1] = {0.f};
@@ -758,7 +821,7 @@ __device__ __forceinline__ float row_normalise(float (&v)[VPT][8], const int (&n
 #pragma unroll
         for (int j = 0; j < VPT; ++j)
 #pragma unroll
-            for (int i = 0; i < 8; ++i) v[j][i] = i < nv[j] ? v[j][i] - m[0] : 0.f;
+            for (int i = 0; i < 8; ++i) v[j][i] = c0[j] + 32 * i < cols ? v[j][i] - m[0] : 0.f;
     }
     float s[1] = {0.f};
 #pragma unroll
@@ -786,20 +849,18 @@ __device__ __forceinline__ float row_normalise(float (&v)[VPT][8], const int (&n
     return r;
 }
 
-// u = n gain + bias on one chunk (either may be NULL)
-__device__ __forceinline__ void affine8(float (&v)[8], const void* gain, const void* bias, int col, int dt, bool vec,
-                                        int nvalid) {
+// u = n gain + bias (either may be NULL)
+__device__ __forceinline__ void affine_cols(float (&v)[8], const void* gain, const void* bias, int c0, int cols, int dt) {
+    float t[8];
     if (gain) {
-        float g[8];
-        load8_dt(gain, col, dt, vec, nvalid, g);
+        load_cols(gain, 0, c0, cols, dt, t);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] *= g[i];
+        for (int i = 0; i < 8; ++i) v[i] *= t[i];
     }
     if (bias) {
-        float b[8];
-        load8_dt(bias, col, dt, vec, nvalid, b);
+        load_cols(bias, 0, c0, cols, dt, t);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] += b[i];
+        for (int i = 0; i < 8; ++i) v[i] += t[i];
     }
 }
 
@@ -809,12 +870,10 @@ __global__ void __launch_bounds__(TPR == 32 ? 128 : TPR) seam_fwd_any(const __gr
     __shared__ float red[TPR > 32 ? 4 * (TPR / 32) : 1];
     const muon_seam& S = p.s;
     const int lane = threadIdx.x & 31, tr = threadIdx.x % TPR;
-    int col[VPT], nv[VPT];
+    const int cols = S.cols;
+    int c0[VPT];            // this lane's column of the first of a warp's eight blocks
 #pragma unroll
-    for (int j = 0; j < VPT; ++j) {
-        col[j] = (j * TPR + tr) * 8;
-        nv[j] = min(8, max(0, S.cols - col[j]));
-    }
+    for (int j = 0; j < VPT; ++j) c0[j] = (j * TPR + (tr & ~31)) * 8 + (tr & 31);
     int slot = 0;
     bool bad = false;
     for (long long row = (long long)blockIdx.x * RPB + threadIdx.x / TPR; row < S.rows;
@@ -822,46 +881,42 @@ __global__ void __launch_bounds__(TPR == 32 ? 128 : TPR) seam_fwd_any(const __gr
         float x[VPT][8], u[VPT][8];
 #pragma unroll
         for (int j = 0; j < VPT; ++j) {
-            load8_dt(S.x, row * S.ldx + col[j], DT, p.vec && nv[j] == 8, nv[j], x[j]);
-            if (S.f) load8_dt(S.f, row * S.ldf + col[j], DT, p.vec && nv[j] == 8, nv[j], u[j]);
+            load_cols(S.x, row * S.ldx, c0[j], cols, DT, x[j]);
+            if (S.f) load_cols(S.f, row * S.ldf, c0[j], cols, DT, u[j]);
         }
         if (S.f) {
             if (S.post != MUON_NORM_NONE) {
-                const float r = row_normalise<TPR, VPT>(u, nv, S.post, S.eps, p.inv_c, red, slot);
+                const float r = row_normalise<TPR, VPT>(u, c0, cols, S.post, S.eps, p.inv_c, red, slot);
                 if (S.post_rstd && tr == 0) S.post_rstd[row] = r;
             }
 #pragma unroll
             for (int j = 0; j < VPT; ++j) {
-                const bool vec = p.vec && nv[j] == 8, wvec = p.wvec && nv[j] == 8;
                 if (S.post_c.q)
-                    bad |= !act8_encode8(u[j], col[j], nv[j], S.post_c.q + row * S.post_c.ldq,
-                                         S.post_c.e + row * S.post_c.lde, lane);
-                affine8(u[j], S.post_gain, S.post_bias, col[j], p.w_dt, wvec, nv[j]);
+                    bad |= !encode_cols(S.post_c, row, c0[j], cols, u[j]);
+                affine_cols(u[j], S.post_gain, S.post_bias, c0[j], cols, p.w_dt);
                 if (S.gate) {
                     float g[8];
-                    load8_dt(S.gate, (row / S.gate_rows) * S.ldgate + col[j], DT, vec, nv[j], g);
+                    load_cols(S.gate, (row / S.gate_rows) * S.ldgate, c0[j], cols, DT, g);
 #pragma unroll
                     for (int i = 0; i < 8; ++i) u[j][i] *= g[i];
                 }
 #pragma unroll
                 for (int i = 0; i < 8; ++i)
                     x[j][i] = round_dt(fmaf(S.scale, u[j][i], S.skip * x[j][i]), DT);
-                if (nv[j] < 8)
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) x[j][i] = i < nv[j] ? x[j][i] : 0.f;
-                store8_dt(S.out, row * S.ldout + col[j], DT, vec, nv[j], x[j]);
+                for (int i = 0; i < 8; ++i) x[j][i] = c0[j] + 32 * i < cols ? x[j][i] : 0.f;
+                store_cols(S.out, row * S.ldout, c0[j], cols, DT, x[j]);
             }
         }
         if (S.pre != MUON_NORM_NONE) {
-            const float r = row_normalise<TPR, VPT>(x, nv, S.pre, S.eps, p.inv_c, red, slot);
+            const float r = row_normalise<TPR, VPT>(x, c0, cols, S.pre, S.eps, p.inv_c, red, slot);
             if (S.pre_rstd && tr == 0) S.pre_rstd[row] = r;
 #pragma unroll
             for (int j = 0; j < VPT; ++j) {
                 if (S.pre_c.q)
-                    bad |= !act8_encode8(x[j], col[j], nv[j], S.pre_c.q + row * S.pre_c.ldq,
-                                         S.pre_c.e + row * S.pre_c.lde, lane);
-                affine8(x[j], S.pre_gain, S.pre_bias, col[j], p.w_dt, p.wvec && nv[j] == 8, nv[j]);
-                store8_dt(S.y, row * S.ldy + col[j], DT, p.vec && nv[j] == 8, nv[j], x[j]);
+                    bad |= !encode_cols(S.pre_c, row, c0[j], cols, x[j]);
+                affine_cols(x[j], S.pre_gain, S.pre_bias, c0[j], cols, p.w_dt);
+                store_cols(S.y, row * S.ldy, c0[j], cols, DT, x[j]);
             }
         }
     }
@@ -873,12 +928,10 @@ __global__ void __launch_bounds__(TPR) seam_bwd_any(const __grid_constant__ BwdP
     __shared__ float red[TPR > 32 ? 4 * (TPR / 32) : 1];
     const muon_seam_grad& S = p.s;
     const int tr = threadIdx.x;
-    int col[VPT], nv[VPT];
+    const int cols = S.cols;
+    int c0[VPT];            // this lane's column of the first of a warp's eight blocks
 #pragma unroll
-    for (int j = 0; j < VPT; ++j) {
-        col[j] = (j * TPR + tr) * 8;
-        nv[j] = min(8, max(0, S.cols - col[j]));
-    }
+    for (int j = 0; j < VPT; ++j) c0[j] = (j * TPR + (tr & ~31)) * 8 + (tr & 31);
     long long r0, r1;
     if (p.plan.parts == 0) {
         r0 = (long long)blockIdx.x * p.plan.run_rows;
@@ -896,7 +949,7 @@ __global__ void __launch_bounds__(TPR) seam_bwd_any(const __grid_constant__ BwdP
         float d[VPT][8];
 #pragma unroll
         for (int j = 0; j < VPT; ++j) {
-            if (S.dout) load8_dt(S.dout, row * S.lddout + col[j], DT, p.vec && nv[j] == 8, nv[j], d[j]);
+            if (S.dout) load_cols(S.dout, row * S.lddout, c0[j], cols, DT, d[j]);
             else
 #pragma unroll
                 for (int i = 0; i < 8; ++i) d[j][i] = 0.f;
@@ -906,16 +959,14 @@ __global__ void __launch_bounds__(TPR) seam_bwd_any(const __grid_constant__ BwdP
             float sums[2] = {0.f, 0.f};
 #pragma unroll
             for (int j = 0; j < VPT; ++j) {
-                const bool vec = p.vec && nv[j] == 8;
-                load8_dt(S.dy, row * S.lddy + col[j], DT, vec, nv[j], g[j]);
-                act8_decode8(act8_load8(S.pre_c.q + row * S.pre_c.ldq, col[j], nv[j]),
-                             nv[j] > 0 ? S.pre_c.e[row * S.pre_c.lde + col[j] / kActBlock] : 127, n[j]);
+                load_cols(S.dy, row * S.lddy, c0[j], cols, DT, g[j]);
+                decode_cols(S.pre_c, row, c0[j], cols, n[j]);
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
                     a_pg[j][i] = fmaf(g[j][i], n[j][i], a_pg[j][i]);
                     if constexpr (ALL) a_pb[j][i] += g[j][i];
                 }
-                affine8(g[j], S.pre_gain, nullptr, col[j], p.w_dt, p.wvec && nv[j] == 8, nv[j]);
+                affine_cols(g[j], S.pre_gain, nullptr, c0[j], cols, p.w_dt);
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
                     sums[0] = fmaf(g[j][i], n[j][i], sums[0]);
@@ -929,7 +980,7 @@ __global__ void __launch_bounds__(TPR) seam_bwd_any(const __grid_constant__ BwdP
             for (int j = 0; j < VPT; ++j)
 #pragma unroll
                 for (int i = 0; i < 8; ++i)        // columns beyond the row stay out of the sums over it
-                    d[j][i] = i < nv[j] ? fmaf(r, fmaf(-n[j][i], s1, g[j][i] - s0), d[j][i]) : 0.f;
+                    d[j][i] = c0[j] + 32 * i < cols ? fmaf(r, fmaf(-n[j][i], s1, g[j][i] - s0), d[j][i]) : 0.f;
         }
         if (S.df) {
             float n[VPT][8], h[VPT][8];
@@ -937,10 +988,8 @@ __global__ void __launch_bounds__(TPR) seam_bwd_any(const __grid_constant__ BwdP
             const long long grow = S.gate ? row / S.gate_rows : 0;
 #pragma unroll
             for (int j = 0; j < VPT; ++j) {
-                const bool vec = p.vec && nv[j] == 8, wvec = p.wvec && nv[j] == 8;
                 if (post_c)
-                    act8_decode8(act8_load8(S.post_c.q + row * S.post_c.ldq, col[j], nv[j]),
-                                 nv[j] > 0 ? S.post_c.e[row * S.post_c.lde + col[j] / kActBlock] : 127, n[j]);
+                    decode_cols(S.post_c, row, c0[j], cols, n[j]);
                 else
 #pragma unroll
                     for (int i = 0; i < 8; ++i) n[j][i] = 0.f;
@@ -948,15 +997,15 @@ __global__ void __launch_bounds__(TPR) seam_bwd_any(const __grid_constant__ BwdP
                 for (int i = 0; i < 8; ++i) h[j][i] = S.scale * d[j][i];
                 if (S.gate) {
                     float g[8];
-                    load8_dt(S.gate, grow * S.ldgate + col[j], DT, vec, nv[j], g);
+                    load_cols(S.gate, grow * S.ldgate, c0[j], cols, DT, g);
                     if (S.dgate) {
                         float t[8];
 #pragma unroll
                         for (int i = 0; i < 8; ++i) t[i] = n[j][i];
-                        affine8(t, S.post_gain, S.post_bias, col[j], p.w_dt, wvec, nv[j]);
+                        affine_cols(t, S.post_gain, S.post_bias, c0[j], cols, p.w_dt);
 #pragma unroll
                         for (int i = 0; i < 8; ++i) t[i] *= h[j][i];
-                        if (!p.gate_sums) store8_dt(S.dgate, grow * S.lddgate + col[j], DT, vec, nv[j], t);
+                        if (!p.gate_sums) store_cols(S.dgate, grow * S.lddgate, c0[j], cols, DT, t);
                         if constexpr (ALL)
 #pragma unroll
                             for (int i = 0; i < 8; ++i) a_gt[j][i] += t[i];
@@ -969,7 +1018,7 @@ __global__ void __launch_bounds__(TPR) seam_bwd_any(const __grid_constant__ BwdP
                     a_qg[j][i] = fmaf(h[j][i], n[j][i], a_qg[j][i]);
                     if constexpr (ALL) a_qb[j][i] += h[j][i];
                 }
-                affine8(h[j], S.post_gain, nullptr, col[j], p.w_dt, wvec, nv[j]);
+                affine_cols(h[j], S.post_gain, nullptr, c0[j], cols, p.w_dt);
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
                     sums[0] = fmaf(h[j][i], n[j][i], sums[0]);
@@ -987,20 +1036,20 @@ __global__ void __launch_bounds__(TPR) seam_bwd_any(const __grid_constant__ BwdP
             }
 #pragma unroll
             for (int j = 0; j < VPT; ++j)
-                store8_dt(S.df, row * S.lddf + col[j], DT, p.vec && nv[j] == 8, nv[j], h[j]);
+                store_cols(S.df, row * S.lddf, c0[j], cols, DT, h[j]);
         }
 #pragma unroll
         for (int j = 0; j < VPT; ++j) {
 #pragma unroll
             for (int i = 0; i < 8; ++i) d[j][i] *= S.skip;
-            store8_dt(S.dx, row * S.lddx + col[j], DT, p.vec && nv[j] == 8, nv[j], d[j]);
+            store_cols(S.dx, row * S.lddx, c0[j], cols, DT, d[j]);
         }
         if constexpr (ALL) {
             if (p.gate_sums && p.plan.parts == 0 && ((row + 1) % S.gate_rows == 0 || row + 1 == S.rows)) {
                 const long long grow = row / S.gate_rows;
 #pragma unroll
                 for (int j = 0; j < VPT; ++j) {
-                    store8_dt(S.dgate, grow * S.lddgate + col[j], DT, p.vec && nv[j] == 8, nv[j], a_gt[j]);
+                    store_cols(S.dgate, grow * S.lddgate, c0[j], cols, DT, a_gt[j]);
 #pragma unroll
                     for (int i = 0; i < 8; ++i) a_gt[j][i] = 0.f;
                 }
@@ -1008,8 +1057,7 @@ __global__ void __launch_bounds__(TPR) seam_bwd_any(const __grid_constant__ BwdP
         }
     }
     auto put = [&](int v, const float (&a)[8], int j) {
-        store8_dt(p.part, ((long long)v * p.plan.runs + blockIdx.x) * S.cols + col[j], DT_FP32,
-                  (S.cols & 3) == 0 && nv[j] == 8, nv[j], a);
+        store_cols(p.part, ((long long)v * p.plan.runs + blockIdx.x) * cols, c0[j], cols, DT_FP32, a);
     };
 #pragma unroll
     for (int j = 0; j < VPT; ++j) {
