@@ -61,6 +61,11 @@ struct Cfg {
     static constexpr int kSmem = 1024 + kExpOffset + kRaw * kExpBytes + 512;
     static_assert(kConvGroups == kBStages && kBStages <= kAStages && kConvGroups < kRaw, "see the converters");
 };
+// The tensor cores' accumulation truncates: every 16 tokens cost up to a unit in the last place of the running sum,
+// towards zero (measured 1.7e-8 relative per step, 4e-5 over 40,000 terms).  An fp32 G is therefore summed in segments of
+// kSeg k-blocks, 6e-6, that are added rounded to nearest; for a 16-bit G (half a unit 2^-9 or 2^-12) 65,536
+// tokens are one segment.
+constexpr int kSeg32 = 96, kSeg16 = 1024;
 constexpr int kPlanSms = 148;           // work lists are planned for a whole B200, so a size query needs no device
 
 struct GradItem {
@@ -86,6 +91,7 @@ struct GradItem {
 struct GradParams {
     GradItem it[kItems];
     int n, w_dt;
+    int seg;                            // k-blocks summed in tensor memory before the sum goes on in fp32 (kSeg)
     long long whole_works, works;       // whole tiles of every layer, then the ranges of the tail tiles
     int* d_status;
 };
@@ -183,10 +189,11 @@ __device__ __forceinline__ void convert32(const uint4& a, const uint4& b, int by
     for (int g = 0; g < 4; ++g) o[g] = make_uint4(r[g][0], r[g][1], r[g][2], r[g][3]);
 }
 
-// gain, shift and beta on a thread's four rows (row + 8 u) of eight columns, in the
+// gain, shift and beta (first segment; later ones add to G) on a thread's four rows (row + 8 u) of eight columns, in the
 // accumulator's register order (tmem_ld_16x256b_x4_twice, convert32).
 template <int WDT>
-__device__ __forceinline__ void edit_rows(const GradItem& I, int row, int col, bool vec, int nv, float (&v)[32]) {
+__device__ __forceinline__ void edit_rows(const GradItem& I, int row, int col, bool vec, int nv, bool first,
+                                          float (&v)[32]) {
     constexpr int at[8] = {0, 4, 1, 5, 8, 12, 9, 13};
     const int out = I.out;
     if (I.gain) {
@@ -197,7 +204,7 @@ __device__ __forceinline__ void edit_rows(const GradItem& I, int row, int col, b
 #pragma unroll
             for (int i = 0; i < 8; ++i) v[16 * (u >> 1) + 2 * (u & 1) + at[i]] *= g[i];
     }
-    if (I.shift) {
+    if (I.shift && first) {
         float s[8];
         load8_dt(I.shift, col, WDT, false, nv, s);
 #pragma unroll
@@ -210,19 +217,30 @@ __device__ __forceinline__ void edit_rows(const GradItem& I, int row, int col, b
             }
         }
     }
-    const float beta = I.beta;
-    if (beta != 0.f)
+    const float beta = first ? I.beta : 1.f;
+    if (beta != 0.f) {
+        const long long at_row = (long long)row * I.cols + col, step = 8LL * I.cols;
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
-            if (row + 8 * u >= out) continue;
-            float g[8];
-            load8_dt(I.G, (long long)(row + 8 * u) * I.cols + col, WDT, vec, nv, g);
+        for (int h = 0; h < 2; ++h) {
+            Raw8<WDT> raw[2];                   // two rows' loads in flight together (four would spill)
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                float& x = v[16 * (u >> 1) + 2 * (u & 1) + at[i]];
-                x = fmaf(beta, g[i], x);
+            for (int k = 0; k < 2; ++k)
+                raw[k].load(static_cast<const char*>(I.G) + (at_row + (2 * h + k) * step) * (WDT == DT_FP32 ? 4 : 2),
+                            vec && row + 8 * (2 * h + k) < out);
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                const int u = 2 * h + k;
+                float g[8];
+                raw[k].get(g);
+                if (!vec) load8_dt(I.G, at_row + u * step, WDT, false, row + 8 * u < out ? nv : 0, g);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    float& x = v[16 * (u >> 1) + 2 * (u & 1) + at[i]];
+                    x = fmaf(beta, g[i], x);
+                }
             }
         }
+    }
 }
 
 template <typename T, int MH, int WDT>
@@ -318,14 +336,15 @@ __global__ void __launch_bounds__(kThreads, 1) act8_grad_kernel(const __grid_con
             int as = 0, bs = 0, it = 0;
             uint32_t aphase = 0, bphase = 0;
             bool ok = true;
-            for (long long w = unit; ok && w < p.works; w += nunits, ++it) {
-                const Work k = decode_work(p, w);
-                const int buf = it % kBufs;
+            for (long long w = unit; ok && w < p.works; w += nunits) {
+              const Work k = decode_work(p, w);
+              for (int s0 = k.kb0; ok && s0 < k.kb1; s0 += p.seg, ++it) {
+                const int s1 = min(k.kb1, s0 + p.seg), buf = it % kBufs;
                 ok = __all_sync(0xFFFFFFFFu, mbar_wait(&tempty_bar[buf], ((it / kBufs) & 1) ^ 1, abort_flag, d_status));
                 if (!ok) break;
                 tc_fence_after();
                 const uint32_t d_tmem = tmem_base + (uint32_t)(buf * kBN);
-                for (int kb = k.kb0; kb < k.kb1; ++kb) {
+                for (int kb = s0; kb < s1; ++kb) {
                     bool ready = mbar_try_wait(&afull_bar[as], aphase) && mbar_try_wait(&bfull_bar[bs], bphase);
                     if (!__all_sync(0xFFFFFFFFu, ready)) {
                         ready = mbar_wait(&afull_bar[as], aphase, abort_flag, d_status) &&
@@ -341,7 +360,7 @@ __global__ void __launch_bounds__(kThreads, 1) act8_grad_kernel(const __grid_con
 #pragma unroll
                             for (int h = 0; h < MH; ++h)
                                 tc_mma_f16_pair(d_tmem + h * kBN, da + (h * kBM * kBK * 2 >> 4) + s * (2048 >> 4),
-                                                db + s * (2048 >> 4), idesc, kb > k.kb0 || s > 0 ? 1u : 0u);
+                                                db + s * (2048 >> 4), idesc, kb > s0 || s > 0 ? 1u : 0u);
                         tc_commit_pair_multicast(smem_u32(&done_bar[as]), 3);
                     }
                     __syncwarp();
@@ -351,6 +370,7 @@ __global__ void __launch_bounds__(kThreads, 1) act8_grad_kernel(const __grid_con
                 if (!ok) break;
                 if (elect_one()) tc_commit_pair_multicast(smem_u32(&tfull_bar[buf]), 3);
                 __syncwarp();
+              }
             }
             // no MMA may still be writing tensor memory when it is freed
             if (elect_one()) tc_commit_pair(smem_u32(drain_bar));
@@ -363,16 +383,19 @@ __global__ void __launch_bounds__(kThreads, 1) act8_grad_kernel(const __grid_con
         // ---------------------------------------------------- epilogue
         const int quad = warp & 3, part = (warp - 2) >> 2;
         int it = 0;
-        for (long long w = unit; w < p.works; w += nunits, ++it) {
-            const Work k = decode_work(p, w);
-            const GradItem& I = p.it[k.item];
+        bool ok = true;
+        for (long long w = unit; ok && w < p.works; w += nunits) {
+          const Work k = decode_work(p, w);
+          const GradItem& I = p.it[k.item];
+          for (int s0 = k.kb0; s0 < k.kb1; s0 += p.seg, ++it) {
             const int buf = it % kBufs;
-            if (!mbar_wait(&tfull_bar[buf], (it / kBufs) & 1, abort_flag, d_status)) break;
+            if (!mbar_wait(&tfull_bar[buf], (it / kBufs) & 1, abort_flag, d_status)) { ok = false; break; }
             tc_fence_after();
+            const bool first = s0 == k.kb0;         // later segments are added to G
             // the layer's fields in registers: the loop's fences would have them read again for every row
             const int out = I.out, cols = I.cols;
             const bool whole = k.slot < 0;
-            const bool edit = whole && (I.gain || I.shift || I.beta != 0.f), wide = !whole || I.vec;
+            const bool edit = whole && (I.gain || I.shift || I.beta != 0.f || !first), wide = !whole || I.vec;
             // G, or the part's own 256 MH x 256 tile
             const int width = whole ? cols : kBN, esz = whole ? (WDT == DT_FP32 ? 4 : 2) : 4;
             const int row_at = whole ? k.ti * MH * 2 * kBM : 0, col_at = whole ? k.tj * kBN : 0;
@@ -391,7 +414,7 @@ __global__ void __launch_bounds__(kThreads, 1) act8_grad_kernel(const __grid_con
                 char* dst = base + ((long long)(row_at + lr + (lane >> 2)) * width + col_at + lc + (lane & 3) * 8) * esz;
                 float v[32];
                 tmem_ld_16x256b_x4_twice(tmem_base + ((uint32_t)(quad * 32) << 16) + (uint32_t)((buf + h) * kBN + lc), v);
-                if (edit) edit_rows<WDT>(I, row0 + (lane >> 2), c0 + (lane & 3) * 8, vec, nv, v);
+                if (edit) edit_rows<WDT>(I, row0 + (lane >> 2), c0 + (lane & 3) * 8, vec, nv, first, v);
 #pragma unroll
                 for (int u = 0; u < 4; ++u, dst += step) {
                     const int z = 16 * (u >> 1) + 2 * (u & 1);
@@ -405,6 +428,7 @@ __global__ void __launch_bounds__(kThreads, 1) act8_grad_kernel(const __grid_con
             __syncwarp();
             // only this warp's accumulator reads have to be over, not its stores
             if (lane == 0) mbar_arrive_cluster_cta(mapa_shared(smem_u32(&tempty_bar[buf]), 0));
+          }
         }
     } else if (warp < 2 + kEpiWarps + kConvWarps) {
         // ---------------------------------------------------- converters
@@ -530,8 +554,9 @@ __global__ void __launch_bounds__(kThreads, 1) act8_grad_kernel(const __grid_con
 
 // ---------------------------------------------------------------------------
 // Copies of dY the tensor maps can read: rows that are not 16-byte aligned, and
-// fp32 rows as three bfloat16 parts hi + mid + lo (8 significant bits each,
-// so the three hold all 24; a part of a non-finite value keeps it in hi).
+// fp32 rows as three bfloat16 parts lo + mid + hi (8 significant bits each, so the
+// three hold all 24; a non-finite value is kept in hi), summed in that order: the small
+// parts meet a small running sum.
 // ---------------------------------------------------------------------------
 struct CopyItem {
     const void* src;
@@ -575,7 +600,7 @@ __global__ void __launch_bounds__(256) act8_copy_kernel(const __grid_constant__ 
             }
 #pragma unroll
             for (int k = 0; k < 3; ++k)
-                *reinterpret_cast<uint4*>(dst + k * I.part_stride) = make_uint4(o[k][0], o[k][1], o[k][2], o[k][3]);
+                *reinterpret_cast<uint4*>(dst + (2 - k) * I.part_stride) = make_uint4(o[k][0], o[k][1], o[k][2], o[k][3]);
         } else {
             const unsigned short* src = static_cast<const unsigned short*>(I.src) + row * I.ld + col;
             uint32_t o[4];
@@ -618,21 +643,23 @@ __global__ void __launch_bounds__(256) act8_join_kernel(const __grid_constant__ 
                     s[0] += a.x; s[1] += a.y; s[2] += a.z; s[3] += a.w;
                     s[4] += b.x; s[5] += b.y; s[6] += b.z; s[7] += b.w;
                 }
+                // fp32 rows of 8 k + 4 columns end inside a group
+                const int nv = min(8, I.cols - col);
                 float g8[8];
                 if (I.gain) {
-                    load8_dt(I.gain, col, w_dt, true, 8, g8);
+                    load8_dt(I.gain, col, w_dt, nv == 8, nv, g8);
 #pragma unroll
                     for (int j = 0; j < 8; ++j) s[j] *= g8[j];
                 }
                 if (I.shift)
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) s[j] = fmaf(d, ld_elem(I.shift, col + j, w_dt), s[j]);
+                    for (int j = 0; j < 8; ++j) s[j] = fmaf(d, j < nv ? ld_elem(I.shift, col + j, w_dt) : 0.f, s[j]);
                 if (I.beta != 0.f) {
-                    load8_dt(I.G, at + col, w_dt, true, 8, g8);
+                    load8_dt(I.G, at + col, w_dt, nv == 8, nv, g8);
 #pragma unroll
                     for (int j = 0; j < 8; ++j) s[j] = fmaf(I.beta, g8[j], s[j]);
                 }
-                store8_dt(I.G, at + col, w_dt, true, 8, s);
+                store8_dt(I.G, at + col, w_dt, nv == 8, nv, s);
             } else {
                 float s[8] = {};
 #pragma unroll 2
@@ -684,7 +711,7 @@ bool aligned_G(const muon_act8_grad_item& q, int w_dt) {
 
 struct Plan {
     int mh;                                       // MMAs that share a converted operand: tiles of 256 mh x 256
-    int whole[kItems], tail[kItems], splits[kItems], len;
+    int whole[kItems], tail[kItems], splits[kItems], len, seg;
     long long copy_at[kItems], part_at[kItems];   // workspace offsets (-1: none)
     long long bytes;
 };
@@ -709,6 +736,11 @@ void plan_batch(const muon_act8_grad_item* items, int n, int dt, int w_dt, Plan&
         longest = std::max(longest, total[i]);
         any_unaligned |= !aligned_G(items[i], w_dt);
     }
+    P.seg = w_dt == DT_FP32 ? kSeg32 : kSeg16;
+    if (longest > P.seg) {                          // equal segments of the longest sum
+        const int n_seg = (longest + P.seg - 1) / P.seg;
+        P.seg = (longest + n_seg - 1) / n_seg;
+    }
     double best = -1.0;
     long long best_whole = 0;
     int best_s = 1;
@@ -718,12 +750,13 @@ void plan_batch(const muon_act8_grad_item* items, int n, int dt, int w_dt, Plan&
         for (int i = 0; i < n; ++i)
             tiles += (long long)((items[i].out + mh * 2 * kBM - 1) / (mh * 2 * kBM)) * ((items[i].c.cols + kBN - 1) / kBN);
         const double kb_us = mh == 2 ? 0.73 : 0.48, tile_us = mh, part_us = mh * 4.0 * 2 * kBM * kBN * 2 / 3e6;
-        for (int s = 1; s <= (int)pairs && s <= std::max(1, longest); ++s) {
+        for (int s = 1; s <= std::max((int)pairs, (longest + P.seg - 1) / P.seg) && s <= std::max(1, longest); ++s) {
             const int len = std::max(1, (longest + s - 1) / s);
             long long whole = s == 1 ? tiles : tiles / pairs * pairs;
-            if (any_unaligned) whole = 0;
+            if (any_unaligned || (w_dt != DT_FP32 && longest > P.seg)) whole = 0;
             const long long tail = tiles - whole;
-            const double us = std::ceil((double)whole / pairs) * (longest * kb_us + tile_us) +
+            if (tail && len > P.seg) continue;              // a part is one segment
+            const double us = std::ceil((double)whole / pairs) * (longest * kb_us + tile_us * ((longest + P.seg - 1) / P.seg)) +
                               (tail ? std::ceil((double)(tail * s) / pairs) * (len * kb_us + tile_us) + tail * s * part_us + 4.0 : 0.0);
             if (best < 0.0 || us < best) {
                 best = us; best_whole = whole; best_s = s; P.mh = mh;
@@ -845,6 +878,7 @@ muon_status run_batch(const muon_act8_grad_item* items, int n, int dt, int w_dt,
     }
     prm.n = n;
     prm.w_dt = w_dt;
+    prm.seg = P.seg;
     prm.d_status = d_status;
     int dev = 0, nsm = kPlanSms;
     cudaGetDevice(&dev);

@@ -223,6 +223,16 @@ def test_grad_strided_and_unaligned_dY(dt, pad, base):
     _run_and_check([it])
 
 
+@pytest.mark.parametrize("O,C", [(130, 308), (512, 308), (70, 4), (300, 1284)])
+def test_grad_rows_that_end_inside_a_group_of_eight(O, C):
+    # fp32 rows of 8 k + 4 columns are 16-byte aligned; over many tokens they go through the join, over few not
+    for T in (40, 1984):
+        for beta in (0.0, 1.0):
+            it, buf = _case(T, O, C, torch.float16, torch.float32, seed=C, gain=True, shift=beta != 0, beta=beta)
+            _run_and_check([it])
+            assert bool((buf[O * C:] == GUARD).all())
+
+
 def test_grad_without_tokens_writes_zeros():
     it, buf = _case(0, 130, 70, torch.bfloat16, torch.bfloat16)
     it["G"].fill_(float("nan"))
@@ -258,6 +268,25 @@ def test_grad_equal_inputs_give_equal_bits():
 def test_grad_long_sum():
     it, _ = _case(20001, 96, 64, torch.bfloat16, torch.float32, seed=9)
     _run_and_check([it])
+
+
+@pytest.mark.parametrize("dt", [torch.bfloat16, torch.float32])
+def test_grad_long_sums_of_many_tiles_do_not_shrink(dt):
+    # Whole tiles over 24576 tokens, with an fp32 G (81 tiles, so their tokens are not split).  The tensor cores truncate
+    # the running sum at every 16 tokens, on average by half of at most 2^-23: over n steps of a sum that grows like a
+    # random walk n 2^-24 2/3 of the result.  Segments hold at most 96 x 4 steps (a third of them in the hi parts of an fp32
+    # dY): 1.6e-5; one sum over all 1536 steps measured 2.6e-5.
+    T, O, C = 24576, 4608, 2304
+    g = torch.Generator(device="cuda").manual_seed(3)
+    c = _ckpt_of(torch.randn(T, C, generator=g, device="cuda"))
+    dY = torch.randn(T, O, generator=g, device="cuda").to(dt)
+    G = torch.empty(O, C, device="cuda")
+    items = [dict(dY=dY, G=G, **c)]
+    mo.act8_grad_batched(items, _ws(items))
+    X = torch.empty(T, C, device="cuda")
+    mo.act8_decode_batched([dict(x=X, **c)])
+    ref = dY.double().T @ X.double()
+    assert float((G.double() - ref).norm() / ref.norm()) <= 1.6e-5
 
 
 def test_grad_extreme_exponents():
