@@ -19,6 +19,7 @@ vector parameters in one step), :func:`limuon_step_batched` and
 import ctypes
 import math
 import os
+import struct
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 # the library next to this file; MUON_B200_LIB names another build of it (A/B comparisons)
@@ -452,71 +453,111 @@ ACT8_BLOCK = 32
 NORMS = {"none": 0, "rms": 1, "layer": 2}
 SEAM_MAX_COLS = 16384
 
+# The descriptors' native layouts, filled in one call each (field by field they cost more than a
+# small launch); the layouts themselves are those of the Structures above.
+_ACT8 = "iiPqPq"
+_PACK_ITEM = struct.Struct("@" + _ACT8 + "Pq")
+_PACK_GRAD = struct.Struct("@" + _ACT8 + "PqiPPPPf")
+_PACK_SEAM = struct.Struct("@iiiifffPqPqPqiPPPPPqPq" + 2 * _ACT8 + "PP")
+_PACK_SEAM_GRAD = struct.Struct("@iiiiffPqiPPP" + 2 * _ACT8 + "PPPqPqPqPqPqPPPPf")
+_NO_ACT8 = (0, 0, 0, 0, 0, 0)
+_codes = None
+
+
+def _code(dtype):
+    """Library code of a tensor's dtype."""
+    global _codes
+    if _codes is None:
+        import torch
+        _codes = {torch.bfloat16: BF16, torch.float16: FP16, torch.float32: FP32}
+    code = _codes.get(dtype)
+    if code is None:
+        raise ValueError(f"unsupported dtype {dtype}")
+    return code
+
 
 def act8_empty(rows, cols, device="cuda"):
     """An 8-bit activation checkpoint of a rows x cols matrix, not yet written:
     dict(q=int8 codes with 16-byte aligned rows, e=uint8 exponents of the blocks of 32 columns)."""
     import torch
-    q = torch.empty(rows, (cols + 15) // 16 * 16, dtype=torch.int8, device=device)
-    return dict(q=q[:, :cols], e=torch.empty(rows, (cols + ACT8_BLOCK - 1) // ACT8_BLOCK, dtype=torch.uint8,
-                                             device=device))
+    ld = (cols + 15) // 16 * 16
+    q = torch.empty(rows, ld, dtype=torch.int8, device=device)
+    return dict(q=q if ld == cols else q[:, :cols],
+                e=torch.empty(rows, (cols + ACT8_BLOCK - 1) // ACT8_BLOCK, dtype=torch.uint8, device=device))
 
 
-def _row_stride(t, where, rows=None, cols=None, dtype=None):
-    """Row stride (elements) of a 2-D tensor on the current device whose rows are contiguous."""
+def _device(t, where):
+    """Index of the current CUDA device, which t must be on."""
     import torch
-    if t.dim() != 2 or (rows is not None and tuple(t.shape) != (rows, cols)):
-        raise ValueError(f"{where}: expected a {rows} x {cols} tensor, got {tuple(t.shape)}")
-    if dtype is not None and t.dtype != dtype:
-        raise ValueError(f"{where}: expected {dtype}, got {t.dtype}")
-    _on_device(t, where)
-    if t.shape[0] == 0 or t.shape[1] == 0:
-        return t.shape[1]
-    if t.shape[1] > 1 and t.stride(1) != 1 or t.shape[0] > 1 and t.stride(0) < t.shape[1]:
-        raise ValueError(f"{where}: rows must be contiguous and not overlap")
-    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1])
-
-
-def _on_device(t, where):
-    import torch
-    if not t.is_cuda or t.device.index != torch.cuda.current_device():
+    dev = t.get_device()
+    if dev < 0 or dev != torch.cuda.current_device():
         raise ValueError(f"{where}: must be a tensor of the current CUDA device, is on {t.device}")
+    return dev
 
 
-def _vector(t, where, n, dtype):
-    """Address of a contiguous vector of n values, or None."""
+def _refuse(t, where, dev, rows, cols, dtype):
+    if t.get_device() != dev:
+        raise ValueError(f"{where}: must be a tensor of the current CUDA device, is on {t.device}")
+    raise ValueError(f"{where}: expected a {rows} x {cols} tensor of {dtype}, got {tuple(t.shape)} of {t.dtype}")
+
+
+def _matrix(t, where, dev, rows, cols, dtype):
+    """(address, row stride in elements) of a rows x cols matrix whose rows are contiguous."""
+    shape = t.shape
+    if len(shape) != 2 or shape[0] != rows or shape[1] != cols or t.dtype != dtype or t.get_device() != dev:
+        _refuse(t, where, dev, rows, cols, dtype)
+    if t.is_contiguous():
+        return t.data_ptr(), cols
+    s0, s1 = t.stride()
+    if cols > 1 and s1 != 1 or rows > 1 and s0 < cols:
+        raise ValueError(f"{where}: rows must be contiguous and not overlap")
+    return t.data_ptr(), s0 if rows > 1 else cols
+
+
+def _vector(t, where, dev, n, dtype):
+    """Address of a contiguous vector of n values, 0 for None."""
     if t is None:
-        return None
-    _on_device(t, where)
-    if t.numel() != n or not t.is_contiguous() or t.dtype != dtype:
+        return 0
+    if t.numel() != n or t.dtype != dtype or t.get_device() != dev or not t.is_contiguous():
+        if t.get_device() != dev:
+            raise ValueError(f"{where}: must be a tensor of the current CUDA device, is on {t.device}")
         raise ValueError(f"{where}: expected {n} contiguous values of {dtype}")
     return t.data_ptr()
 
 
-def _act8(q, e, where, rows=None, cols=None):
+def _act8(q, e, where, dev, rows, cols):
+    """The fields of a checkpoint of rows x cols."""
     import torch
-    rows, cols = (q.shape if q.dim() == 2 else (-1, -1)) if rows is None else (rows, cols)
-    ldq = _row_stride(q, where + " q", rows, cols, torch.int8)
-    blocks = (cols + ACT8_BLOCK - 1) // ACT8_BLOCK
-    lde = _row_stride(e, where + " e", rows, blocks, torch.uint8)
-    if rows <= 1:                      # the only row's stride means nothing
+    qp, ldq = _matrix(q, where + " q", dev, rows, cols, torch.int8)
+    ep, lde = _matrix(e, where + " e", dev, rows, (cols + ACT8_BLOCK - 1) // ACT8_BLOCK, torch.uint8)
+    if rows == 0:
+        return 0, cols, 0, (cols + 15) // 16 * 16, 0, lde
+    if rows == 1:                      # the only row's stride means nothing
         ldq = (cols + 15) // 16 * 16
-    if rows and (ldq % 16 or q.data_ptr() % 16):
+    if ldq % 16 or qp % 16:
         raise ValueError(f"{where}: q needs 16-byte aligned rows (see act8_empty)")
-    return Act8(rows, cols, q.data_ptr() if rows else None, ldq, e.data_ptr() if rows else None, lde)
+    return rows, cols, qp, ldq, ep, lde
+
+
+def _rows_cols(t, where):
+    if t.dim() != 2:
+        raise ValueError(f"{where}: must be 2-D")
+    return t.shape
 
 
 def make_act8_items(items):
     """items: list of dicts with a checkpoint's q and e (see act8_empty) and x, the matrix it is
     made from or decoded into; all x of one dtype, rows contiguous (any row stride)."""
     arr = (Act8Item * len(items))()
+    arr.x_dtype = BF16
+    if items:
+        dt, dev = items[0]["x"].dtype, _device(items[0]["x"], "item 0 x")
+        arr.x_dtype = _code(dt)
     for i, p in enumerate(items):
         x, where = p["x"], f"item {i}"
-        if x.dtype != items[0]["x"].dtype:
-            raise ValueError(f"{where}: every x of a call has one dtype")
-        c = _act8(p["q"], p["e"], where)
-        arr[i] = Act8Item(c, x.data_ptr(), _row_stride(x, where + " x", c.rows, c.cols))
-    arr.x_dtype = _dtype_code(items[0]["x"].dtype) if len(items) else BF16
+        rows, cols = _rows_cols(x, where + " x")
+        _PACK_ITEM.pack_into(arr, i * _PACK_ITEM.size, *_act8(p["q"], p["e"], where, dev, rows, cols),
+                             *_matrix(x, where + " x", dev, rows, cols, dt))
     return arr
 
 
@@ -540,25 +581,25 @@ def make_act8_grads(items):
     shift) and beta (default 0); all dY of one dtype, all G of one dtype."""
     import torch
     arr = (Act8GradItem * len(items))()
+    arr.dy_dtype = arr.w_dtype = BF16
+    if items:
+        dt, wt, dev = items[0]["dY"].dtype, items[0]["G"].dtype, _device(items[0]["dY"], "item 0 dY")
+        arr.dy_dtype, arr.w_dtype = _code(dt), _code(wt)
+    size = ctypes.sizeof(Act8GradItem)
     for i, p in enumerate(items):
-        dY, G, where = p["dY"], p["G"], f"item {i}"
-        if dY.dtype != items[0]["dY"].dtype or G.dtype != items[0]["G"].dtype:
-            raise ValueError(f"{where}: every dY, and every G, of a call has one dtype")
-        c = _act8(p["q"], p["e"], where)
-        if dY.dim() != 2:
-            raise ValueError(f"{where} dY: must be 2-D")
-        out = dY.shape[1]
-        lddy = _row_stride(dY, where + " dY", c.rows, out)
-        _row_stride(G, where + " G", out, c.cols)
-        if not G.is_contiguous():
+        dY, G, q, where = p["dY"], p["G"], p["q"], f"item {i}"
+        rows, out = _rows_cols(dY, where + " dY")
+        cols = _rows_cols(q, where + " q")[1]
+        get = p.get
+        g, ldg = _matrix(G, where + " G", dev, out, cols, wt)
+        if ldg != cols:
             raise ValueError(f"{where} G: must be contiguous")
-        arr[i] = Act8GradItem(c, dY.data_ptr(), lddy, out, G.data_ptr(),
-                              _vector(p.get("gain"), where + " gain", c.cols, G.dtype),
-                              _vector(p.get("shift"), where + " shift", c.cols, G.dtype),
-                              _vector(p.get("dy_sum"), where + " dy_sum", out, torch.float32),
-                              float(p.get("beta", 0.0)))
-    arr.dy_dtype = _dtype_code(items[0]["dY"].dtype) if len(items) else BF16
-    arr.w_dtype = _dtype_code(items[0]["G"].dtype) if len(items) else BF16
+        dy, lddy = _matrix(dY, where + " dY", dev, rows, out, dt)
+        _PACK_GRAD.pack_into(arr, i * size, *_act8(q, p["e"], where, dev, rows, cols), dy, lddy, out, g,
+                             _vector(get("gain"), where + " gain", dev, cols, wt),
+                             _vector(get("shift"), where + " shift", dev, cols, wt),
+                             _vector(get("dy_sum"), where + " dy_sum", dev, out, torch.float32),
+                             get("beta", 0.0))
     return arr
 
 
@@ -581,37 +622,42 @@ def act8_grad_batched(items, workspace=None, d_status=None, stream=None):
                                    _stream_ptr(stream)), "act8_grad_batched")
 
 
-_NO_ACT8 = Act8(0, 0, None, 0, None, 0)
-
-
-def _seam_common(s, lead):
-    """(rows, cols, x dtype, w dtype, post, pre, matrix(), vector(), checkpoint()) of a seam's dict."""
+def _seam_common(s, name):
+    """(rows, cols, dtype codes, matrix(), vector(), rstd(), checkpoint(), norm(), gate rows) of a seam's dict."""
     import torch
-    rows, cols = lead.shape if lead.dim() == 2 else (-1, -1)
-    vecs = [s[k] for k in ("post_gain", "post_bias", "pre_gain", "pre_bias", "d_post_gain", "d_post_bias",
-                           "d_pre_gain", "d_pre_bias") if s.get(k) is not None]
-    wt = vecs[0].dtype if vecs else lead.dtype
+    get, lead = s.get, s[name]
+    rows, cols = _rows_cols(lead, name)
+    dt, dev = lead.dtype, _device(lead, name)
+    wt = dt
+    for k in ("post_gain", "post_bias", "pre_gain", "pre_bias", "d_post_gain", "d_post_bias", "d_pre_gain", "d_pre_bias"):
+        t = get(k)
+        if t is not None:
+            wt = t.dtype
+            break
+    gr = get("gate_rows") or 1
+    if gr < 1:
+        raise ValueError("gate_rows: must be at least 1")
 
     def matrix(k, n=rows):
-        t = s.get(k)
-        return (None, 0) if t is None else (t.data_ptr(), _row_stride(t, k, n, cols, lead.dtype))
+        t = get(k)
+        return (0, 0) if t is None else _matrix(t, k, dev, n, cols, dt)
+
+    def vector(k):
+        return _vector(get(k), k, dev, cols, wt)
+
+    def rstd(k):
+        return _vector(get(k), k, dev, rows, torch.float32)
 
     def checkpoint(k):
-        c = s.get(k)
-        return _NO_ACT8 if c is None else _act8(c["q"], c["e"], k, rows, cols)
+        c = get(k)
+        return _NO_ACT8 if c is None else _act8(c["q"], c["e"], k, dev, rows, cols)
 
     def norm(k):
-        kind = s.get(k, "none")
+        kind = get(k, "none")
         if kind not in NORMS:
             raise ValueError(f"{k}: must be one of {sorted(NORMS)}")
         return NORMS[kind]
-
-    gr = int(s.get("gate_rows") or 1)
-    if gr < 1:
-        raise ValueError("gate_rows: must be at least 1")
-    return dict(rows=rows, cols=cols, wt=wt, norm=norm, matrix=matrix, checkpoint=checkpoint, gate_rows=gr,
-                gate_len=-(-rows // gr), vector=lambda k: _vector(s.get(k), k, cols, wt),
-                rstd=lambda k: _vector(s.get(k), k, rows, torch.float32))
+    return rows, cols, (_code(dt), _code(wt)), matrix, vector, rstd, checkpoint, norm, gr
 
 
 def make_seam(s):
@@ -619,13 +665,14 @@ def make_seam(s):
     gate_rows, post and pre ("none", "rms" or "layer"), post_gain, post_bias, pre_gain, pre_bias (cols
     values of one dtype), eps, skip, scale; outputs out, y, post_c and pre_c (checkpoints, see
     act8_empty), post_rstd and pre_rstd (rows float32 values).  Matrices: x's dtype, rows contiguous."""
-    h = _seam_common(s, s["x"])
-    m, v = h["matrix"], h["vector"]
-    d = Seam(h["rows"], h["cols"], h["norm"]("post"), h["norm"]("pre"), float(s.get("eps", 1e-5)),
-             float(s.get("skip", 1.0)), float(s.get("scale", 1.0)), *m("x"), *m("f"), *m("gate", h["gate_len"]),
-             h["gate_rows"], v("post_gain"), v("post_bias"), v("pre_gain"), v("pre_bias"), *m("out"), *m("y"),
-             h["checkpoint"]("post_c"), h["checkpoint"]("pre_c"), h["rstd"]("post_rstd"), h["rstd"]("pre_rstd"))
-    d.x_dtype, d.w_dtype = _dtype_code(s["x"].dtype), _dtype_code(h["wt"])
+    rows, cols, codes, m, v, rstd, ckpt, norm, gr = _seam_common(s, "x")
+    get = s.get
+    d = Seam()
+    _PACK_SEAM.pack_into(d, 0, rows, cols, norm("post"), norm("pre"), get("eps", 1e-5), get("skip", 1.0),
+                         get("scale", 1.0), *m("x"), *m("f"), *m("gate", -(-rows // gr)), gr, v("post_gain"),
+                         v("post_bias"), v("pre_gain"), v("pre_bias"), *m("out"), *m("y"), *ckpt("post_c"),
+                         *ckpt("pre_c"), rstd("post_rstd"), rstd("pre_rstd"))
+    d.x_dtype, d.w_dtype = codes
     return d
 
 
@@ -644,15 +691,15 @@ def make_seam_grad(s):
     by seam_forward; dy and dout, the gradients of y and of out; outputs df, dgate (as gate),
     d_post_gain, d_post_bias, d_pre_gain, d_pre_bias (cols values of the gains' dtype) and beta
     (default 0) that scales what those four held."""
-    h = _seam_common(s, s["dx"])
-    m, v = h["matrix"], h["vector"]
-    d = SeamGrad(h["rows"], h["cols"], h["norm"]("post"), h["norm"]("pre"), float(s.get("skip", 1.0)),
-                 float(s.get("scale", 1.0)), *m("gate", h["gate_len"]), h["gate_rows"], v("post_gain"),
-                 v("post_bias"), v("pre_gain"), h["checkpoint"]("post_c"), h["checkpoint"]("pre_c"),
-                 h["rstd"]("post_rstd"), h["rstd"]("pre_rstd"), *m("dy"), *m("dout"), *m("dx"), *m("df"),
-                 *m("dgate", h["gate_len"]), v("d_post_gain"), v("d_post_bias"), v("d_pre_gain"), v("d_pre_bias"),
-                 float(s.get("beta", 0.0)))
-    d.x_dtype, d.w_dtype = _dtype_code(s["dx"].dtype), _dtype_code(h["wt"])
+    rows, cols, codes, m, v, rstd, ckpt, norm, gr = _seam_common(s, "dx")
+    get, n = s.get, -(-rows // gr)
+    d = SeamGrad()
+    _PACK_SEAM_GRAD.pack_into(d, 0, rows, cols, norm("post"), norm("pre"), get("skip", 1.0), get("scale", 1.0),
+                              *m("gate", n), gr, v("post_gain"), v("post_bias"), v("pre_gain"), *ckpt("post_c"),
+                              *ckpt("pre_c"), rstd("post_rstd"), rstd("pre_rstd"), *m("dy"), *m("dout"), *m("dx"),
+                              *m("df"), *m("dgate", n), v("d_post_gain"), v("d_post_bias"), v("d_pre_gain"),
+                              v("d_pre_bias"), get("beta", 0.0))
+    d.x_dtype, d.w_dtype = codes
     return d
 
 

@@ -46,6 +46,30 @@ def test_struct_layouts_match_header(tmp_path):
             assert ctypes.sizeof(STRUCTS[key]) == int(val), key
 
 
+@pytest.mark.parametrize("pack,cls", [(mo._PACK_ITEM, mo.Act8Item), (mo._PACK_GRAD, mo.Act8GradItem),
+                                      (mo._PACK_SEAM, mo.Seam), (mo._PACK_SEAM_GRAD, mo.SeamGrad)])
+def test_packed_descriptors_match_the_structures(pack, cls):
+    # distinct values through the binding's one-call layouts come back out of the right fields
+    flat = []
+
+    def fields(c, prefix=""):
+        for n, t in c._fields_:
+            if t is mo.Act8:
+                yield from fields(t, prefix + n + ".")
+            else:
+                yield prefix + n, t
+    names = list(fields(cls))
+    flat = [float(i) + 0.5 if t is ctypes.c_float else i + 1 for i, (_, t) in enumerate(names)]
+    obj = cls()
+    pack.pack_into(obj, 0, *flat)
+    assert ctypes.sizeof(cls) - pack.size < 8
+    for (name, _), want in zip(names, flat):
+        got = obj
+        for part in name.split("."):
+            got = getattr(got, part)
+        assert got == want, name
+
+
 def _ckpt(**kw):
     d = dict(rows=4, cols=40, q=P, ldq=48, e=P, lde=2)
     d.update(kw)
