@@ -14,7 +14,8 @@
 // Two forms of each pass.  Where every row can be read in 16-byte pieces, a block
 // has exactly the warps its rows need, and each thread copies its own pieces of the next
 // rows into shared memory (cp.async, no barrier: nobody else reads them) while it
-// works on this one.  Other rows (seam_*_any) are read element by element.
+// works on this one.  Rows of other alignments (ANY) are copied as 4-byte words by the warp that
+// works on them and written element by element.
 #include <algorithm>
 #include <cmath>
 
@@ -116,12 +117,11 @@ __device__ __forceinline__ void block_sum(float (&v)[N], float* red, int& slot, 
     }
 }
 
-// Normalise the row in v (columns beyond the row hold 0 and stay 0, `in` tells them):
-// returns the reciprocal deviation.  The two-pass variance keeps rows whose mean is large
+// Normalise the row in v (columns beyond the row, nv columns into a chunk, hold 0 and stay 0): returns the reciprocal deviation.  The two-pass variance keeps rows whose mean is large
 // against their deviation exact; a sum of squares beyond fp32's range is formed again
 // at 2^-100.
 template <int VPT>
-__device__ __forceinline__ float normalise(float (&v)[VPT][8], const bool (&in)[VPT], int kind, float eps, float inv_c,
+__device__ __forceinline__ float normalise(float (&v)[VPT][8], const int (&nv)[VPT], int kind, float eps, float inv_c,
                                            float* red, int& slot, int nw) {
     if (kind == MUON_NORM_LAYER) {
         float m[1] = {0.f};
@@ -133,7 +133,7 @@ __device__ __forceinline__ float normalise(float (&v)[VPT][8], const bool (&in)[
 #pragma unroll
         for (int j = 0; j < VPT; ++j)
 #pragma unroll
-            for (int i = 0; i < 8; ++i) v[j][i] = in[j] ? v[j][i] - m[0] : 0.f;
+            for (int i = 0; i < 8; ++i) v[j][i] = i < nv[j] ? v[j][i] - m[0] : 0.f;
     }
     float s[1] = {0.f};
 #pragma unroll
@@ -168,6 +168,7 @@ __device__ __forceinline__ float normalise(float (&v)[VPT][8], const bool (&in)[
 struct Vectors {
     float* sm;              // NULL: global
     int chunks, dt;         // chunks of a vector in shared memory: those of all threads
+    int cols, vec;          // vec: 16-byte accesses of whole chunks
     __device__ __forceinline__ void get(int slot, const void* g, float mul, int col, bool in, float (&v)[8]) const {
         if (sm) {
             const float4 a = *reinterpret_cast<const float4*>(sm + 2 * slot * chunks * 4 + col / 2);
@@ -180,16 +181,16 @@ struct Vectors {
     }
     __device__ __forceinline__ void load(const void* g, float mul, int col, bool in, float (&v)[8]) const {
         if (g) {
-            load8_dt(g, col, dt, in, 0, v);
+            load8_dt(g, col, dt, in && vec, in ? min(8, cols - col) : 0, v);
 #pragma unroll
             for (int i = 0; i < 8; ++i) v[i] *= mul;
         } else {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] = in ? mul : 0.f;
+            for (int i = 0; i < 8; ++i) v[i] = in ? mul : 0.f;      // beyond the row's end it meets zeros
         }
     }
     // fill one vector of `cols` columns (before a barrier)
-    __device__ __forceinline__ void fill(int slot, const void* g, float mul, int cols) const {
+    __device__ __forceinline__ void fill(int slot, const void* g, float mul) const {
         for (int c = threadIdx.x; c < chunks; c += blockDim.x) {
             float v[8];
             load(g, mul, c * 8, c * 8 < cols, v);
@@ -225,6 +226,83 @@ __device__ __forceinline__ void ring_get(const Ring<VPT>& ring, int d, int u, in
     r.get(v);
 }
 
+// Rows of any alignment (ANY).  The 256 columns of a warp's chunk are copied by its lanes in
+// turn as the aligned 4-byte words that hold them, and written back through shared memory as
+// whole runs of elements; a warp exchanges its data only with itself.  A row of 16-bit
+// elements that starts in the middle of a word (`shift`) is read two bytes on, and the word behind the
+// warp's 512 bytes has a place of its own.
+template <typename T, int VPT>
+struct AnyRow {
+    const Ring<VPT>& ring;
+    uint32_t* extra;        // this warp's words behind its chunks: one per piece of the ring, `warps` apart
+    int warps, lane;
+
+    __device__ __forceinline__ uint32_t* behind(int d, int u, int j) const {
+        return extra + ((d * ring.units + u) * VPT + j) * warps;
+    }
+    // columns seg .. seg + 255 of a row
+    __device__ __forceinline__ void copy(int d, int u, int j, const T* row, int seg, int cols) const {
+        const uintptr_t a = reinterpret_cast<uintptr_t>(row + seg);
+        uint8_t* base = ring.at(d, u, j) - lane * 16;
+        if constexpr (sizeof(T) == 4) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const int c = i * 32 + lane;
+                if (seg + c < cols)
+                    cp_async4(ring.at(d, u + ((c >> 2) & 1), j) - lane * 16 + (c >> 3) * 16 + (c & 3) * 4,
+                              reinterpret_cast<const void*>(a + 4 * c), 4u);
+            }
+        } else {
+            const int bytes = (int)(a & 2) + 2 * min(256, cols - seg);      // from the first word on
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int w = (i * 32 + lane) * 4;
+                if (w < bytes) cp_async4(base + w, reinterpret_cast<const void*>((a & ~uintptr_t(3)) + w), 4u);
+            }
+            if (lane == 0 && bytes > 512) cp_async4(behind(d, u, j), reinterpret_cast<const void*>((a & ~uintptr_t(3)) + 512), 4u);
+        }
+    }
+    // this lane's eight columns, nv of them in the row
+    __device__ __forceinline__ void get(int d, int u, int j, const T* row, int nv, float (&v)[8]) const {
+        constexpr int DT = DtOf<T>::v;
+        Raw8<DT> r;
+#pragma unroll
+        for (int n = 0; n < Raw8<DT>::N; ++n) r.w[n] = *reinterpret_cast<const uint4*>(ring.at(d, u + n, j));
+        if constexpr (sizeof(T) == 2) {
+            if (reinterpret_cast<uintptr_t>(row) & 2) {
+                const uint32_t next = lane < 31 ? *reinterpret_cast<const uint32_t*>(ring.at(d, u, j) + 16) : *behind(d, u, j);
+                uint4& w = r.w[0];
+                w = make_uint4(__byte_perm(w.x, w.y, 0x5432), __byte_perm(w.y, w.z, 0x5432), __byte_perm(w.z, w.w, 0x5432),
+                               __byte_perm(w.w, next, 0x5432));
+            }
+        }
+        r.get(v);
+        if (nv < 8)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] = i < nv ? v[i] : 0.f;
+    }
+    // write the columns through the places of the first stream's pieces, which have been read
+    template <typename U>
+    __device__ __forceinline__ void put(int d, int j, U* row, int seg, int cols, const float (&v)[8]) const {
+        Raw8<DtOf<U>::v> o;
+        o.set(v);
+        __syncwarp();
+#pragma unroll
+        for (int n = 0; n < o.N; ++n) *reinterpret_cast<uint4*>(ring.at(d, n, j)) = o.w[n];
+        __syncwarp();
+        if (seg < cols) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const int c = i * 32 + lane;
+                const uint8_t* p = sizeof(U) == 4 ? ring.at(d, (c >> 2) & 1, j) - lane * 16 + (c >> 3) * 16 + (c & 3) * 4
+                                                  : ring.at(d, 0, j) - lane * 16 + c * 2;
+                if (seg + c < cols) row[seg + c] = *reinterpret_cast<const U*>(p);
+            }
+        }
+        __syncwarp();
+    }
+};
+
 struct FwdParams {
     muon_seam s;
     float inv_c;
@@ -240,7 +318,7 @@ constexpr int kRedBytes = 512;      // block_sum's areas
 // D rows are in flight or at work; MINB blocks of MAXT threads per SM bound the registers.  WARP: every
 // warp of the block has rows of its own (rows of up to 1024 columns: no barriers, and the block's
 // warps share its vectors).
-template <typename T, int VPT, int MAXT, int D, int MINB, bool WARP>
+template <typename T, int VPT, int MAXT, int D, int MINB, bool WARP, bool ANY>
 __global__ void __launch_bounds__(MAXT, MINB) seam_fwd_kernel(const __grid_constant__ FwdParams p) {
     constexpr int DT = DtOf<T>::v;
     constexpr int NPC = sizeof(T) == 4 ? 2 : 1, kF = NPC, kGate = 2 * NPC;        // units of a stage (x first)
@@ -254,34 +332,39 @@ __global__ void __launch_bounds__(MAXT, MINB) seam_fwd_kernel(const __grid_const
     const int post = S.post, pre = S.pre;
     for (int i = threadIdx.x; i < kRedBytes / 4; i += blockDim.x) red[i] = 0.f;
     // scale rides on the post-norm's vectors
-    const Vectors V{p.vecs_in_smem ? reinterpret_cast<float*>(smem + kRedBytes) : nullptr, threads * VPT, p.w_dt};
+    const Vectors V{p.vecs_in_smem ? reinterpret_cast<float*>(smem + kRedBytes) : nullptr, threads * VPT, p.w_dt, S.cols, !ANY};
     if (V.sm) {
-        V.fill(F_POST_GAIN, S.post_gain, S.scale, S.cols);
-        V.fill(F_PRE_GAIN, S.pre_gain, 1.f, S.cols);
-        if (has_pb) V.fill(F_POST_BIAS, S.post_bias, S.scale, S.cols);
-        if (has_yb) V.fill(F_PRE_BIAS, S.pre_bias, 1.f, S.cols);
+        V.fill(F_POST_GAIN, S.post_gain, S.scale);
+        V.fill(F_PRE_GAIN, S.pre_gain, 1.f);
+        if (has_pb) V.fill(F_POST_BIAS, S.post_bias, S.scale);
+        if (has_yb) V.fill(F_PRE_BIAS, S.pre_bias, 1.f);
     }
     const Ring<VPT> ring{smem + kRedBytes + (V.sm ? p.vectors * 32 * V.chunks : 0) + threadIdx.x * 16, (int)blockDim.x * 16, p.units};
-    int col[VPT];
+    int col[VPT], nv[VPT];
     bool in[VPT];
 #pragma unroll
     for (int j = 0; j < VPT; ++j) {
         col[j] = (j * threads + tr) * 8;
         in[j] = col[j] < S.cols;
+        nv[j] = max(0, min(8, S.cols - col[j]));
         if (!in[j])
             for (int u = 0; u < D * p.units; ++u) *reinterpret_cast<uint4*>(ring.at(0, u, j)) = make_uint4(0u, 0u, 0u, 0u);
     }
+    uint8_t* after = smem + kRedBytes + (V.sm ? p.vectors * 32 * V.chunks : 0) + D * p.units * VPT * blockDim.x * 16;
+    const AnyRow<T, VPT> any{ring, reinterpret_cast<uint32_t*>(after) + (threadIdx.x >> 5), (int)blockDim.x >> 5, lane};
+    const int seg0 = (tr - lane) * 8;                      // the warp's first column of a chunk
     __syncthreads();
     const long long worker = WARP ? (long long)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5) : blockIdx.x;
     const long long workers = WARP ? (long long)gridDim.x * (blockDim.x >> 5) : gridDim.x;
     const int r0 = (int)(S.rows * worker / workers), r1 = (int)(S.rows * (worker + 1) / workers);
     // this thread's first chunk of the next row to copy, and of the row at work
-    const T* x = static_cast<const T*>(S.x) + r0 * S.ldx + tr * 8;
-    const T* f = static_cast<const T*>(S.f) + r0 * S.ldf + tr * 8;
+    const int t8 = ANY ? 0 : tr * 8;
+    const T* x = static_cast<const T*>(S.x) + r0 * S.ldx + t8;
+    const T* f = static_cast<const T*>(S.f) + r0 * S.ldf + t8;
     int grow = has_gate ? r0 / S.gate_rows : 0, gleft = has_gate ? S.gate_rows - r0 % S.gate_rows : 0;
-    const T* gate = static_cast<const T*>(S.gate) + grow * S.ldgate + tr * 8;
-    T* out = static_cast<T*>(S.out) + r0 * S.ldout + tr * 8;
-    T* y = static_cast<T*>(S.y) + r0 * S.ldy + tr * 8;
+    const T* gate = static_cast<const T*>(S.gate) + grow * S.ldgate + t8;
+    T* out = static_cast<T*>(S.out) + r0 * S.ldout + t8;
+    T* y = static_cast<T*>(S.y) + r0 * S.ldy + t8;
     signed char *pq = S.post_c.q + r0 * S.post_c.ldq + tr * 8, *yq = S.pre_c.q + r0 * S.pre_c.ldq + tr * 8;
     unsigned char *pe = S.post_c.e + r0 * S.post_c.lde, *ye = S.pre_c.e + r0 * S.pre_c.lde;
     const bool keep_f = S.post_c.q != nullptr, keep_y = S.pre_c.q != nullptr;
@@ -289,6 +372,14 @@ __global__ void __launch_bounds__(MAXT, MINB) seam_fwd_kernel(const __grid_const
         if (row < r1) {
 #pragma unroll
             for (int j = 0; j < VPT; ++j) {
+                if constexpr (ANY) {
+                    const int seg = seg0 + j * threads * 8;
+                    if (seg >= S.cols) continue;
+                    any.copy(d, 0, j, x, seg, S.cols);
+                    if (has_f) any.copy(d, kF, j, f, seg, S.cols);
+                    if (has_gate) any.copy(d, kGate, j, gate, seg, S.cols);
+                    continue;
+                }
                 if (!in[j]) continue;
 #pragma unroll
                 for (int n = 0; n < NPC; ++n) {
@@ -314,13 +405,17 @@ __global__ void __launch_bounds__(MAXT, MINB) seam_fwd_kernel(const __grid_const
     for (int row = r0; row < r1; ++row) {
         copy(row + D - 1, d == 0 ? D - 1 : d - 1);
         cp_async_wait<D - 1>();
+        if (ANY) __syncwarp();                              // the other lanes' copies too
         float v[VPT][8];
         if (has_f) {
             float u[VPT][8];
 #pragma unroll
-            for (int j = 0; j < VPT; ++j) ring_get<DT, VPT>(ring, d, kF, j, u[j]);
+            for (int j = 0; j < VPT; ++j) {
+                if constexpr (ANY) any.get(d, kF, j, static_cast<const T*>(S.f) + row * S.ldf, nv[j], u[j]);
+                else ring_get<DT, VPT>(ring, d, kF, j, u[j]);
+            }
             if (post != MUON_NORM_NONE) {
-                const float r = normalise<VPT>(u, in, post, S.eps, p.inv_c, red, slot, nw);
+                const float r = normalise<VPT>(u, nv, post, S.eps, p.inv_c, red, slot, nw);
                 if (S.post_rstd && tr == 0) S.post_rstd[row] = r;
             }
             if (keep_f) {
@@ -329,7 +424,10 @@ __global__ void __launch_bounds__(MAXT, MINB) seam_fwd_kernel(const __grid_const
                     uint2 w;
                     const int byte = act8_quantise8(u[j], w);
                     bad |= byte == kActBad;
-                    if (in[j]) {
+                    if (ANY && nv[j] < 8) {
+                        for (int i = 0; i < nv[j]; ++i) pq[j * threads * 8 + i] = (signed char)((i < 4 ? w.x : w.y) >> (8 * (i & 3)));
+                        if ((lane & 3) == 0 && in[j]) pe[col[j] / kActBlock] = (unsigned char)byte;
+                    } else if (in[j]) {
                         *reinterpret_cast<uint2*>(pq + j * threads * 8) = w;
                         if ((lane & 3) == 0) pe[col[j] / kActBlock] = (unsigned char)byte;
                     }
@@ -348,12 +446,16 @@ __global__ void __launch_bounds__(MAXT, MINB) seam_fwd_kernel(const __grid_const
 #pragma unroll
                     for (int i = 0; i < 8; ++i) u[j][i] += t[i];
                 }
-                ring_get<DT, VPT>(ring, d, 0, j, v[j]);
+                if constexpr (ANY) any.get(d, 0, j, static_cast<const T*>(S.x) + row * S.ldx, nv[j], v[j]);
+                else ring_get<DT, VPT>(ring, d, 0, j, v[j]);
                 if (!unit_skip)
 #pragma unroll
                     for (int i = 0; i < 8; ++i) v[j][i] *= S.skip;
                 if (has_gate) {
-                    ring_get<DT, VPT>(ring, d, kGate, j, t);
+                    if constexpr (ANY)
+                        any.get(d, kGate, j, static_cast<const T*>(S.gate) + (row / S.gate_rows) * S.ldgate, nv[j], t);
+                    else
+                        ring_get<DT, VPT>(ring, d, kGate, j, t);
 #pragma unroll
                     for (int i = 0; i < 8; ++i) v[j][i] = fmaf(u[j][i], t[i], v[j][i]);
                 } else {
@@ -362,16 +464,23 @@ __global__ void __launch_bounds__(MAXT, MINB) seam_fwd_kernel(const __grid_const
                 }
                 Raw8<DT> o;
                 o.set(v[j]);
-                o.store(out + j * threads * 8, in[j]);
+                if constexpr (ANY) any.put(d, j, out, seg0 + j * threads * 8, S.cols, v[j]);
+                else o.store(out + j * threads * 8, in[j]);
                 o.get(v[j]);                    // as it was stored
+                if (ANY && nv[j] < 8)
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) v[j][i] = i < nv[j] ? v[j][i] : 0.f;
             }
             out += S.ldout;
         } else {
 #pragma unroll
-            for (int j = 0; j < VPT; ++j) ring_get<DT, VPT>(ring, d, 0, j, v[j]);
+            for (int j = 0; j < VPT; ++j) {
+                if constexpr (ANY) any.get(d, 0, j, static_cast<const T*>(S.x) + row * S.ldx, nv[j], v[j]);
+                else ring_get<DT, VPT>(ring, d, 0, j, v[j]);
+            }
         }
         if (pre != MUON_NORM_NONE) {
-            const float r = normalise<VPT>(v, in, pre, S.eps, p.inv_c, red, slot, nw);
+            const float r = normalise<VPT>(v, nv, pre, S.eps, p.inv_c, red, slot, nw);
             if (S.pre_rstd && tr == 0) S.pre_rstd[row] = r;
             if (keep_y) {
 #pragma unroll
@@ -379,7 +488,10 @@ __global__ void __launch_bounds__(MAXT, MINB) seam_fwd_kernel(const __grid_const
                     uint2 w;
                     const int byte = act8_quantise8(v[j], w);
                     bad |= byte == kActBad;
-                    if (in[j]) {
+                    if (ANY && nv[j] < 8) {
+                        for (int i = 0; i < nv[j]; ++i) yq[j * threads * 8 + i] = (signed char)((i < 4 ? w.x : w.y) >> (8 * (i & 3)));
+                        if ((lane & 3) == 0 && in[j]) ye[col[j] / kActBlock] = (unsigned char)byte;
+                    } else if (in[j]) {
                         *reinterpret_cast<uint2*>(yq + j * threads * 8) = w;
                         if ((lane & 3) == 0) ye[col[j] / kActBlock] = (unsigned char)byte;
                     }
@@ -400,11 +512,13 @@ __global__ void __launch_bounds__(MAXT, MINB) seam_fwd_kernel(const __grid_const
                 }
                 Raw8<DT> o;
                 o.set(v[j]);
-                o.store(y + j * threads * 8, in[j]);
+                if constexpr (ANY) any.put(d, j, y, seg0 + j * threads * 8, S.cols, v[j]);
+                else o.store(y + j * threads * 8, in[j]);
             }
             y += S.ldy;
         }
         d = d + 1 == D ? 0 : d + 1;
+        if (ANY) __syncwarp();                              // this row is read before its place is copied to again
     }
     cp_async_wait<0>();
     if (__any_sync(0xFFFFFFFFu, bad) && lane == 0 && p.d_status) atomicOr(p.d_status, MUON_FLAG_NONFINITE);
@@ -412,7 +526,7 @@ __global__ void __launch_bounds__(MAXT, MINB) seam_fwd_kernel(const __grid_const
 
 enum BwdVec : int { B_POST_GAIN, B_PRE_GAIN, B_POST_BIAS, B_VECS };
 
-template <typename T, int VPT, int MAXT, int D, int MINB, bool BIAS, bool GSUM>
+template <typename T, int VPT, int MAXT, int D, int MINB, bool BIAS, bool GSUM, bool ANY>
 __global__ void __launch_bounds__(MAXT, MINB) seam_bwd_kernel(const __grid_constant__ BwdParams p) {
     constexpr int DT = DtOf<T>::v;
     constexpr int NPC = sizeof(T) == 4 ? 2 : 1;
@@ -423,26 +537,31 @@ __global__ void __launch_bounds__(MAXT, MINB) seam_bwd_kernel(const __grid_const
     const int threads = blockDim.x, nw = threads >> 5;
     const bool has_pre = S.pre != MUON_NORM_NONE, has_post = S.post != MUON_NORM_NONE, has_f = S.df != nullptr;
     const bool has_dout = S.dout != nullptr, has_gate = S.gate != nullptr, post_c = S.post_c.q != nullptr;
-    const bool has_pb = S.post_bias != nullptr, dgate = S.dgate != nullptr, gate_sums = GSUM;
+    const bool has_pb = S.post_bias != nullptr, dgate = S.dgate != nullptr, gate_sums = GSUM && p.gate_sums;
     for (int i = threadIdx.x; i < kRedBytes / 4; i += threads) red[i] = 0.f;
     // scale rides on the post-norm's vectors
-    const Vectors V{p.vecs_in_smem ? reinterpret_cast<float*>(smem + kRedBytes) : nullptr, threads * VPT, p.w_dt};
+    const Vectors V{p.vecs_in_smem ? reinterpret_cast<float*>(smem + kRedBytes) : nullptr, threads * VPT, p.w_dt, S.cols, !ANY};
     if (V.sm) {
-        V.fill(B_POST_GAIN, S.post_gain, S.scale, S.cols);
-        V.fill(B_PRE_GAIN, S.pre_gain, 1.f, S.cols);
-        if (has_pb) V.fill(B_POST_BIAS, S.post_bias, S.scale, S.cols);
+        V.fill(B_POST_GAIN, S.post_gain, S.scale);
+        V.fill(B_PRE_GAIN, S.pre_gain, 1.f);
+        if (has_pb) V.fill(B_POST_BIAS, S.post_bias, S.scale);
     }
     const Ring<VPT> ring{smem + kRedBytes + (V.sm ? p.vectors * 32 * V.chunks : 0) + threadIdx.x * 16, threads * 16, p.units};
-    int col[VPT], ecol[VPT];
+    int col[VPT], ecol[VPT], nv[VPT];
     bool in[VPT];
 #pragma unroll
     for (int j = 0; j < VPT; ++j) {
         col[j] = (j * threads + (int)threadIdx.x) * 8;
         in[j] = col[j] < S.cols;
+        nv[j] = max(0, min(8, S.cols - col[j]));
         ecol[j] = (in[j] ? col[j] : 0) / kActBlock;
         if (!in[j])
             for (int u = 0; u < D * p.units; ++u) *reinterpret_cast<uint4*>(ring.at(0, u, j)) = make_uint4(0u, 0u, 0u, 0u);
     }
+    const int lane = threadIdx.x & 31;
+    uint8_t* after = smem + kRedBytes + (V.sm ? p.vectors * 32 * V.chunks : 0) + D * p.units * VPT * threads * 16;
+    const AnyRow<T, VPT> any{ring, reinterpret_cast<uint32_t*>(after) + (threadIdx.x >> 5), nw, lane};
+    const int seg0 = ((int)threadIdx.x - lane) * 8;        // the warp's first column of a chunk
     __syncthreads();
     int r0, r1;
     if (p.plan.parts == 0) {
@@ -456,25 +575,35 @@ __global__ void __launch_bounds__(MAXT, MINB) seam_bwd_kernel(const __grid_const
     const int gr = has_gate ? S.gate_rows : 1;
     int gleft = has_gate ? gr - r0 % gr : 0, cleft = gleft;                 // rows left of the gate row: of the next copy, at work
     // this thread's first chunk of the next row to copy, and of the row at work
-    const T* dy = static_cast<const T*>(S.dy) + r0 * S.lddy + threadIdx.x * 8;
-    const T* dout = static_cast<const T*>(S.dout) + r0 * S.lddout + threadIdx.x * 8;
-    const T* gate = static_cast<const T*>(S.gate) + (r0 / gr) * S.ldgate + threadIdx.x * 8;
+    const int t8 = ANY ? 0 : threadIdx.x * 8;
+    const T* dy = static_cast<const T*>(S.dy) + r0 * S.lddy + t8;
+    const T* dout = static_cast<const T*>(S.dout) + r0 * S.lddout + t8;
+    const T* gate = static_cast<const T*>(S.gate) + (r0 / gr) * S.ldgate + t8;
     const signed char* yq = S.pre_c.q + r0 * S.pre_c.ldq + threadIdx.x * 8;
     const signed char* pq = S.post_c.q + r0 * S.post_c.ldq + threadIdx.x * 8;
-    T* dx = static_cast<T*>(S.dx) + r0 * S.lddx + threadIdx.x * 8;
-    T* df = static_cast<T*>(S.df) + r0 * S.lddf + threadIdx.x * 8;
-    T* dg = static_cast<T*>(S.dgate) + (r0 / gr) * S.lddgate + threadIdx.x * 8;
+    T* dx = static_cast<T*>(S.dx) + r0 * S.lddx + t8;
+    T* df = static_cast<T*>(S.df) + r0 * S.lddf + t8;
+    T* dg = static_cast<T*>(S.dgate) + (r0 / gr) * S.lddgate + t8;
     auto copy = [&](int row, int d) {
         if (row < r1) {
 #pragma unroll
             for (int j = 0; j < VPT; ++j) {
-                if (!in[j]) continue;
                 const int cj = j * threads * 8;
+                if constexpr (ANY) {
+                    if (seg0 + cj < S.cols) {
+                        if (has_pre) any.copy(d, 0, j, dy, seg0 + cj, S.cols);
+                        if (has_dout) any.copy(d, kDout, j, dout, seg0 + cj, S.cols);
+                        if (has_gate) any.copy(d, kGate, j, gate, seg0 + cj, S.cols);
+                    }
+                }
+                if (!in[j]) continue;
+                if constexpr (!ANY) {
 #pragma unroll
-                for (int n = 0; n < NPC; ++n) {
-                    if (has_pre) copy16<NPC>(ring.at(d, n, j), dy + cj + n * 4);
-                    if (has_dout) copy16<NPC>(ring.at(d, kDout + n, j), dout + cj + n * 4);
-                    if (has_gate) copy16<NPC>(ring.at(d, kGate + n, j), gate + cj + n * 4);
+                    for (int n = 0; n < NPC; ++n) {
+                        if (has_pre) copy16<NPC>(ring.at(d, n, j), dy + cj + n * 4);
+                        if (has_dout) copy16<NPC>(ring.at(d, kDout + n, j), dout + cj + n * 4);
+                        if (has_gate) copy16<NPC>(ring.at(d, kGate + n, j), gate + cj + n * 4);
+                    }
                 }
                 if (has_pre) cp_async8(ring.at(d, kCodes, j), yq + cj);
                 if (post_c) cp_async8(ring.at(d, kCodes, j) + 8, pq + cj);
@@ -509,6 +638,9 @@ __global__ void __launch_bounds__(MAXT, MINB) seam_bwd_kernel(const __grid_const
     // codes of a thread without columns are 0 under any finite scale; a bad block's byte must not reach them
     auto decode = [&](int d, int half, int j, int byte, float (&n)[8]) {
         act8_decode8(*reinterpret_cast<const uint2*>(ring.at(d, kCodes, j) + 8 * half), in[j] ? byte : 127, n);
+        if (ANY && nv[j] < 8)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) n[i] = i < nv[j] ? n[i] : 0.f;
     };
     float a_pg[VPT][8] = {}, a_qg[VPT][8] = {};               // d_pre_gain, d_post_gain / scale
     float a_pb[BIAS ? VPT : 1][8] = {}, a_qb[BIAS ? VPT : 1][8] = {}, a_gt[GSUM ? VPT : 1][8] = {};
@@ -519,6 +651,7 @@ __global__ void __launch_bounds__(MAXT, MINB) seam_bwd_kernel(const __grid_const
     for (int row = r0; row < r1; ++row) {
         copy(row + D - 1, d == 0 ? D - 1 : d - 1);
         cp_async_wait<D - 1>();
+        if (ANY) __syncwarp();                                // the other lanes' copies too
         const float r_pre = rp, r_post = rq;
         int b_pre[VPT], b_post[VPT];
 #pragma unroll
@@ -533,7 +666,8 @@ __global__ void __launch_bounds__(MAXT, MINB) seam_bwd_kernel(const __grid_const
 #pragma unroll
             for (int j = 0; j < VPT; ++j) {
                 float t[8];
-                ring_get<DT, VPT>(ring, d, 0, j, x[j]);
+                if constexpr (ANY) any.get(d, 0, j, static_cast<const T*>(S.dy) + row * S.lddy, nv[j], x[j]);
+                else ring_get<DT, VPT>(ring, d, 0, j, x[j]);
                 decode(d, 0, j, b_pre[j], n[j]);
                 V.get(B_PRE_GAIN, S.pre_gain, 1.f, col[j], in[j], t);
 #pragma unroll
@@ -562,7 +696,10 @@ __global__ void __launch_bounds__(MAXT, MINB) seam_bwd_kernel(const __grid_const
 #pragma unroll
             for (int j = 0; j < VPT; ++j) {
                 float t[8];
-                if (has_dout) ring_get<DT, VPT>(ring, d, kDout, j, t);
+                if (has_dout) {
+                    if constexpr (ANY) any.get(d, kDout, j, static_cast<const T*>(S.dout) + row * S.lddout, nv[j], t);
+                    else ring_get<DT, VPT>(ring, d, kDout, j, t);
+                }
                 else
 #pragma unroll
                     for (int i = 0; i < 8; ++i) t[i] = 0.f;
@@ -570,10 +707,16 @@ __global__ void __launch_bounds__(MAXT, MINB) seam_bwd_kernel(const __grid_const
                 const float s0j = in[j] ? s0 : 0.f;
 #pragma unroll
                 for (int i = 0; i < 8; ++i) x[j][i] = fmaf(r_pre, x[j][i], fmaf(-s1, n[j][i], t[i] - s0j));
+                if (ANY && nv[j] < 8)
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) x[j][i] = i < nv[j] ? x[j][i] : 0.f;
             }
         } else {
 #pragma unroll
-            for (int j = 0; j < VPT; ++j) ring_get<DT, VPT>(ring, d, kDout, j, x[j]);
+            for (int j = 0; j < VPT; ++j) {
+                if constexpr (ANY) any.get(d, kDout, j, static_cast<const T*>(S.dout) + row * S.lddout, nv[j], x[j]);
+                else ring_get<DT, VPT>(ring, d, kDout, j, x[j]);
+            }
         }
         if (has_f) {
             float n[VPT][8], h[VPT][8], sums[2] = {0.f, 0.f};
@@ -587,7 +730,8 @@ __global__ void __launch_bounds__(MAXT, MINB) seam_bwd_kernel(const __grid_const
                 V.get(B_POST_GAIN, S.post_gain, S.scale, col[j], in[j], t);
                 if (has_gate) {
                     float g[8];
-                    ring_get<DT, VPT>(ring, d, kGate, j, g);
+                    if constexpr (ANY) any.get(d, kGate, j, static_cast<const T*>(S.gate) + (row / gr) * S.ldgate, nv[j], g);
+                    else ring_get<DT, VPT>(ring, d, kGate, j, g);
                     if (dgate) {
                         float u[8];
                         if (has_pb) {
@@ -601,11 +745,13 @@ __global__ void __launch_bounds__(MAXT, MINB) seam_bwd_kernel(const __grid_const
                         if (!gate_sums) {
                             Raw8<DT> o;
                             o.set(u);
-                            o.store(dg + j * threads * 8, in[j]);
+                            if constexpr (ANY) any.put(d, j, dg, seg0 + j * threads * 8, S.cols, u);
+                            else o.store(dg + j * threads * 8, in[j]);
                         }
-                        if constexpr (GSUM)
+                        if constexpr (GSUM) {
 #pragma unroll
                             for (int i = 0; i < 8; ++i) a_gt[j][i] += u[i];
+                        }
                     }
 #pragma unroll
                     for (int i = 0; i < 8; ++i) h[j][i] = x[j][i] * g[i];
@@ -646,7 +792,8 @@ __global__ void __launch_bounds__(MAXT, MINB) seam_bwd_kernel(const __grid_const
             for (int j = 0; j < VPT; ++j) {
                 Raw8<DT> o;
                 o.set(h[j]);
-                o.store(df + j * threads * 8, in[j]);
+                if constexpr (ANY) any.put(d, j, df, seg0 + j * threads * 8, S.cols, h[j]);
+                else o.store(df + j * threads * 8, in[j]);
             }
             df += S.lddf;
         }
@@ -657,24 +804,29 @@ __global__ void __launch_bounds__(MAXT, MINB) seam_bwd_kernel(const __grid_const
                 for (int i = 0; i < 8; ++i) x[j][i] *= S.skip;
             Raw8<DT> o;
             o.set(x[j]);
-            o.store(dx + j * threads * 8, in[j]);
+            if constexpr (ANY) any.put(d, j, dx, seg0 + j * threads * 8, S.cols, x[j]);
+            else o.store(dx + j * threads * 8, in[j]);
         }
         dx += S.lddx;
         if (has_gate && (--cleft == 0 || row + 1 == S.rows)) {
-            if constexpr (GSUM)
-                if (p.plan.parts == 0)
+            if constexpr (GSUM) {
+                if (gate_sums && p.plan.parts == 0) {
 #pragma unroll
                     for (int j = 0; j < VPT; ++j) {
                         Raw8<DT> o;
                         o.set(a_gt[j]);
-                        o.store(dg + j * threads * 8, in[j]);
+                        if constexpr (ANY) any.put(d, j, dg, seg0 + j * threads * 8, S.cols, a_gt[j]);
+                        else o.store(dg + j * threads * 8, in[j]);
 #pragma unroll
                         for (int i = 0; i < 8; ++i) a_gt[j][i] = 0.f;
                     }
+                }
+            }
             dg += S.lddgate;
             cleft = gr;
         }
         d = d + 1 == D ? 0 : d + 1;
+        if (ANY) __syncwarp();                                // this row is read before its place is copied to again
     }
     cp_async_wait<0>();
     auto put = [&](int v, float (&a)[8], float mul, int j) {
@@ -682,7 +834,9 @@ __global__ void __launch_bounds__(MAXT, MINB) seam_bwd_kernel(const __grid_const
 #pragma unroll
         for (int i = 0; i < 8; ++i) a[i] *= mul;
         o.set(a);
-        o.store(p.part + ((long long)v * p.plan.runs + blockIdx.x) * S.cols + col[j], in[j]);
+        float* row = p.part + ((long long)v * p.plan.runs + blockIdx.x) * S.cols;
+        if constexpr (ANY) any.put(0, j, row, seg0 + j * threads * 8, S.cols, a);
+        else o.store(row + col[j], in[j]);
     };
 #pragma unroll
     for (int j = 0; j < VPT; ++j) {
@@ -693,381 +847,7 @@ __global__ void __launch_bounds__(MAXT, MINB) seam_bwd_kernel(const __grid_const
             if (S.d_post_bias) put(V_POST_BIAS, a_qb[j], S.scale, j);
         }
         if constexpr (GSUM)
-            if (p.plan.parts) put(V_COUNT, a_gt[j], 1.f, j);
-    }
-}
-
-// ---------------------------------------------------------------------------
-// Any rows: element by element.  A lane takes one column of each of eight blocks of 32
-// columns, so that a warp's accesses are whole runs of 32 elements (eight
-// neighbouring columns per lane took 2.2 times as long backward at 16384 x 2900).
-// ---------------------------------------------------------------------------
-
-// (One choice of type around the eight accesses, which are then in flight together.)
-template <typename T>
-__device__ __forceinline__ void load_cols_t(const T* p, int c0, int cols, float (&v)[8]) {
-    T t[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) t[i] = c0 + 32 * i < cols ? p[32 * i] : from_float<T>(0.f);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = to_float(t[i]);
-}
-
-__device__ __forceinline__ void load_cols(const void* p, long long row_at, int c0, int cols, int dt, float (&v)[8]) {
-    if (dt == DT_BF16) load_cols_t(static_cast<const __nv_bfloat16*>(p) + row_at + c0, c0, cols, v);
-    else if (dt == DT_FP16) load_cols_t(static_cast<const __half*>(p) + row_at + c0, c0, cols, v);
-    else load_cols_t(static_cast<const float*>(p) + row_at + c0, c0, cols, v);
-}
-
-template <typename T>
-__device__ __forceinline__ void store_cols_t(T* p, int c0, int cols, const float (&v)[8]) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-        if (c0 + 32 * i < cols) p[32 * i] = from_float<T>(v[i]);
-}
-
-__device__ __forceinline__ void store_cols(void* p, long long row_at, int c0, int cols, int dt, const float (&v)[8]) {
-    if (dt == DT_BF16) store_cols_t(static_cast<__nv_bfloat16*>(p) + row_at + c0, c0, cols, v);
-    else if (dt == DT_FP16) store_cols_t(static_cast<__half*>(p) + row_at + c0, c0, cols, v);
-    else store_cols_t(static_cast<float*>(p) + row_at + c0, c0, cols, v);
-}
-
-// Blocks of a checkpoint's row, a lane one column of each; false if one cannot be held.
-__device__ __forceinline__ bool encode_cols(const muon_act8& c, long long row, int c0, int cols, const float (&v)[8]) {
-    const int lane = threadIdx.x & 31;
-    signed char* q = c.q + row * c.ldq + c0;
-    unsigned char* e = c.e + row * c.lde + c0 / kActBlock;
-    bool ok = true;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const int byte = act8_exp_byte(__reduce_max_sync(0xFFFFFFFFu, __float_as_uint(fabsf(v[i]))));
-        const int code = byte == kActBad ? 0 : (int)act8_codes4(v[i], 0.f, 0.f, 0.f, act8_inv(byte));
-        ok = ok && byte != kActBad;
-        if (c0 + 32 * i < cols) {
-            q[32 * i] = (signed char)code;
-            if (lane == 0) e[i] = (unsigned char)byte;
-        }
-    }
-    return ok;
-}
-
-__device__ __forceinline__ void decode_cols(const muon_act8& c, long long row, int c0, int cols, float (&v)[8]) {
-    const signed char* qp = c.q + row * c.ldq + c0;
-    const unsigned char* ep = c.e + row * c.lde + c0 / kActBlock;
-    int q[8], e[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        q[i] = c0 + 32 * i < cols ? qp[32 * i] : 0;
-        e[i] = c0 + 32 * i < cols ? ep[i] : 127;
-    }
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = (float)q[i] * act8_step(e[i]);
-}
-
-__device__ __forceinline__ float round_dt(float v, int dt) {
-    if (dt == DT_BF16) return __bfloat162float(__float2bfloat16_rn(v));
-    if (dt == DT_FP16) return __half2float(__float2half_rn(v));
-    return v;
-}
-
-// Sums of N values over the TPR threads of a row; every thread gets them.  `slot`
-// alternates between two shared-memory areas, so one barrier per call is enough.
-template <int TPR, int N>
-__device__ __forceinline__ void row_sum(float (&v)[N], float* red, int& slot) {
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1)
-#pragma unroll
-        for (int k = 0; k < N; ++k) v[k] += __shfl_xor_sync(0xFFFFFFFFu, v[k], o);
-    if constexpr (TPR > 32) {
-        constexpr int NW = TPR / 32;
-        float* s = red + slot * (NW * 2);
-        slot ^= 1;
-        if ((threadIdx.x & 31) == 0)
-#pragma unroll
-            for (int k = 0; k < N; ++k) s[k * NW + (threadIdx.x >> 5)] = v[k];
-        __syncthreads();
-#pragma unroll
-        for (int k = 0; k < N; ++k) {
-            if constexpr (NW <= 8) {
-                float t = s[k * NW];
-#pragma unroll
-                for (int w = 1; w < NW; ++w) t += s[k * NW + w];
-                v[k] = t;
-            } else {
-                const int lane = threadIdx.x & 31;
-                float t = lane < NW ? s[k * NW + lane] : 0.f;
-#pragma unroll
-                for (int o = 16; o > 0; o >>= 1) t += __shfl_xor_sync(0xFFFFFFFFu, t, o);
-                v[k] = t;
-            }
-        }
-    }
-}
-
-// Normalise the row in v (columns beyond the row hold 0 and stay 0): returns the
-// reciprocal deviation.  The two-pass variance keeps rows whose mean is large
-// against their deviation exact; a sum of squares beyond fp32's range is formed
-// again at 2^-100.
-template <int TPR, int VPT>
-__device__ __forceinline__ float row_normalise(float (&v)[VPT][8], const int (&c0)[VPT], int cols, int kind, float eps,
-                                               float inv_c, float* red, int& slot) {
-    if (kind == MUON_NORM_LAYER) {
-        float m[1] = {0.f};
-#pragma unroll
-        for (int j = 0; j < VPT; ++j)
-#pragma unroll
-            for (int i = 0; i < 8; ++i) m[0] = fmaf(v[j][i], inv_c, m[0]);
-        row_sum<TPR, 1>(m, red, slot);
-#pragma unroll
-        for (int j = 0; j < VPT; ++j)
-#pragma unroll
-            for (int i = 0; i < 8; ++i) v[j][i] = c0[j] + 32 * i < cols ? v[j][i] - m[0] : 0.f;
-    }
-    float s[1] = {0.f};
-#pragma unroll
-    for (int j = 0; j < VPT; ++j)
-#pragma unroll
-        for (int i = 0; i < 8; ++i) s[0] = fmaf(v[j][i], v[j][i], s[0]);
-    row_sum<TPR, 1>(s, red, slot);
-    float r;
-    if (s[0] == __uint_as_float(0x7F800000u)) {      // uniform over the row
-        const float down = __uint_as_float((127u - 100u) << 23);
-        s[0] = 0.f;
-#pragma unroll
-        for (int j = 0; j < VPT; ++j)
-#pragma unroll
-            for (int i = 0; i < 8; ++i) s[0] = fmaf(v[j][i] * down, v[j][i] * down, s[0]);
-        row_sum<TPR, 1>(s, red, slot);
-        r = rsqrtf(s[0] * inv_c) * down;
-    } else {
-        r = rsqrtf(fmaf(s[0], inv_c, eps));
-    }
-#pragma unroll
-    for (int j = 0; j < VPT; ++j)
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[j][i] *= r;
-    return r;
-}
-
-// u = n gain + bias (either may be NULL)
-__device__ __forceinline__ void affine_cols(float (&v)[8], const void* gain, const void* bias, int c0, int cols, int dt) {
-    float t[8];
-    if (gain) {
-        load_cols(gain, 0, c0, cols, dt, t);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] *= t[i];
-    }
-    if (bias) {
-        load_cols(bias, 0, c0, cols, dt, t);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] += t[i];
-    }
-}
-
-template <int TPR, int VPT>
-__global__ void __launch_bounds__(TPR == 32 ? 128 : TPR) seam_fwd_any(const __grid_constant__ FwdParams p, int DT) {
-    constexpr int RPB = TPR == 32 ? 4 : 1;
-    __shared__ float red[TPR > 32 ? 4 * (TPR / 32) : 1];
-    const muon_seam& S = p.s;
-    const int lane = threadIdx.x & 31, tr = threadIdx.x % TPR;
-    const int cols = S.cols;
-    int c0[VPT];            // this lane's column of the first of a warp's eight blocks
-#pragma unroll
-    for (int j = 0; j < VPT; ++j) c0[j] = (j * TPR + (tr & ~31)) * 8 + (tr & 31);
-    int slot = 0;
-    bool bad = false;
-    for (long long row = (long long)blockIdx.x * RPB + threadIdx.x / TPR; row < S.rows;
-         row += (long long)gridDim.x * RPB) {
-        float x[VPT][8], u[VPT][8];
-#pragma unroll
-        for (int j = 0; j < VPT; ++j) {
-            load_cols(S.x, row * S.ldx, c0[j], cols, DT, x[j]);
-            if (S.f) load_cols(S.f, row * S.ldf, c0[j], cols, DT, u[j]);
-        }
-        if (S.f) {
-            if (S.post != MUON_NORM_NONE) {
-                const float r = row_normalise<TPR, VPT>(u, c0, cols, S.post, S.eps, p.inv_c, red, slot);
-                if (S.post_rstd && tr == 0) S.post_rstd[row] = r;
-            }
-#pragma unroll
-            for (int j = 0; j < VPT; ++j) {
-                if (S.post_c.q)
-                    bad |= !encode_cols(S.post_c, row, c0[j], cols, u[j]);
-                affine_cols(u[j], S.post_gain, S.post_bias, c0[j], cols, p.w_dt);
-                if (S.gate) {
-                    float g[8];
-                    load_cols(S.gate, (row / S.gate_rows) * S.ldgate, c0[j], cols, DT, g);
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) u[j][i] *= g[i];
-                }
-#pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    x[j][i] = round_dt(fmaf(S.scale, u[j][i], S.skip * x[j][i]), DT);
-#pragma unroll
-                for (int i = 0; i < 8; ++i) x[j][i] = c0[j] + 32 * i < cols ? x[j][i] : 0.f;
-                store_cols(S.out, row * S.ldout, c0[j], cols, DT, x[j]);
-            }
-        }
-        if (S.pre != MUON_NORM_NONE) {
-            const float r = row_normalise<TPR, VPT>(x, c0, cols, S.pre, S.eps, p.inv_c, red, slot);
-            if (S.pre_rstd && tr == 0) S.pre_rstd[row] = r;
-#pragma unroll
-            for (int j = 0; j < VPT; ++j) {
-                if (S.pre_c.q)
-                    bad |= !encode_cols(S.pre_c, row, c0[j], cols, x[j]);
-                affine_cols(x[j], S.pre_gain, S.pre_bias, c0[j], cols, p.w_dt);
-                store_cols(S.y, row * S.ldy, c0[j], cols, DT, x[j]);
-            }
-        }
-    }
-    if (__any_sync(0xFFFFFFFFu, bad) && lane == 0 && p.d_status) atomicOr(p.d_status, MUON_FLAG_NONFINITE);
-}
-
-template <int TPR, int VPT, bool ALL>
-__global__ void __launch_bounds__(TPR) seam_bwd_any(const __grid_constant__ BwdParams p, int DT) {
-    __shared__ float red[TPR > 32 ? 4 * (TPR / 32) : 1];
-    const muon_seam_grad& S = p.s;
-    const int tr = threadIdx.x;
-    const int cols = S.cols;
-    int c0[VPT];            // this lane's column of the first of a warp's eight blocks
-#pragma unroll
-    for (int j = 0; j < VPT; ++j) c0[j] = (j * TPR + (tr & ~31)) * 8 + (tr & 31);
-    long long r0, r1;
-    if (p.plan.parts == 0) {
-        r0 = (long long)blockIdx.x * p.plan.run_rows;
-        r1 = min((long long)S.rows, r0 + p.plan.run_rows);
-    } else {
-        const long long g = blockIdx.x / p.plan.parts;
-        r0 = g * S.gate_rows + (long long)(blockIdx.x % p.plan.parts) * p.plan.run_rows;
-        r1 = min(min((long long)S.rows, r0 + p.plan.run_rows), (g + 1) * S.gate_rows);
-    }
-    float a_pg[VPT][8] = {}, a_qg[VPT][8] = {};               // d_pre_gain, d_post_gain
-    float a_pb[ALL ? VPT : 1][8] = {}, a_qb[ALL ? VPT : 1][8] = {}, a_gt[ALL ? VPT : 1][8] = {};
-    int slot = 0;
-    const bool post_c = S.post_c.q != nullptr;
-    for (long long row = r0; row < r1; ++row) {
-        float d[VPT][8];
-#pragma unroll
-        for (int j = 0; j < VPT; ++j) {
-            if (S.dout) load_cols(S.dout, row * S.lddout, c0[j], cols, DT, d[j]);
-            else
-#pragma unroll
-                for (int i = 0; i < 8; ++i) d[j][i] = 0.f;
-        }
-        if (S.pre != MUON_NORM_NONE) {
-            float g[VPT][8], n[VPT][8];
-            float sums[2] = {0.f, 0.f};
-#pragma unroll
-            for (int j = 0; j < VPT; ++j) {
-                load_cols(S.dy, row * S.lddy, c0[j], cols, DT, g[j]);
-                decode_cols(S.pre_c, row, c0[j], cols, n[j]);
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    a_pg[j][i] = fmaf(g[j][i], n[j][i], a_pg[j][i]);
-                    if constexpr (ALL) a_pb[j][i] += g[j][i];
-                }
-                affine_cols(g[j], S.pre_gain, nullptr, c0[j], cols, p.w_dt);
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    sums[0] = fmaf(g[j][i], n[j][i], sums[0]);
-                    sums[1] += g[j][i];
-                }
-            }
-            row_sum<TPR, 2>(sums, red, slot);
-            const float r = S.pre_rstd[row];
-            const float s1 = sums[0] * p.inv_c, s0 = S.pre == MUON_NORM_LAYER ? sums[1] * p.inv_c : 0.f;
-#pragma unroll
-            for (int j = 0; j < VPT; ++j)
-#pragma unroll
-                for (int i = 0; i < 8; ++i)        // columns beyond the row stay out of the sums over it
-                    d[j][i] = c0[j] + 32 * i < cols ? fmaf(r, fmaf(-n[j][i], s1, g[j][i] - s0), d[j][i]) : 0.f;
-        }
-        if (S.df) {
-            float n[VPT][8], h[VPT][8];
-            float sums[2] = {0.f, 0.f};
-            const long long grow = S.gate ? row / S.gate_rows : 0;
-#pragma unroll
-            for (int j = 0; j < VPT; ++j) {
-                if (post_c)
-                    decode_cols(S.post_c, row, c0[j], cols, n[j]);
-                else
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) n[j][i] = 0.f;
-#pragma unroll
-                for (int i = 0; i < 8; ++i) h[j][i] = S.scale * d[j][i];
-                if (S.gate) {
-                    float g[8];
-                    load_cols(S.gate, grow * S.ldgate, c0[j], cols, DT, g);
-                    if (S.dgate) {
-                        float t[8];
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) t[i] = n[j][i];
-                        affine_cols(t, S.post_gain, S.post_bias, c0[j], cols, p.w_dt);
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) t[i] *= h[j][i];
-                        if (!p.gate_sums) store_cols(S.dgate, grow * S.lddgate, c0[j], cols, DT, t);
-                        if constexpr (ALL)
-#pragma unroll
-                            for (int i = 0; i < 8; ++i) a_gt[j][i] += t[i];
-                    }
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) h[j][i] *= g[i];
-                }
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    a_qg[j][i] = fmaf(h[j][i], n[j][i], a_qg[j][i]);
-                    if constexpr (ALL) a_qb[j][i] += h[j][i];
-                }
-                affine_cols(h[j], S.post_gain, nullptr, c0[j], cols, p.w_dt);
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    sums[0] = fmaf(h[j][i], n[j][i], sums[0]);
-                    sums[1] += h[j][i];
-                }
-            }
-            if (S.post != MUON_NORM_NONE) {
-                row_sum<TPR, 2>(sums, red, slot);
-                const float r = S.post_rstd[row];
-                const float s1 = sums[0] * p.inv_c, s0 = S.post == MUON_NORM_LAYER ? sums[1] * p.inv_c : 0.f;
-#pragma unroll
-                for (int j = 0; j < VPT; ++j)
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) h[j][i] = r * fmaf(-n[j][i], s1, h[j][i] - s0);
-            }
-#pragma unroll
-            for (int j = 0; j < VPT; ++j)
-                store_cols(S.df, row * S.lddf, c0[j], cols, DT, h[j]);
-        }
-#pragma unroll
-        for (int j = 0; j < VPT; ++j) {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) d[j][i] *= S.skip;
-            store_cols(S.dx, row * S.lddx, c0[j], cols, DT, d[j]);
-        }
-        if constexpr (ALL) {
-            if (p.gate_sums && p.plan.parts == 0 && ((row + 1) % S.gate_rows == 0 || row + 1 == S.rows)) {
-                const long long grow = row / S.gate_rows;
-#pragma unroll
-                for (int j = 0; j < VPT; ++j) {
-                    store_cols(S.dgate, grow * S.lddgate, c0[j], cols, DT, a_gt[j]);
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) a_gt[j][i] = 0.f;
-                }
-            }
-        }
-    }
-    auto put = [&](int v, const float (&a)[8], int j) {
-        store_cols(p.part, ((long long)v * p.plan.runs + blockIdx.x) * cols, c0[j], cols, DT_FP32, a);
-    };
-#pragma unroll
-    for (int j = 0; j < VPT; ++j) {
-        if (S.d_pre_gain) put(V_PRE_GAIN, a_pg[j], j);
-        if (S.d_post_gain) put(V_POST_GAIN, a_qg[j], j);
-        if constexpr (ALL) {
-            if (S.d_pre_bias) put(V_PRE_BIAS, a_pb[j], j);
-            if (S.d_post_bias) put(V_POST_BIAS, a_qb[j], j);
-            if (p.gate_sums && p.plan.parts) put(V_COUNT, a_gt[j], j);
-        }
+            if (gate_sums && p.plan.parts) put(V_COUNT, a_gt[j], 1.f, j);
     }
 }
 
@@ -1200,11 +980,12 @@ struct Form {
 // with a gate forward 150 us with three blocks and global vectors); the blocks that are resident then are
 // the grid, unless the runs of rows are given.
 template <typename K, typename P>
-cudaError_t seam_launch(K kern, P& p, const Form& f, long long runs, cudaStream_t s) {
+cudaError_t seam_launch(K kern, P& p, const Form& f, bool any, long long runs, cudaStream_t s) {
     const int t = f.threads(p.s.cols), most = f.blocks(p.s.cols), room = 227 * 1024;
     const int ring = kRedBytes + f.stages * p.units * f.vpt * t * 16, vecs = p.vectors * 32 * f.vpt * f.row_threads(p.s.cols);
-    p.vecs_in_smem = ring + vecs + 1024 <= room;
-    const int smem = ring + (p.vecs_in_smem ? vecs : 0);
+    const int more = any ? t / 32 * 4 * f.stages * p.units * f.vpt : 0;     // AnyRow's words behind the pieces
+    p.vecs_in_smem = ring + more + vecs + 1024 <= room;
+    const int smem = ring + more + (p.vecs_in_smem ? vecs : 0);
     const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     const long long resident = (long long)sm_count() * std::max(1, std::min(most, room / (smem + 1024)));
@@ -1214,29 +995,35 @@ cudaError_t seam_launch(K kern, P& p, const Form& f, long long runs, cudaStream_
 }
 
 template <typename T>
-cudaError_t launch_fwd(FwdParams& p, cudaStream_t s) {
+cudaError_t launch_fwd(FwdParams& p, bool any, cudaStream_t s) {
     const int c = p.s.cols, npc = sizeof(T) == 4 ? 2 : 1;
     p.units = npc * (p.s.gate ? 3 : p.s.f ? 2 : 1);
     p.vectors = p.s.post_bias || p.s.pre_bias ? F_VECS : F_POST_BIAS;
-#define SEAM_FWD(VPT, MAXT, D, MINB, WARP) \
-    return seam_launch(seam_fwd_kernel<T, VPT, MAXT, D, MINB, WARP>, p, Form{VPT, MAXT, D, MINB, WARP}, 0, s)
-    if (c <= 256) SEAM_FWD(1, 256, 3, 4, true);
-    if (c <= 512) SEAM_FWD(2, 256, 2, 3, true);
-    if (c <= 768) SEAM_FWD(3, 256, 2, 3, true);
-    if (c <= 1024) SEAM_FWD(4, 128, 2, 4, true);
-    if (c <= 4096) SEAM_FWD(2, 256, 2, 3, false);
-    if (c <= 8192) SEAM_FWD(2, 512, 2, 1, false);
-    SEAM_FWD(2, 1024, 1, 1, false);
+#define SEAM_FWD(VPT, MAXT, D, MINB, WARP, ANY) \
+    return seam_launch(seam_fwd_kernel<T, VPT, MAXT, D, MINB, WARP, ANY>, p, Form{VPT, MAXT, D, MINB, WARP}, ANY, 0, s)
+    if (any) {
+        if (c <= 1024) SEAM_FWD(4, 128, 2, 3, true, true);
+        if (c <= 4096) SEAM_FWD(2, 256, 2, 2, false, true);
+        if (c <= 8192) SEAM_FWD(2, 512, 2, 1, false, true);
+        SEAM_FWD(2, 1024, 1, 1, false, true);
+    }
+    if (c <= 256) SEAM_FWD(1, 256, 3, 4, true, false);
+    if (c <= 512) SEAM_FWD(2, 256, 2, 3, true, false);
+    if (c <= 768) SEAM_FWD(3, 256, 2, 3, true, false);
+    if (c <= 1024) SEAM_FWD(4, 128, 2, 4, true, false);
+    if (c <= 4096) SEAM_FWD(2, 256, 2, 3, false, false);
+    if (c <= 8192) SEAM_FWD(2, 512, 2, 1, false, false);
+    SEAM_FWD(2, 1024, 1, 1, false, false);
 #undef SEAM_FWD
 }
 
-template <typename T, bool BIAS, bool GSUM>
+template <typename T, bool BIAS, bool GSUM, bool ANY>
 cudaError_t launch_bwd_form(BwdParams& p, cudaStream_t s) {
     const int c = p.s.cols, npc = sizeof(T) == 4 ? 2 : 1;
     p.units = 2 * npc + 1 + (p.s.gate ? npc : 0);
     p.vectors = p.s.post_bias ? B_VECS : B_POST_BIAS;
 #define SEAM_BWD(VPT, MAXT, D, MINB)                                                                                    \
-    return seam_launch(seam_bwd_kernel<T, VPT, MAXT, D, MINB, BIAS, GSUM>, p, Form{VPT, MAXT, D, MINB, false}, p.plan.runs, s)
+    return seam_launch(seam_bwd_kernel<T, VPT, MAXT, D, MINB, BIAS, GSUM, ANY>, p, Form{VPT, MAXT, D, MINB, false}, ANY, p.plan.runs, s)
     if (c <= 768) SEAM_BWD(1, 96, 3, BIAS || GSUM ? 6 : 8);
     if (c <= 4096) SEAM_BWD(2, 256, 2, BIAS ? 1 : 2);
     if (c <= 8192) SEAM_BWD(2, 512, 2, 1);
@@ -1245,49 +1032,11 @@ cudaError_t launch_bwd_form(BwdParams& p, cudaStream_t s) {
 }
 
 template <typename T>
-cudaError_t launch_bwd(BwdParams& p, cudaStream_t s) {
+cudaError_t launch_bwd(BwdParams& p, bool any, cudaStream_t s) {
     const bool bias = p.s.d_post_bias || p.s.d_pre_bias;
-    if (p.gate_sums) return bias ? launch_bwd_form<T, true, true>(p, s) : launch_bwd_form<T, false, true>(p, s);
-    return bias ? launch_bwd_form<T, true, false>(p, s) : launch_bwd_form<T, false, false>(p, s);
-}
-
-cudaError_t launch_fwd_any(const FwdParams& p, int dt, cudaStream_t s) {
-    const int c = p.s.cols;
-#define SEAM_FWD(TPR, VPT)                                                                              \
-    do {                                                                                                \
-        const int rpb = TPR == 32 ? 4 : 1, threads = TPR == 32 ? 128 : TPR;                             \
-        const long long blocks = ((long long)p.s.rows + rpb - 1) / rpb;                                 \
-        const int grid = (int)std::min<long long>(blocks, (long long)sm_count() * (2048 / threads));    \
-        seam_fwd_any<TPR, VPT><<<grid, threads, 0, s>>>(p, dt);                                         \
-    } while (0)
-    if (c <= 256) SEAM_FWD(32, 1);
-    else if (c <= 512) SEAM_FWD(32, 2);
-    else if (c <= 1024) SEAM_FWD(32, 4);
-    else if (c <= 2048) SEAM_FWD(128, 2);
-    else if (c <= 4096) SEAM_FWD(256, 2);
-    else if (c <= 8192) SEAM_FWD(512, 2);
-    else SEAM_FWD(1024, 2);
-#undef SEAM_FWD
-    return cudaGetLastError();
-}
-
-cudaError_t launch_bwd_any(const BwdParams& p, int dt, bool all, cudaStream_t s) {
-    const int c = p.s.cols;
-    const unsigned grid = (unsigned)p.plan.runs;
-#define SEAM_BWD(TPR, VPT)                                                       \
-    do {                                                                         \
-        if (all) seam_bwd_any<TPR, VPT, true><<<grid, TPR, 0, s>>>(p, dt);       \
-        else seam_bwd_any<TPR, VPT, false><<<grid, TPR, 0, s>>>(p, dt);          \
-    } while (0)
-    if (c <= 256) SEAM_BWD(32, 1);
-    else if (c <= 512) SEAM_BWD(64, 1);
-    else if (c <= 1024) SEAM_BWD(128, 1);
-    else if (c <= 2048) SEAM_BWD(256, 1);
-    else if (c <= 4096) SEAM_BWD(512, 1);
-    else if (c <= 8192) SEAM_BWD(1024, 1);
-    else SEAM_BWD(1024, 2);
-#undef SEAM_BWD
-    return cudaGetLastError();
+    if (any) return bias || p.gate_sums ? launch_bwd_form<T, true, true, true>(p, s) : launch_bwd_form<T, false, false, true>(p, s);
+    if (p.gate_sums) return bias ? launch_bwd_form<T, true, true, false>(p, s) : launch_bwd_form<T, false, true, false>(p, s);
+    return bias ? launch_bwd_form<T, true, false, false>(p, s) : launch_bwd_form<T, false, false, false>(p, s);
 }
 
 bool vec_ok(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
@@ -1321,9 +1070,9 @@ muon_status seam_forward(const muon_seam* seam, muon_dtype x_dtype, muon_dtype w
     const double el = (double)q.rows * q.cols;
     trace_begin(MUON_KERNEL_SEAM, el * (esz * (1 + (q.f ? 2 : 0) + (q.y ? 1 : 0) + (q.gate && q.gate_rows == 1 ? 1 : 0)) +
                                         33.0 / 32 * ((q.post_c.q ? 1 : 0) + (q.pre_c.q ? 1 : 0))), s);
-    const cudaError_t e = !(p.vec && p.wvec && q.cols % 8 == 0) ? launch_fwd_any(p, x_dtype, s)
-                          : x_dtype == MUON_BF16 ? launch_fwd<__nv_bfloat16>(p, s)
-                          : x_dtype == MUON_FP16 ? launch_fwd<__half>(p, s) : launch_fwd<float>(p, s);
+    const bool any = !(p.vec && p.wvec && q.cols % 8 == 0);
+    const cudaError_t e = x_dtype == MUON_BF16   ? launch_fwd<__nv_bfloat16>(p, any, s)
+                          : x_dtype == MUON_FP16 ? launch_fwd<__half>(p, any, s) : launch_fwd<float>(p, any, s);
     trace_end(s);
     return e == cudaSuccess ? MUON_OK : MUON_ERR_CUDA;
 }
@@ -1361,17 +1110,14 @@ muon_status seam_backward(const muon_seam_grad* seam, muon_dtype x_dtype, muon_d
             rows_aligned(q.dx, q.lddx, esz) && (!q.df || rows_aligned(q.df, q.lddf, esz)) &&
             (!q.gate || rows_aligned(q.gate, q.ldgate, esz)) && (!q.dgate || rows_aligned(q.dgate, q.lddgate, esz));
     p.wvec = vec_ok(q.post_gain) && vec_ok(q.post_bias) && vec_ok(q.pre_gain);
-    const bool all = q.d_post_bias || q.d_pre_bias || p.gate_sums;
     const bool tok = q.gate && q.gate_rows == 1;
     if (p.plan.runs > 0) {
         trace_begin(MUON_KERNEL_SEAM, (double)q.rows * q.cols *
                         (esz * (1.0 + (q.dy ? 1 : 0) + (q.dout ? 1 : 0) + (q.df ? 1 : 0) + (tok ? 1 : 0) + (tok && q.dgate ? 1 : 0)) +
                          33.0 / 32 * ((q.dy ? 1 : 0) + (q.post_c.q ? 1 : 0))), s);
-        cudaError_t e;
-        if (!(p.vec && p.wvec && q.cols % 8 == 0)) e = launch_bwd_any(p, x_dtype, all, s);
-        else if (x_dtype == MUON_BF16) e = launch_bwd<__nv_bfloat16>(p, s);
-        else if (x_dtype == MUON_FP16) e = launch_bwd<__half>(p, s);
-        else e = launch_bwd<float>(p, s);
+        const bool any = !(p.vec && p.wvec && q.cols % 8 == 0);
+        const cudaError_t e = x_dtype == MUON_BF16   ? launch_bwd<__nv_bfloat16>(p, any, s)
+                              : x_dtype == MUON_FP16 ? launch_bwd<__half>(p, any, s) : launch_bwd<float>(p, any, s);
         trace_end(s);
         if (e != cudaSuccess) return MUON_ERR_CUDA;
     }
