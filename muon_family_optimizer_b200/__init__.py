@@ -486,31 +486,35 @@ def act8_empty(rows, cols, device="cuda"):
                 e=torch.empty(rows, (cols + ACT8_BLOCK - 1) // ACT8_BLOCK, dtype=torch.uint8, device=device))
 
 
+def _name(where):
+    """A tensor's name in an error: a name, or an item's number and a name."""
+    return where if isinstance(where, str) else f"item {where[0]} {where[1]}"
+
+
 def _device(t, where):
     """Index of the current CUDA device, which t must be on."""
     import torch
     dev = t.get_device()
     if dev < 0 or dev != torch.cuda.current_device():
-        raise ValueError(f"{where}: must be a tensor of the current CUDA device, is on {t.device}")
+        raise ValueError(f"{_name(where)}: must be a tensor of the current CUDA device, is on {t.device}")
     return dev
 
 
-def _refuse(t, where, dev, rows, cols, dtype):
+def _refuse(t, where, dev, expected):
     if t.get_device() != dev:
-        raise ValueError(f"{where}: must be a tensor of the current CUDA device, is on {t.device}")
-    raise ValueError(f"{where}: expected a {rows} x {cols} tensor of {dtype}, got {tuple(t.shape)} of {t.dtype}")
+        raise ValueError(f"{_name(where)}: must be a tensor of the current CUDA device, is on {t.device}")
+    raise ValueError(f"{_name(where)}: expected {expected}, got {tuple(t.shape)} of {t.dtype}")
 
 
 def _matrix(t, where, dev, rows, cols, dtype):
     """(address, row stride in elements) of a rows x cols matrix whose rows are contiguous."""
-    shape = t.shape
-    if len(shape) != 2 or shape[0] != rows or shape[1] != cols or t.dtype != dtype or t.get_device() != dev:
-        _refuse(t, where, dev, rows, cols, dtype)
+    if t.shape != (rows, cols) or t.dtype != dtype or t.get_device() != dev:
+        _refuse(t, where, dev, f"a {rows} x {cols} tensor of {dtype}")
     if t.is_contiguous():
         return t.data_ptr(), cols
     s0, s1 = t.stride()
     if cols > 1 and s1 != 1 or rows > 1 and s0 < cols:
-        raise ValueError(f"{where}: rows must be contiguous and not overlap")
+        raise ValueError(f"{_name(where)}: rows must be contiguous and not overlap")
     return t.data_ptr(), s0 if rows > 1 else cols
 
 
@@ -519,45 +523,44 @@ def _vector(t, where, dev, n, dtype):
     if t is None:
         return 0
     if t.numel() != n or t.dtype != dtype or t.get_device() != dev or not t.is_contiguous():
-        if t.get_device() != dev:
-            raise ValueError(f"{where}: must be a tensor of the current CUDA device, is on {t.device}")
-        raise ValueError(f"{where}: expected {n} contiguous values of {dtype}")
+        _refuse(t, where, dev, f"{n} contiguous values of {dtype}")
     return t.data_ptr()
 
 
-def _act8(q, e, where, dev, rows, cols):
-    """The fields of a checkpoint of rows x cols."""
-    import torch
-    qp, ldq = _matrix(q, where + " q", dev, rows, cols, torch.int8)
-    ep, lde = _matrix(e, where + " e", dev, rows, (cols + ACT8_BLOCK - 1) // ACT8_BLOCK, torch.uint8)
+def _act8(q, e, where, dev, rows, cols, types):
+    """The fields of a checkpoint of rows x cols; types: the dtypes of q and e."""
+    qp, ldq = _matrix(q, where, dev, rows, cols, types[0])
+    ep, lde = _matrix(e, where, dev, rows, (cols + 31) // 32, types[1])
     if rows == 0:
         return 0, cols, 0, (cols + 15) // 16 * 16, 0, lde
     if rows == 1:                      # the only row's stride means nothing
         ldq = (cols + 15) // 16 * 16
     if ldq % 16 or qp % 16:
-        raise ValueError(f"{where}: q needs 16-byte aligned rows (see act8_empty)")
+        raise ValueError(f"{_name(where)}: q needs 16-byte aligned rows (see act8_empty)")
     return rows, cols, qp, ldq, ep, lde
 
 
 def _rows_cols(t, where):
     if t.dim() != 2:
-        raise ValueError(f"{where}: must be 2-D")
+        raise ValueError(f"{_name(where)}: must be 2-D")
     return t.shape
 
 
 def make_act8_items(items):
     """items: list of dicts with a checkpoint's q and e (see act8_empty) and x, the matrix it is
     made from or decoded into; all x of one dtype, rows contiguous (any row stride)."""
+    import torch
     arr = (Act8Item * len(items))()
     arr.x_dtype = BF16
+    types, size = (torch.int8, torch.uint8), ctypes.sizeof(Act8Item)
     if items:
-        dt, dev = items[0]["x"].dtype, _device(items[0]["x"], "item 0 x")
+        dt, dev = items[0]["x"].dtype, _device(items[0]["x"], (0, "x"))
         arr.x_dtype = _code(dt)
     for i, p in enumerate(items):
-        x, where = p["x"], f"item {i}"
-        rows, cols = _rows_cols(x, where + " x")
-        _PACK_ITEM.pack_into(arr, i * _PACK_ITEM.size, *_act8(p["q"], p["e"], where, dev, rows, cols),
-                             *_matrix(x, where + " x", dev, rows, cols, dt))
+        x = p["x"]
+        rows, cols = _rows_cols(x, (i, "x"))
+        _PACK_ITEM.pack_into(arr, i * size, *_act8(p["q"], p["e"], (i, "checkpoint"), dev, rows, cols, types),
+                             *_matrix(x, (i, "x"), dev, rows, cols, dt))
     return arr
 
 
@@ -582,24 +585,23 @@ def make_act8_grads(items):
     import torch
     arr = (Act8GradItem * len(items))()
     arr.dy_dtype = arr.w_dtype = BF16
+    types, size, f32 = (torch.int8, torch.uint8), ctypes.sizeof(Act8GradItem), torch.float32
     if items:
-        dt, wt, dev = items[0]["dY"].dtype, items[0]["G"].dtype, _device(items[0]["dY"], "item 0 dY")
+        dt, wt, dev = items[0]["dY"].dtype, items[0]["G"].dtype, _device(items[0]["dY"], (0, "dY"))
         arr.dy_dtype, arr.w_dtype = _code(dt), _code(wt)
-    size = ctypes.sizeof(Act8GradItem)
     for i, p in enumerate(items):
-        dY, G, q, where = p["dY"], p["G"], p["q"], f"item {i}"
-        rows, out = _rows_cols(dY, where + " dY")
-        cols = _rows_cols(q, where + " q")[1]
-        get = p.get
-        g, ldg = _matrix(G, where + " G", dev, out, cols, wt)
+        dY, G, q, get = p["dY"], p["G"], p["q"], p.get
+        rows, out = _rows_cols(dY, (i, "dY"))
+        cols = _rows_cols(q, (i, "q"))[1]
+        g, ldg = _matrix(G, (i, "G"), dev, out, cols, wt)
         if ldg != cols:
-            raise ValueError(f"{where} G: must be contiguous")
-        dy, lddy = _matrix(dY, where + " dY", dev, rows, out, dt)
-        _PACK_GRAD.pack_into(arr, i * size, *_act8(q, p["e"], where, dev, rows, cols), dy, lddy, out, g,
-                             _vector(get("gain"), where + " gain", dev, cols, wt),
-                             _vector(get("shift"), where + " shift", dev, cols, wt),
-                             _vector(get("dy_sum"), where + " dy_sum", dev, out, torch.float32),
-                             get("beta", 0.0))
+            raise ValueError(f"item {i} G: must be contiguous")
+        dy, lddy = _matrix(dY, (i, "dY"), dev, rows, out, dt)
+        gain, shift, dy_sum = get("gain"), get("shift"), get("dy_sum")
+        _PACK_GRAD.pack_into(arr, i * size, *_act8(q, p["e"], (i, "checkpoint"), dev, rows, cols, types), dy, lddy, out,
+                             g, 0 if gain is None else _vector(gain, (i, "gain"), dev, cols, wt),
+                             0 if shift is None else _vector(shift, (i, "shift"), dev, cols, wt),
+                             0 if dy_sum is None else _vector(dy_sum, (i, "dy_sum"), dev, out, f32), get("beta", 0.0))
     return arr
 
 
@@ -650,7 +652,7 @@ def _seam_common(s, name):
 
     def checkpoint(k):
         c = get(k)
-        return _NO_ACT8 if c is None else _act8(c["q"], c["e"], k, dev, rows, cols)
+        return _NO_ACT8 if c is None else _act8(c["q"], c["e"], k, dev, rows, cols, (torch.int8, torch.uint8))
 
     def norm(k):
         kind = get(k, "none")
