@@ -322,10 +322,12 @@ MUON_API muon_status limuon_step_batched(const muon_rsvd_param* params, int n, m
  *   - A block with a NaN, an infinity or a magnitude above 127 2^119 gets the
  *     byte 255 and codes 0, and stands for 32 NaNs.
  * Any row may hold nothing else than zeros.  rows == 0 is a valid empty
- * checkpoint (an expert without tokens); its pointers may be NULL.
+ * checkpoint (an expert without tokens); its pointers may be NULL.  Readers of a
+ * checkpoint load q in whole aligned pieces of 16 bytes and e in whole aligned
+ * words of 4, so bytes that share one with the checkpoint's are read (not used).
  */
 typedef struct {
-    int rows, cols;        /* rows >= 0 (tokens), cols >= 1 */
+    int rows, cols;        /* 0 <= rows (tokens) <= 2^30, 1 <= cols <= 2^30 */
     signed char* q;        /* rows x cols codes, row r at q + r * ldq; 16-byte aligned */
     long long ldq;         /* >= cols, a multiple of 16 */
     unsigned char* e;      /* rows x ceil(cols / 32) exponent bytes, row r at e + r * lde */
@@ -344,7 +346,10 @@ typedef struct {
  * ceil(cols / 32)) are left as they were.  A block that cannot be held raises
  * MUON_FLAG_NONFINITE in *d_status (when given).  One launch per 64 items;
  * asynchronous on `stream`; argument errors (MUON_ERR_INVALID_ARG) return
- * before any launch.  No workspace.
+ * before any launch, but a batch of 64 whose elements exceed 2^41 (for rows that
+ * are not 16-byte aligned 2^31 groups of eight rows) returns
+ * MUON_ERR_UNSUPPORTED where it is reached.  No workspace.  What one item writes
+ * may not overlap what another reads or writes.
  */
 MUON_API muon_status act8_encode_batched(const muon_act8_item* items, int n, muon_dtype x_dtype, int* d_status,
                                          muon_stream_t stream);
@@ -365,7 +370,10 @@ MUON_API muon_status act8_decode_batched(const muon_act8_item* items, int n, muo
  * overwrites G without reading it; rows == 0 leaves beta G (+ the shift term).
  * The product accumulates in fp32: 16-bit dY runs on tensor cores with X^ taken
  * in dY's type (exact in bfloat16; in fp16 rounded, see act8_decode_batched); fp32
- * dY is split into three bfloat16 parts that sum to it.  The sums run in a
+ * dY is split into three bfloat16 parts that sum to it.  The tensor cores'
+ * running sum is truncated (up to 2^-23 of it every 16 tokens), so an fp32 G is summed
+ * in segments of 6144 terms (tokens times parts) that are added rounded to nearest; a 16-bit G
+ * in segments of 65,536.  The sums run in a
  * fixed order: equal inputs give equal bits.  A NaN block makes NaNs of its columns of
  * G (the step then flags the matrix and keeps its W).
  */
@@ -373,7 +381,7 @@ typedef struct {
     muon_act8 c;           /* X^: rows (tokens) x cols; e as above */
     const void* dY;        /* c.rows x out elements of dy_dtype, row r at dY + r * lddy elements */
     long long lddy;        /* >= out */
-    int out;               /* >= 1 */
+    int out;               /* 1 to 2^30 */
     void* G;               /* out x cols, w_dtype, contiguous */
     const void* gain;      /* cols elements of w_dtype, or NULL */
     const void* shift;     /* cols elements of w_dtype, or NULL; needs dy_sum */
@@ -388,10 +396,14 @@ MUON_API muon_status act8_grad_workspace_size(const muon_act8_grad_item* items, 
 
 /*
  * The gradients of n layers (any mix of shapes; two items may share a
- * checkpoint or a dY, not a G), asynchronous on `stream`.  workspace: device,
- * 256-byte aligned, at least act8_grad_workspace_size bytes (NULL when that is
- * 0); no state is kept in it between calls.  Argument errors return before any
- * launch.
+ * checkpoint or a dY; G's that overlap are refused), asynchronous on `stream`:
+ * per 48 layers one launch, a second that joins ranges of tokens where layers have few
+ * tiles or G's rows are not 16-byte aligned, and one ahead of them where dY has to be copied (fp32, or rows
+ * that are not 16-byte aligned).  workspace: device, 256-byte aligned, at least
+ * act8_grad_workspace_size bytes (NULL when that is 0); no state is kept in it
+ * between calls, and calls that overlap on the GPU each need their own.
+ * *d_status (when given) receives MUON_FLAG_TIMEOUT if a bounded wait inside the
+ * kernel ran out.  Argument errors return before any launch.
  */
 MUON_API muon_status act8_grad_batched(const muon_act8_grad_item* items, int n, muon_dtype dy_dtype,
                                        muon_dtype w_dtype, void* workspace, size_t ws_bytes, int* d_status,
@@ -424,7 +436,7 @@ typedef enum {
 #define MUON_SEAM_MAX_COLS 16384
 
 typedef struct {
-    int rows, cols;             /* rows >= 0; 1 <= cols <= MUON_SEAM_MAX_COLS */
+    int rows, cols;             /* 0 <= rows <= 2^30; 1 <= cols <= MUON_SEAM_MAX_COLS */
     muon_norm post, pre;        /* norm of f; norm of x'.  post must be NONE without f */
     float eps;                  /* > 0 */
     float skip, scale;          /* finite; skip must be 1 without f */
@@ -434,7 +446,7 @@ typedef struct {
     int gate_rows;                       /* >= 1 with a gate */
     const void *post_gain, *post_bias;   /* cols elements of w_dtype, or NULL; need f */
     const void *pre_gain, *pre_bias;     /* likewise; need a pre-norm */
-    void* out; long long ldout;          /* x'; NULL if and only if f is NULL; may be x or f */
+    void* out; long long ldout;          /* x'; NULL if and only if f is NULL; may be x or f, with its ld */
     void* y;   long long ldy;            /* NULL if and only if pre is NONE; may not overlap the others */
     muon_act8 post_c;           /* receives n_f (rows x cols); q NULL: not kept.  Needs f */
     muon_act8 pre_c;            /* receives n; q NULL: not kept.  Needs a pre-norm */
@@ -474,8 +486,8 @@ typedef struct {
     const float *post_rstd, *pre_rstd;   /* needed for that norm */
     const void* dy;   long long lddy;    /* x_dtype, as all that follow; NULL if and only if pre is NONE */
     const void* dout; long long lddout;  /* gradient that reaches x' on the residual path; NULL: none */
-    void* dx; long long lddx;            /* required; may be dout or dy */
-    void* df; long long lddf;            /* NULL: the seam had no f; may be dy or dout when dx is not */
+    void* dx; long long lddx;            /* required; may be dout or dy, with its ld */
+    void* df; long long lddf;            /* NULL: the seam had no f; may be dy or dout, with its ld, when dx is not */
     void* dgate; long long lddgate;      /* as gate; NULL to skip */
     void *d_post_gain, *d_post_bias, *d_pre_gain, *d_pre_bias;   /* cols elements of w_dtype; NULL to skip */
     float beta;                 /* finite */
@@ -488,7 +500,9 @@ MUON_API muon_status seam_backward_workspace_size(const muon_seam_grad* seam, si
  * Asynchronous on `stream`: one launch, and a second one that joins the sums over
  * tokens where vector or shared gate gradients are asked for.  workspace: device,
  * 256-byte aligned, at least seam_backward_workspace_size bytes (NULL when that
- * is 0); no state is kept in it between calls.  Errors as seam_forward.
+ * is 0); no state is kept in it between calls, and calls that overlap on the GPU
+ * each need their own.  Errors as seam_forward; d_status is not written (a
+ * checkpoint's NaN blocks make NaN gradients, which the step flags).
  */
 MUON_API muon_status seam_backward(const muon_seam_grad* seam, muon_dtype x_dtype, muon_dtype w_dtype,
                                    void* workspace, size_t ws_bytes, int* d_status, muon_stream_t stream);

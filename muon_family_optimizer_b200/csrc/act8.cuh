@@ -17,6 +17,7 @@ namespace muon {
 
 constexpr int kActBlock = 32;
 constexpr int kActExpMin = -120, kActExpMax = 119;
+constexpr int kActMaxDim = 1 << 30; // rows, columns, outputs: sums of a few of them with tile sizes stay ints
 constexpr int kActBad = 255;        // exponent byte of a block that stands for NaNs
 
 __host__ __device__ inline int act8_blocks(int cols) { return (cols + kActBlock - 1) / kActBlock; }
@@ -160,22 +161,9 @@ __device__ __forceinline__ void act8_decode8(uint2 w, int byte, float (&v)[8]) {
     for (int i = 0; i < 8; ++i) v[i] *= s;
 }
 
-// Codes col..col+7 of a row; those past the row read as 0.
-__device__ __forceinline__ uint2 act8_load8(const signed char* qrow, int col, int nvalid) {
-    if (nvalid >= 8) return *reinterpret_cast<const uint2*>(qrow + col);
-    uint2 w = make_uint2(0u, 0u);
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-        if (i < nvalid) {
-            const uint32_t b = (uint32_t)(unsigned char)qrow[col + i] << (8 * (i & 3));
-            if (i < 4) w.x |= b; else w.y |= b;
-        }
-    return w;
-}
-
 // Host: whether a checkpoint's fields can be used (an empty one needs no pointers).
 inline bool act8_valid(const muon_act8& c) {
-    if (c.rows < 0 || c.cols < 1 || c.ldq < c.cols || c.ldq % 16 != 0 || c.lde < act8_blocks(c.cols)) return false;
+    if (c.rows < 0 || c.rows > kActMaxDim || c.cols < 1 || c.cols > kActMaxDim || c.ldq < c.cols || c.ldq % 16 != 0 || c.lde < act8_blocks(c.cols)) return false;
     if (c.rows == 0) return true;
     return c.q && c.e && (reinterpret_cast<uintptr_t>(c.q) & 15) == 0;
 }

@@ -7,30 +7,41 @@
 // (kind::f16, fp32 accumulation), and the kernel turns codes into that operand on
 // the way into shared memory: the codes are what crosses HBM and L2.
 //
-// One persistent CTA pair per two SMs (cta_group::2, 256 x 256 tiles of G), a
-// work list of (tile, range of tokens) over all layers of the call:
-//   warp 0      TMA producer: this CTA's 128 columns of dY, 128-byte-swizzled
-//               boxes of 64 x 64 tokens (no multicast);
-//   warp 1      allocates tensor memory; one thread of the leader CTA issues the MMAs;
-//   warps 2-9   epilogue: tcgen05.ld, gain, shift, beta, store (or the fp32 part of a
-//               range of tokens), overlapped with the next tile through two
-//               accumulator buffers;
-//   warps 10-21 converters: 16 codes and their exponent byte from a ring of raw
-//               stages to two 16-byte pieces of the swizzled operand;
-//   warps 22-23 fill the raw ring: codes by TMA (128 columns x 64 tokens), exponent
-//               bytes (any alignment) as the aligned words that hold them by cp.async.
-// A stage is full when both CTAs' boxes have landed and the converters of
-// both have arrived on the leader's barrier.  The converters touch no global memory: the
-// fence that shows their stores to the tensor cores waits for every access of
-// the thread, and with the codes loaded by the converters themselves it waited
-// for the loads of later k-blocks too (2.44 ms for 14336 x 4096 over 8192 tokens).
+// One persistent CTA pair per two SMs (cta_group::2), a work list of (tile of G, range
+// of tokens) over all layers of the call.  Tiles are 512 x 256 where they fill the
+// device, else 256 x 256 (plan_batch): in the larger, two MMAs of 256 rows share a
+// converted operand, which halves the conversions and their shared-memory traffic per
+// flop, but their accumulators fill tensor memory, so an epilogue is not overlapped with
+// the next tile's sum.
+//   warp 0       TMA producer: this CTA's 128 columns of dY of each MMA, 128-byte-swizzled
+//                boxes of 64 x 64 tokens (no multicast);
+//   warp 1       allocates tensor memory; one lane of the leader CTA issues the MMAs;
+//   warps 2-9    epilogue: tcgen05.ld, gain, shift, beta, store (or the fp32 part of a
+//                range of tokens);
+//   warps 10-17  converters: two groups that take k-blocks of 64 tokens in turn, codes and
+//                exponent bytes from the ring of raw stages to the swizzled operand;
+//   warps 18-19  fill the raw ring: codes by TMA (128 columns x 64 tokens), exponent
+//                bytes (any alignment) as the aligned words that hold them by cp.async.
+// An operand is full when the converters of both CTAs have arrived on the leader's
+// barrier, and one commit per k-block, to both CTAs, frees dY's stage and the operand's.
+// The converters touch no global memory: the fence that shows their stores to the tensor
+// cores waits for every access of the thread, and with the codes loaded by the converters
+// themselves it waited for the loads of later k-blocks too (2.44 ms for 14336 x 4096 over
+// 8192 tokens).
+//
+// Bound by the tensor cores where there are thousands of tokens: 14336 x 4096 over 8192
+// 615 us (1560 TFLOP/s; a k-block 0.73 us, of which its MMAs are 0.55), 4096 x 4096
+// over 8192 184 us, over 2048 73 us.  fp32 dY has three bfloat16 parts to multiply: 575 us
+// for 4096 x 4096 over 8192.
 //
 // Layers with few tiles split the tokens (plan_batch): the ranges write fp32
-// parts to the workspace and a second kernel adds them in order.
+// parts to the workspace and a second kernel adds them in order.  768 x 768 over 16,384
+// tokens: 35 us, of which the join 7; 16 layers of 2048 x 768 over 333 tokens in fp16 33 us.
 #include <algorithm>
 #include <cmath>
 #include <cstring>
 #include <mutex>
+#include <new>
 
 #include "act8.cuh"
 #include "gemm.h"
@@ -46,6 +57,7 @@ constexpr int kEpiWarps = 8, kConvWarps = 8, kRawWarps = 2;
 constexpr int kGroupWarps = 4, kConvGroups = kConvWarps / kGroupWarps;     // converters of one k-block; k-blocks at once
 constexpr int kTokens = 8 / kGroupWarps;                                   // 32-code blocks of a thread
 constexpr int kThreads = 32 * (2 + kEpiWarps + kConvWarps + kRawWarps);
+constexpr int kEditBytes = 2 * 4 * kBN / 2;     // fp32 gain and shift of the half of a tile's columns an epilogue warp has
 constexpr int kGroup = 8;               // tile rows walked together
 
 // MH MMAs of 256 rows share a converted operand: tiles of 256 MH x 256.
@@ -58,8 +70,9 @@ struct Cfg {
     static constexpr int kBufs = 2 / MH;                    // accumulators in the 512 columns
     static constexpr int kBOffset = kAStages * kABytes, kRawOffset = kBOffset + kBStages * kBBytes;
     static constexpr int kExpOffset = kRawOffset + kRaw * kRawBytes;
-    static constexpr int kSmem = 1024 + kExpOffset + kRaw * kExpBytes + 512;
-    static_assert(kConvGroups == kBStages && kBStages <= kAStages && kConvGroups < kRaw, "see the converters");
+    static constexpr int kEditOffset = kExpOffset + kRaw * kExpBytes + 512;     // behind the barriers
+    static constexpr int kSmem = 1024 + kEditOffset + kEpiWarps * kEditBytes;
+    static_assert(kEpiWarps == 8 && kSmem <= 227 * 1024 && kConvGroups == kBStages && kBStages <= kAStages && kConvGroups < kRaw, "see the converters");
 };
 // The tensor cores' accumulation truncates: every 16 tokens cost up to a unit in the last place of the running sum,
 // towards zero (measured 1.7e-8 relative per step, 4e-5 over 40,000 terms).  An fp32 G is therefore summed in segments of
@@ -190,23 +203,25 @@ __device__ __forceinline__ void convert32(const uint4& a, const uint4& b, int by
 }
 
 // gain, shift and beta (first segment; later ones add to G) on a thread's four rows (row + 8 u) of eight columns, in the
-// accumulator's register order (tmem_ld_16x256b_x4_twice, convert32).
+// accumulator's register order (tmem_ld_16x256b_x4_twice, convert32).  edit: the eight columns' gain and, kBN / 2 values
+// on, shift in shared memory.
 template <int WDT>
 __device__ __forceinline__ void edit_rows(const GradItem& I, int row, int col, bool vec, int nv, bool first,
-                                          float (&v)[32]) {
+                                          const float* edit, float (&v)[32]) {
     constexpr int at[8] = {0, 4, 1, 5, 8, 12, 9, 13};
     const int out = I.out;
     if (I.gain) {
-        float g[8];
-        load8_dt(I.gain, col, WDT, vec, nv, g);
+        const float4 a = *reinterpret_cast<const float4*>(edit), b = *reinterpret_cast<const float4*>(edit + 4);
+        const float g[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
 #pragma unroll
         for (int u = 0; u < 4; ++u)
 #pragma unroll
             for (int i = 0; i < 8; ++i) v[16 * (u >> 1) + 2 * (u & 1) + at[i]] *= g[i];
     }
     if (I.shift && first) {
-        float s[8];
-        load8_dt(I.shift, col, WDT, false, nv, s);
+        const float4 a = *reinterpret_cast<const float4*>(edit + kBN / 2);
+        const float4 b = *reinterpret_cast<const float4*>(edit + kBN / 2 + 4);
+        const float s[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
             const float d = row + 8 * u < out ? I.dy_sum[row + 8 * u] : 0.f;
@@ -382,11 +397,24 @@ __global__ void __launch_bounds__(kThreads, 1) act8_grad_kernel(const __grid_con
     } else if (warp < 2 + kEpiWarps) {
         // ---------------------------------------------------- epilogue
         const int quad = warp & 3, part = (warp - 2) >> 2;
+        float* const mine = reinterpret_cast<float*>(smem + C::kEditOffset + (warp - 2) * kEditBytes);
         int it = 0;
         bool ok = true;
         for (long long w = unit; ok && w < p.works; w += nunits) {
           const Work k = decode_work(p, w);
           const GradItem& I = p.it[k.item];
+          // The warp's columns of gain and shift, read while the tile is summed (4096 x 4096 over 2048 tokens, bf16,
+          // with both: 94 us when every 32 columns of the epilogue read theirs, 85 us so, 73 us without them).
+          if (k.slot < 0 && (I.gain || I.shift)) {
+              __syncwarp();
+#pragma unroll
+              for (int i = 0; i < kBN / 64; ++i) {
+                  const int col = k.tj * kBN + (2 * i + part) * 32 + lane;
+                  if (I.gain) mine[i * 32 + lane] = col < I.cols ? ld_elem(I.gain, col, WDT) : 0.f;
+                  if (I.shift) mine[kBN / 2 + i * 32 + lane] = col < I.cols ? ld_elem(I.shift, col, WDT) : 0.f;
+              }
+              __syncwarp();
+          }
           for (int s0 = k.kb0; s0 < k.kb1; s0 += p.seg, ++it) {
             const int buf = it % kBufs;
             if (!mbar_wait(&tfull_bar[buf], (it / kBufs) & 1, abort_flag, d_status)) { ok = false; break; }
@@ -414,7 +442,9 @@ __global__ void __launch_bounds__(kThreads, 1) act8_grad_kernel(const __grid_con
                 char* dst = base + ((long long)(row_at + lr + (lane >> 2)) * width + col_at + lc + (lane & 3) * 8) * esz;
                 float v[32];
                 tmem_ld_16x256b_x4_twice(tmem_base + ((uint32_t)(quad * 32) << 16) + (uint32_t)((buf + h) * kBN + lc), v);
-                if (edit) edit_rows<WDT>(I, row0 + (lane >> 2), c0 + (lane & 3) * 8, vec, nv, first, v);
+                if (edit)
+                    edit_rows<WDT>(I, row0 + (lane >> 2), c0 + (lane & 3) * 8, vec, nv, first,
+                                   mine + (lc >> 6) * 32 + (lane & 3) * 8, v);
 #pragma unroll
                 for (int u = 0; u < 4; ++u, dst += step) {
                     const int z = 16 * (u >> 1) + 2 * (u & 1);
@@ -690,11 +720,29 @@ muon_status check_items(const muon_act8_grad_item* items, int n) {
     if (!items || n < 1) return MUON_ERR_INVALID_ARG;
     for (int i = 0; i < n; ++i) {
         const muon_act8_grad_item& q = items[i];
-        if (!act8_valid(q.c) || q.out < 1 || q.lddy < q.out || !q.G || (q.c.rows > 0 && !q.dY) ||
+        if (!act8_valid(q.c) || q.out < 1 || q.out > kActMaxDim || q.lddy < q.out || !q.G || (q.c.rows > 0 && !q.dY) ||
             !q.shift != !q.dy_sum || !std::isfinite(q.beta))
             return MUON_ERR_INVALID_ARG;
     }
     return MUON_OK;
+}
+
+// Two G's of a call that share memory would be written, and with beta read, in no order.
+muon_status check_disjoint(const muon_act8_grad_item* items, int n, int w_dt) {
+    struct Range { uintptr_t begin, end; };
+    constexpr int kFew = 64;
+    Range few[kFew];
+    Range* r = n <= kFew ? few : new (std::nothrow) Range[n];
+    if (!r) return MUON_ERR_UNSUPPORTED;
+    for (int i = 0; i < n; ++i) {
+        r[i].begin = reinterpret_cast<uintptr_t>(items[i].G);
+        r[i].end = r[i].begin + (uintptr_t)items[i].out * items[i].c.cols * dt_size(w_dt);
+    }
+    std::sort(r, r + n, [](const Range& a, const Range& b) { return a.begin < b.begin; });
+    bool ok = true;
+    for (int i = 1; i < n; ++i) ok &= r[i].begin >= r[i - 1].end;
+    if (r != few) delete[] r;
+    return ok ? MUON_OK : MUON_ERR_INVALID_ARG;
 }
 
 long long align256(long long x) { return (x + 255) / 256 * 256; }
@@ -936,6 +984,7 @@ muon_status act8_grad_batched(const muon_act8_grad_item* items, int n, muon_dtyp
                               void* workspace, size_t ws_bytes, int* d_status, muon_stream_t stream) {
     if (!valid(dy_dtype) || !valid(w_dtype)) return MUON_ERR_INVALID_ARG;
     muon_status st = check_items(items, n);
+    if (st == MUON_OK) st = check_disjoint(items, n, w_dtype);
     if (st != MUON_OK) return st;
     const size_t need = workspace_bytes(items, n, dy_dtype, w_dtype);
     if (need && (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255) || ws_bytes < need))

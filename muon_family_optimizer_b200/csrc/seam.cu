@@ -15,7 +15,7 @@
 // has exactly the warps its rows need, and each thread copies its own pieces of the next
 // rows into shared memory (cp.async, no barrier: nobody else reads them) while it
 // works on this one.  Rows of other alignments (ANY) are copied as 4-byte words by the warp that
-// works on them and written element by element.
+// works on them and written as runs of elements.
 #include <algorithm>
 #include <cmath>
 
@@ -907,7 +907,8 @@ bool kept_ok(const muon_act8& c, int rows, int cols) {
 }
 
 muon_status check_seam(const muon_seam* s) {
-    if (!s || s->rows < 0 || s->cols < 1 || !norm_ok(s->post) || !norm_ok(s->pre)) return MUON_ERR_INVALID_ARG;
+    if (!s || s->rows < 0 || s->rows > kActMaxDim || s->cols < 1 || !norm_ok(s->post) || !norm_ok(s->pre))
+        return MUON_ERR_INVALID_ARG;
     if (!(s->eps > 0.f) || !std::isfinite(s->eps) || !std::isfinite(s->skip) || !std::isfinite(s->scale))
         return MUON_ERR_INVALID_ARG;
     if (s->cols > MUON_SEAM_MAX_COLS) return MUON_ERR_UNSUPPORTED;
@@ -927,7 +928,8 @@ muon_status check_seam(const muon_seam* s) {
 }
 
 muon_status check_grad(const muon_seam_grad* s) {
-    if (!s || s->rows < 0 || s->cols < 1 || !norm_ok(s->post) || !norm_ok(s->pre)) return MUON_ERR_INVALID_ARG;
+    if (!s || s->rows < 0 || s->rows > kActMaxDim || s->cols < 1 || !norm_ok(s->post) || !norm_ok(s->pre))
+        return MUON_ERR_INVALID_ARG;
     if (!std::isfinite(s->skip) || !std::isfinite(s->scale) || !std::isfinite(s->beta)) return MUON_ERR_INVALID_ARG;
     if (s->cols > MUON_SEAM_MAX_COLS) return MUON_ERR_UNSUPPORTED;
     if (s->rows == 0) return MUON_OK;                  // only the vector gradients are written (beta times what they hold)
@@ -964,8 +966,7 @@ int sm_count() {
 }
 
 // One form of a kernel: chunks of 8 columns per thread, most threads, stages, blocks per SM that
-// its registers are bounded for.
-// (warp: a row per warp, blocks of maxt threads.)
+// its registers are bounded for; warp: a row per warp, blocks of maxt threads.
 struct Form {
     int vpt, maxt, stages, per_sm;
     bool warp;
@@ -989,7 +990,7 @@ cudaError_t seam_launch(K kern, P& p, const Form& f, bool any, long long runs, c
     const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     const long long resident = (long long)sm_count() * std::max(1, std::min(most, room / (smem + 1024)));
-    const long long most_blocks = (p.s.rows + t / f.row_threads(p.s.cols) - 1) / (t / f.row_threads(p.s.cols));
+    const long long most_blocks = ((long long)p.s.rows + t / f.row_threads(p.s.cols) - 1) / (t / f.row_threads(p.s.cols));
     kern<<<(unsigned)(runs ? runs : std::min(most_blocks, resident)), t, smem, s>>>(p);
     return cudaGetLastError();
 }

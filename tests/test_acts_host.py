@@ -110,6 +110,33 @@ def test_grad_refusals(L, bad):
     assert L.act8_grad_batched(arr, 2, mo.BF16, mo.BF16, P, 1 << 40, None, None) == mo.ERR_INVALID_ARG
 
 
+@pytest.mark.parametrize("n", [2, 64, 65, 300])
+def test_grad_refuses_gradients_that_overlap(L, n):
+    # G of 24 x 40 bfloat16: 1920 bytes
+    def call(ats):
+        arr = (mo.Act8GradItem * n)(*[_grad(G=at) for at in ats])
+        return L.act8_grad_batched(arr, n, mo.BF16, mo.BF16, None, 0, None, None)
+    apart = [P + 1920 * ((7 * i) % n if n % 7 else i) for i in range(n)]
+    assert len(set(apart)) == n and call(apart) != mo.ERR_INVALID_ARG          # no workspace, or no device
+    for at in (apart[0], apart[0] + 1904, apart[0] + 16):
+        assert call(apart[:-1] + [at]) == mo.ERR_INVALID_ARG
+
+
+@pytest.mark.parametrize("bad", [dict(rows=(1 << 30) + 1), dict(cols=(1 << 30) + 16, ldq=1 << 31, lde=1 << 26),
+                                 dict(out=(1 << 30) + 1, lddy=1 << 31)])
+def test_dimensions_beyond_the_limit_are_refused(L, bad):
+    out = ctypes.c_size_t(0)
+    arr = (mo.Act8GradItem * 1)(_grad(**bad))
+    assert L.act8_grad_workspace_size(arr, 1, mo.BF16, mo.BF16, ctypes.byref(out)) == mo.ERR_INVALID_ARG
+    if "out" not in bad:
+        item = (mo.Act8Item * 1)(mo.Act8Item(_ckpt(**bad), P, 1 << 31))
+        assert L.act8_encode_batched(item, 1, mo.BF16, None, None) == mo.ERR_INVALID_ARG
+    if "rows" in bad:
+        seam = _seam(rows=bad["rows"], post_c=mo.Act8(), pre_c=mo.Act8())
+        assert L.seam_forward(ctypes.byref(seam), mo.BF16, mo.BF16, None, None) == mo.ERR_INVALID_ARG
+        assert L.seam_backward_workspace_size(ctypes.byref(_back(rows=bad["rows"])), ctypes.byref(out)) == mo.ERR_INVALID_ARG
+
+
 def test_grad_refusals_of_the_call(L):
     arr = (mo.Act8GradItem * 1)(_grad())
     out = ctypes.c_size_t(0)
