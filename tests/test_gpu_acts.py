@@ -289,6 +289,28 @@ def test_grad_long_sums_of_many_tiles_do_not_shrink(dt):
     assert float((G.double() - ref).norm() / ref.norm()) <= 1.6e-5
 
 
+@pytest.mark.parametrize("C,base,beta", [(2304, 0, 1.0), (2304, 4, 1.0), (2300, 0, 1.0), (2304, 0, 0.5), (2304, 4, 0.0)])
+def test_grad_fp32_segments_are_added_to_G(C, base, beta):
+    # 81 whole tiles over 98 k-blocks of 64 tokens, so two segments of 49 x 4 steps at the most; the error of the product as in
+    # the test above, 196 x 2^-24 x 2/3, and three roundings.  Rows that can be written in 32-byte pieces, in 16-byte pieces,
+    # and whose last group of eight columns is half there.
+    T, O = 6272, 4608
+    g = torch.Generator(device="cuda").manual_seed(4)
+    c = _ckpt_of(torch.randn(T, C, generator=g, device="cuda"))
+    dY = torch.randn(T, O, generator=g, device="cuda").to(torch.bfloat16)
+    buf = torch.randn(base + O * C + 8, generator=g, device="cuda") * 50
+    G, before = buf[base:base + O * C].view(O, C), buf.clone()
+    G0, gain = before[base:base + O * C].view(O, C), torch.randn(C, generator=g, device="cuda")
+    items = [dict(dY=dY, G=G, gain=gain, beta=beta, **c)]
+    mo.act8_grad_batched(items, _ws(items))
+    X = torch.empty(T, C, device="cuda")
+    mo.act8_decode_batched([dict(x=X, **c)])
+    product = (dY.double().T @ X.double()) * gain.double()
+    err = G.double() - (product + beta * G0.double())
+    assert float(err.norm()) <= 196 * 2.0 ** -24 * 2 / 3 * float(product.norm()) + 3 * 2.0 ** -24 * float((product.abs() + beta * G0.abs()).norm())
+    assert torch.equal(buf[:base], before[:base]) and torch.equal(buf[base + O * C:], before[base + O * C:])
+
+
 def test_grad_extreme_exponents():
     # blocks at the ends of the exponent range times a dY that brings the sum back into range
     for s, d in ((2.0 ** 118, 2.0 ** -100), (2.0 ** -116, 2.0 ** 100)):
