@@ -43,6 +43,12 @@ __device__ __forceinline__ uint32_t act8_codes4(float a, float b, float c, float
     return __byte_perm(__byte_perm(ua, ub, 0x0040), __byte_perm(uc, ud, 0x0040), 0x5410);
 }
 
+// 32 bytes in one store: a whole sector, where two stores of 16 write it half by half.
+__device__ __forceinline__ void st_global_v8(void* p, const uint4& a, const uint4& b) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w),
+                 "r"(b.x), "r"(b.y), "r"(b.z), "r"(b.w) : "memory");
+}
+
 // Eight consecutive elements as they lie in memory (16-byte aligned): loaded without
 // a branch (zeros where not `ok`), so that loads can be in flight together, and
 // turned into floats where they are used.
@@ -88,10 +94,17 @@ template <int DT> struct Raw8 {
             w[0] = make_uint4(u[0], u[1], u[2], u[3]);
         }
     }
-    __device__ __forceinline__ void store(void* p, bool ok) const {
-        if (ok)
+    // wide: p is 32-byte aligned, and fp32 is stored in whole sectors
+    __device__ __forceinline__ void store(void* p, bool ok, bool wide = false) const {
+        if (!ok) return;
+        if constexpr (DT == DT_FP32) {
+            if (wide) {
+                st_global_v8(p, w[0], w[1]);
+                return;
+            }
+        }
 #pragma unroll
-            for (int i = 0; i < N; ++i) static_cast<uint4*>(p)[i] = w[i];
+        for (int i = 0; i < N; ++i) static_cast<uint4*>(p)[i] = w[i];
     }
 };
 

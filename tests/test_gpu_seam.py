@@ -270,6 +270,12 @@ def test_strided_and_unaligned(pad, base, dt):
         _both(_build(11, C, dt, dt, "rms", "layer", 3, seed=C, pad=pad, base=base), pad=pad, base=base)
 
 
+@pytest.mark.parametrize("pad,base", [(0, 0), (0, 4), (4, 0), (8, 8)])
+@pytest.mark.parametrize("C", [1032, 8200])
+def test_fp32_rows_on_16_and_on_32_byte_boundaries(pad, base, C):
+    _both(_build(5, C, FP, FP, "rms", "layer", 1, seed=C, pad=pad, base=base), pad=pad, base=base)
+
+
 def test_without_f():
     for pre in ("rms", "layer"):
         s = _build(13, 300, BF, BF, "none", pre, 0, f=False)
