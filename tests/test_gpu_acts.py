@@ -289,6 +289,15 @@ def test_grad_long_sums_of_many_tiles_do_not_shrink(dt):
     assert float((G.double() - ref).norm() / ref.norm()) <= 1.6e-5
 
 
+@pytest.mark.parametrize("wt", [torch.bfloat16, torch.float16, torch.float32])
+@pytest.mark.parametrize("gain,shift,beta", [(False, False, 1.0), (True, True, 0.5)])
+def test_grad_added_to_G_over_many_tiles(wt, gain, shift, beta):
+    # more tiles than pairs of SMs, the last row of tiles and the last column of tiles partly outside of G
+    it, buf = _case(130, 4648, 2296, torch.bfloat16, wt, seed=11, gain=gain, shift=shift, beta=beta)
+    _run_and_check([it])
+    assert bool((buf[4648 * 2296:] == GUARD).all())
+
+
 @pytest.mark.parametrize("C,base,beta", [(2304, 0, 1.0), (2304, 4, 1.0), (2300, 0, 1.0), (2304, 0, 0.5), (2304, 4, 0.0)])
 def test_grad_fp32_segments_are_added_to_G(C, base, beta):
     # 81 whole tiles over 98 k-blocks of 64 tokens, so two segments of 49 x 4 steps at the most; the error of the product as in
