@@ -424,7 +424,8 @@ MUON_API muon_status act8_grad_batched(const muon_act8_grad_item* items, int n, 
  * The gate of row t is row t / gate_rows of `gate` (1: a value for each token; the
  * tokens of a sequence: a row for each sequence; rows: one learned vector).
  * Without f there is no residual sum: x' = x, and only y is made.  Without a
- * pre-norm (MUON_NORM_NONE) there is no y.
+ * pre-norm (MUON_NORM_NONE) there is no y.  Inputs whose rows are not 16-byte aligned
+ * are read as the aligned 4-byte words that hold them.
  */
 typedef enum {
     MUON_NORM_NONE = 0,
