@@ -271,8 +271,8 @@ def _dtype_code(t):
 
 def _stream_ptr(stream):
     import torch
-    if stream is None:
-        stream = torch.cuda.current_stream()
+    if stream is None:          # without the stream object that torch.cuda.current_stream() makes (2 us)
+        return ctypes.c_void_p(torch._C._cuda_getCurrentRawStream(torch.cuda.current_device()))
     return ctypes.c_void_p(stream.cuda_stream)
 
 
@@ -500,6 +500,27 @@ def _device(t, where):
     return dev
 
 
+def _workspace(t):
+    """(address, bytes) of a workspace on the current CUDA device, (None, 0) for None."""
+    if t is None:
+        return None, 0
+    _device(t, "workspace")
+    if not t.is_contiguous():
+        raise ValueError("workspace: must be contiguous")
+    return ctypes.c_void_p(t.data_ptr()), t.numel() * t.element_size()
+
+
+def _status(t):
+    """Address of a status word on the current CUDA device, None for None."""
+    import torch
+    if t is None:
+        return None
+    _device(t, "d_status")
+    if t.dtype != torch.int32 or t.numel() < 1:
+        raise ValueError("d_status: must be an int32 tensor")
+    return ctypes.c_void_p(t.data_ptr())
+
+
 def _refuse(t, where, dev, expected):
     if t.get_device() != dev:
         raise ValueError(f"{_name(where)}: must be a tensor of the current CUDA device, is on {t.device}")
@@ -568,7 +589,7 @@ def act8_encode_batched(items, d_status=None, stream=None):
     """Write the 8-bit checkpoint (q, e) of every item's x (see include/muon.h).
     items: list of dicts (see make_act8_items) or the array made from it."""
     arr = items if isinstance(items, ctypes.Array) else make_act8_items(items)
-    _check(lib().act8_encode_batched(arr, len(arr), arr.x_dtype, _ptr(d_status), _stream_ptr(stream)),
+    _check(lib().act8_encode_batched(arr, len(arr), arr.x_dtype, _status(d_status), _stream_ptr(stream)),
            "act8_encode_batched")
 
 
@@ -619,8 +640,7 @@ def act8_grad_batched(items, workspace=None, d_status=None, stream=None):
     shifted by gain and shift (see include/muon.h): the G that muon_step_batched reads.
     workspace: a CUDA uint8 tensor of at least act8_grad_workspace_size(...) bytes."""
     arr = items if isinstance(items, ctypes.Array) else make_act8_grads(items)
-    _check(lib().act8_grad_batched(arr, len(arr), arr.dy_dtype, arr.w_dtype, _ptr(workspace),
-                                   workspace.numel() if workspace is not None else 0, _ptr(d_status),
+    _check(lib().act8_grad_batched(arr, len(arr), arr.dy_dtype, arr.w_dtype, *_workspace(workspace), _status(d_status),
                                    _stream_ptr(stream)), "act8_grad_batched")
 
 
@@ -683,7 +703,7 @@ def seam_forward(seam, d_status=None, stream=None):
     y = norm(out), the normalised rows kept as 8-bit checkpoints.  seam: dict (see make_seam) or the
     descriptor made from it."""
     d = seam if isinstance(seam, Seam) else make_seam(seam)
-    _check(lib().seam_forward(ctypes.byref(d), d.x_dtype, d.w_dtype, _ptr(d_status), _stream_ptr(stream)),
+    _check(lib().seam_forward(ctypes.byref(d), d.x_dtype, d.w_dtype, _status(d_status), _stream_ptr(stream)),
            "seam_forward")
 
 
@@ -718,8 +738,7 @@ def seam_backward(seam, workspace=None, d_status=None, stream=None):
     gradients that muon_model_step's AdamW reads.  seam: dict (see make_seam_grad) or the descriptor
     made from it; workspace: a CUDA uint8 tensor of at least seam_backward_workspace_size(...) bytes."""
     d = seam if isinstance(seam, SeamGrad) else make_seam_grad(seam)
-    _check(lib().seam_backward(ctypes.byref(d), d.x_dtype, d.w_dtype, _ptr(workspace),
-                               workspace.numel() if workspace is not None else 0, _ptr(d_status),
+    _check(lib().seam_backward(ctypes.byref(d), d.x_dtype, d.w_dtype, *_workspace(workspace), _status(d_status),
                                _stream_ptr(stream)), "seam_backward")
 
 

@@ -230,6 +230,22 @@ def test_act8_empty_rows_are_aligned():
     assert mo.act8_empty(0, 70, device="cpu")["q"].shape == (0, 70)
 
 
+def test_binding_refuses_host_workspaces_and_status_words(L):
+    ws, status = torch.empty(1 << 20, dtype=torch.uint8), torch.zeros(1, dtype=torch.int32)
+    grads = (mo.Act8GradItem * 1)(_grad())
+    grads.dy_dtype = grads.w_dtype = mo.BF16
+    items = (mo.Act8Item * 1)(mo.Act8Item(_ckpt(), P, 40))
+    items.x_dtype = mo.BF16
+    seam, back = _seam(), _back()
+    for d in (seam, back):
+        d.x_dtype = d.w_dtype = mo.BF16
+    for call in (lambda: mo.act8_grad_batched(grads, ws), lambda: mo.act8_grad_batched(grads, None, status),
+                 lambda: mo.act8_encode_batched(items, status), lambda: mo.seam_forward(seam, status),
+                 lambda: mo.seam_backward(back, ws), lambda: mo.seam_backward(back, None, status)):
+        with pytest.raises(ValueError, match="current CUDA device"):
+            call()
+
+
 def test_binding_refuses_other_devices_and_shapes():
     # host tensors never reach the library
     c = mo.act8_empty(4, 40, device="cpu")
