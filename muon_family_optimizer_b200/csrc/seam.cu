@@ -123,7 +123,8 @@ __device__ __forceinline__ void block_sum(float (&v)[N], float* red, int& slot, 
     }
 }
 
-// Normalise the row in v (columns beyond the row, nv columns into a chunk, hold 0 and stay 0): returns the reciprocal deviation.  The two-pass variance keeps rows whose mean is large
+// Normalise the row in v (columns beyond the row, nv columns into a chunk, hold 0 and stay 0):
+// returns the reciprocal deviation.  The two-pass variance keeps rows whose mean is large
 // against their deviation exact; a sum of squares beyond fp32's range is formed again
 // at 2^-100.
 template <int VPT>
