@@ -611,15 +611,25 @@ def make_act8_grads(items):
         dt, wt, dev = items[0]["dY"].dtype, items[0]["G"].dtype, _device(items[0]["dY"], (0, "dY"))
         arr.dy_dtype, arr.w_dtype = _code(dt), _code(wt)
     for i, p in enumerate(items):
-        dY, G, q, get = p["dY"], p["G"], p["q"], p.get
+        dY, G, q, e, get = p["dY"], p["G"], p["q"], p["e"], p.get
         rows, out = _rows_cols(dY, (i, "dY"))
         cols = _rows_cols(q, (i, "q"))[1]
-        g, ldg = _matrix(G, (i, "G"), dev, out, cols, wt)
-        if ldg != cols:
-            raise ValueError(f"item {i} G: must be contiguous")
-        dy, lddy = _matrix(dY, (i, "dY"), dev, rows, out, dt)
+        if (rows > 1 and dY.dtype is dt and G.dtype is wt and q.dtype is types[0] and e.dtype is types[1] and
+                q.shape == (rows, cols) and e.shape == (rows, (cols + 31) // 32) and G.shape == (out, cols) and
+                dY.is_contiguous() and G.is_contiguous() and q.is_contiguous() and e.is_contiguous() and
+                dev == dY.get_device() == G.get_device() == q.get_device() == e.get_device() and
+                cols % 16 == 0 and q.data_ptr() % 16 == 0):
+            # the usual case in one place: calls of many small layers or experts are bound by this loop
+            act = rows, cols, q.data_ptr(), cols, e.data_ptr(), (cols + 31) // 32
+            dy, lddy, g = dY.data_ptr(), out, G.data_ptr()
+        else:
+            g, ldg = _matrix(G, (i, "G"), dev, out, cols, wt)
+            if ldg != cols:
+                raise ValueError(f"item {i} G: must be contiguous")
+            dy, lddy = _matrix(dY, (i, "dY"), dev, rows, out, dt)
+            act = _act8(q, e, (i, "checkpoint"), dev, rows, cols, types)
         gain, shift, dy_sum = get("gain"), get("shift"), get("dy_sum")
-        _PACK_GRAD.pack_into(arr, i * size, *_act8(q, p["e"], (i, "checkpoint"), dev, rows, cols, types), dy, lddy, out,
+        _PACK_GRAD.pack_into(arr, i * size, *act, dy, lddy, out,
                              g, 0 if gain is None else _vector(gain, (i, "gain"), dev, cols, wt),
                              0 if shift is None else _vector(shift, (i, "shift"), dev, cols, wt),
                              0 if dy_sum is None else _vector(dy_sum, (i, "dy_sum"), dev, out, f32), get("beta", 0.0))
