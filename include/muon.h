@@ -355,7 +355,9 @@ MUON_API muon_status act8_encode_batched(const muon_act8_item* items, int n, muo
                                          muon_stream_t stream);
 
 /* Decode n checkpoints into x_dtype (exact in bfloat16 and float; rounded to
- * nearest even in fp16, where values beyond its range become infinite). */
+ * nearest even in fp16).  fp16 values from 65024 on are held as 65536, which fp16
+ * takes as its largest value, 65504, so that a finite fp16 tensor stays finite and
+ * within half a step; larger values, of checkpoints of other types, become infinite. */
 MUON_API muon_status act8_decode_batched(const muon_act8_item* items, int n, muon_dtype x_dtype,
                                          muon_stream_t stream);
 

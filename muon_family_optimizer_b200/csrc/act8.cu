@@ -60,9 +60,10 @@ __device__ __forceinline__ void decode_row(char* x, const signed char* q, const 
     }
 #pragma unroll
     for (int i = 0; i < 8; ++i)
-        if (col + i * 32 < cols)
-            st_elem(x, col + i * 32, DT,
-                    (float)code[i] * (byte[i] == kActBad ? __uint_as_float(0x7FC00000u) : act8_scale(byte[i])));
+        if (col + i * 32 < cols) {
+            const float v = (float)code[i] * act8_step(byte[i]);
+            st_elem(x, col + i * 32, DT, DT == DT_FP16 ? act8_fp16(v) : v);
+        }
 }
 
 template <int DT, bool ENCODE>
@@ -154,6 +155,9 @@ __global__ void __launch_bounds__(256, DT != DT_FP32 ? 4 : ENCODE ? 2 : 3) act8_
                 } else {
                     Raw8<DT> o;
                     act8_decode8(w[r], b[r][0], v);
+                    if (DT == DT_FP16 && b[r][0] >= kActFp16Top)
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) v[i] = act8_fp16(v[i]);
                     o.set(v);
                     o.store(x, in && r < rows);
                 }

@@ -174,6 +174,12 @@ __device__ __forceinline__ void act8_decode8(uint2 w, int byte, float (&v)[8]) {
     for (int i = 0; i < 8; ++i) v[i] *= s;
 }
 
+// A checkpoint's value as fp16 takes it.  fp16 values from 65024 on lie in a block of e = 10 and
+// are held as 64 2^10 = 65536, which rounds to infinity; fp16's largest value, 65504, is as close to what
+// 65536 stands for (half a step, 512, around it).  65536 is the only value of an fp16 tensor's checkpoint beyond that range.
+constexpr int kActFp16Top = 127 + 10;   // smallest exponent byte under which it occurs
+__device__ __forceinline__ float act8_fp16(float v) { return fabsf(v) == 65536.f ? copysignf(65504.f, v) : v; }
+
 // Host: whether a checkpoint's fields can be used (an empty one needs no pointers).
 inline bool act8_valid(const muon_act8& c) {
     if (c.rows < 0 || c.rows > kActMaxDim || c.cols < 1 || c.cols > kActMaxDim || c.ldq < c.cols || c.ldq % 16 != 0 || c.lde < act8_blocks(c.cols)) return false;

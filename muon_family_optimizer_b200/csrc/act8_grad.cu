@@ -174,8 +174,8 @@ __device__ __forceinline__ void convert32(const uint4& a, const uint4& b, int by
                                                          *reinterpret_cast<const __nv_bfloat162*>(&d)), s2);
                 r[g][i] = *reinterpret_cast<const uint32_t*>(&x);
             }
-    } else if (byte >= 127 - 24 && byte <= 127 + 15) {
-        // 2^e is an fp16 value; the product is rounded once
+    } else if (byte >= 127 - 24 && byte < kActFp16Top) {
+        // 2^e is an fp16 value and 127 2^e in fp16's range; the product is rounded once
         const uint32_t sc = byte >= 127 - 14 ? (uint32_t)(byte - 112) << 10 : 1u << (byte - 103);
         const uint32_t scale2 = sc * 0x00010001u, off2 = 0x64806480u;
         const __half2 s2 = *reinterpret_cast<const __half2*>(&scale2), o2 = *reinterpret_cast<const __half2*>(&off2);
@@ -189,14 +189,14 @@ __device__ __forceinline__ void convert32(const uint4& a, const uint4& b, int by
                 r[g][i] = *reinterpret_cast<const uint32_t*>(&x);
             }
     } else {
-        // below fp16's smallest step or beyond its range: through fp32, one rounding
-        const float s = byte == kActBad ? __uint_as_float(0x7FC00000u) : act8_scale(byte);
+        // below fp16's smallest step or near the end of its range: through fp32, one rounding
+        const float s = act8_step(byte);
 #pragma unroll
         for (int g = 0; g < 4; ++g)
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const uint32_t c = w[2 * i + (g >> 1)] >> (g & 1 ? 8 : 0);
-                r[g][i] = pack2<__half>((float)(signed char)c * s, (float)(signed char)(c >> 16) * s);
+                r[g][i] = pack2<__half>(act8_fp16((float)(signed char)c * s), act8_fp16((float)(signed char)(c >> 16) * s));
             }
     }
 #pragma unroll

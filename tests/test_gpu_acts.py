@@ -393,3 +393,47 @@ def test_other_stream_and_captured_graph():
         q_ref, e_ref = acts.encode(_np(x))
         assert np.array_equal(it["q"].cpu().numpy(), q_ref)
         _check_G(it["G"], it["dY"], acts.decode(q_ref, e_ref))
+
+
+@pytest.mark.parametrize("C", [40, 41, 256])
+def test_fp16_values_at_the_end_of_the_range_stay_finite(C):
+    # fp16 values from 65024 on are held as 64 2^10 = 65536 (half a step: 512), which fp16 does not have; it takes 65504 for it
+    top = torch.tensor([65504.0, -65504.0, 65056.0, 65024.0, -65024.0, 64992.0, 32768.0, 1.0], dtype=torch.float16)
+    x = torch.zeros(9, C, dtype=torch.float16)
+    x[:, :8] = top.roll(1)
+    x[1, :8] = top
+    x[4, C - 1] = 65504.0
+    x = x.cuda()
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    c = mo.act8_empty(9, C)
+    mo.act8_encode_batched([dict(x=x, **c)], d_status=status)
+    q_ref, e_ref = acts.encode(_np(x))
+    assert int(status.item()) == 0 and int(q_ref.max()) == 64
+    assert np.array_equal(c["q"].cpu().numpy(), q_ref) and np.array_equal(c["e"].cpu().numpy(), e_ref)
+    out = torch.empty_like(x)
+    mo.act8_decode_batched([dict(x=out, **c)])
+    assert float((out.double() - x.double()).abs().max()) <= 512         # also: no infinity and no NaN
+    X = acts.decode(q_ref, e_ref)
+    X = np.where(np.abs(X) == 65536, np.copysign(65504.0, X), X)
+    for wt in (torch.float32, torch.float16):
+        dY = (torch.randn(9, 72, generator=torch.Generator().manual_seed(C)) * 1e-2).half().cuda()
+        G = torch.empty(72, C, dtype=wt, device="cuda")
+        items = [dict(dY=dY, G=G, **c)]
+        mo.act8_grad_batched(items, _ws(items))
+        _check_G(G, dY, X)
+
+
+def test_fp16_takes_larger_values_as_infinite():
+    # a checkpoint of another type: 2^16 is 65504 in fp16, the next values up are beyond it
+    x = torch.tensor([[65536.0, -65536.0, 66560.0, 131072.0, -131072.0, 3e38, 1.0, 0.0] + [0.0] * 8 for _ in range(2)])
+    x[1, 5] = float("nan")                                              # a bad block
+    for C in (16, 15):                                                  # vector and single accesses
+        v = x[:, :C].contiguous().cuda()
+        c = mo.act8_empty(2, C)
+        v[0, 5] = 0.0
+        mo.act8_encode_batched([dict(x=v, **c)])
+        out = torch.empty(2, C, dtype=torch.float16, device="cuda")
+        mo.act8_decode_batched([dict(x=out, **c)])
+        inf = float("inf")
+        assert out[0, :5].tolist() == [65504.0, -65504.0, 65504.0, inf, -inf]
+        assert bool(torch.isnan(out[1]).all())
