@@ -989,7 +989,8 @@ struct Form {
 // Launches a form: its shared memory, with the vectors as fp32 wherever they fit (read from
 // global memory they cost more than the blocks per SM that their space may cost: 16384 x 4096
 // with a gate forward 150 us with three blocks and global vectors); the blocks that are resident then are
-// the grid, unless the runs of rows are given.
+// the grid, unless the runs of rows are given.  The kernel's limit on shared memory is the device's whatever this
+// call needs: another thread's call of the same kernel may set it between this one's setting and launch.
 template <typename K, typename P>
 cudaError_t seam_launch(K kern, P& p, const Form& f, bool any, long long runs, cudaStream_t s) {
     const int t = f.threads(p.s.cols), most = f.blocks(p.s.cols), room = 227 * 1024;
@@ -997,7 +998,7 @@ cudaError_t seam_launch(K kern, P& p, const Form& f, bool any, long long runs, c
     const int more = any ? t / 32 * 4 * f.stages * p.units * f.vpt : 0;     // AnyRow's words behind the pieces
     p.vecs_in_smem = ring + more + vecs + 1024 <= room;
     const int smem = ring + more + (p.vecs_in_smem ? vecs : 0);
-    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, room);
     if (e != cudaSuccess) return e;
     const long long resident = (long long)sm_count() * std::max(1, std::min(most, room / (smem + 1024)));
     const long long most_blocks = ((long long)p.s.rows + t / f.row_threads(p.s.cols) - 1) / (t / f.row_threads(p.s.cols));

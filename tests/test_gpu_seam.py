@@ -12,6 +12,8 @@ stored type, eps / 2):
   backward: with A the magnitudes that enter an element (formulas below), 2^-18 A and one rounding H;
   sums over T tokens add T roundings: (2^-18 + T u) sum A, and H.
 """
+import threading
+
 import numpy as np
 import pytest
 import torch
@@ -578,3 +580,37 @@ def test_a_block_trained_end_to_end():
     assert int(status.item()) == 0
     for p, w in zip(mats + vecs, before):
         assert bool(torch.isfinite(p["W"]).all()) and not torch.equal(p["W"], w)
+
+
+def test_calls_of_two_threads():
+    # seams of different widths that share a kernel, and their gradients, called from two threads at once
+    jobs = []
+    for C, pre in ((4096, "layer"), (1032, "rms")):
+        s = _build(3, C, BF, BF, "rms", pre, 1, seed=C)
+        mo.seam_forward(s)
+        b = _back_of(s)
+        ws = _run_back(b)
+        outs = [s["out"], s["y"], b["dx"], b["df"], b["dgate"]]
+        jobs.append((mo.make_seam(s), mo.make_seam_grad(b), ws, outs, [t.clone() for t in outs], (s, b)))   # (s, b): alive
+    torch.cuda.synchronize()
+    errors = []
+    start = threading.Barrier(2)
+
+    def run(fwd, back, ws):
+        try:
+            stream = torch.cuda.Stream()
+            start.wait()
+            for _ in range(2000):
+                mo.seam_forward(fwd, stream=stream)
+                mo.seam_backward(back, ws, stream=stream)
+        except Exception as e:          # noqa: BLE001 - reported by the test's own thread
+            errors.append(e)
+    threads = [threading.Thread(target=run, args=job[:3]) for job in jobs]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert not errors
+    for _, _, _, outs, ref, _ in jobs:
+        assert all(torch.equal(a, r) for a, r in zip(outs, ref))
