@@ -372,7 +372,7 @@ MUON_API muon_status act8_decode_batched(const muon_act8_item* items, int n, muo
  * overwrites G without reading it; rows == 0 leaves beta G (+ the shift term).
  * The product accumulates in fp32: 16-bit dY runs on tensor cores with X^ taken
  * in dY's type (exact in bfloat16; in fp16 rounded, see act8_decode_batched); fp32
- * dY is split into three bfloat16 parts that sum to it.  The tensor cores'
+ * dY is split into three bfloat16 parts that sum to it (but for bits below 2^-133).  The tensor cores'
  * running sum is truncated (up to 2^-23 of it every 16 tokens), so an fp32 G is summed
  * in segments of 6144 terms (tokens times parts) that are added rounded to nearest; a 16-bit G
  * in segments of 65,536.  The sums run in a

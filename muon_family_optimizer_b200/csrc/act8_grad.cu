@@ -662,8 +662,8 @@ __global__ void __launch_bounds__(kThreads, 1) act8_grad_kernel(const __grid_con
 // ---------------------------------------------------------------------------
 // Copies of dY the tensor maps can read: rows that are not 16-byte aligned, and
 // fp32 rows as three bfloat16 parts lo + mid + hi (8 significant bits each, so the
-// three hold all 24; a non-finite value is kept in hi), summed in that order: the small
-// parts meet a small running sum.
+// three hold all 24; bits below 2^-133, bfloat16's smallest step, are dropped; a non-finite
+// value is kept in hi), summed in that order: the small parts meet a small running sum.
 // ---------------------------------------------------------------------------
 struct CopyItem {
     const void* src;
@@ -677,6 +677,13 @@ struct CopyParams {
     int n;
     long long units;
 };
+
+// What the first part takes of a value: finite ones beyond bfloat16's largest, which may round to infinity, as
+// that largest.  The rest, below 2^120 and a multiple of 2^104, fits the other two parts.
+__device__ __forceinline__ float bf16_finite(float a) {
+    const float top = __uint_as_float(0x7F7F0000u);
+    return fabsf(a) > top && fabsf(a) <= 3.402823466e38f ? copysignf(top, a) : a;
+}
 
 template <int DT>
 __global__ void __launch_bounds__(256) act8_copy_kernel(const __grid_constant__ CopyParams p) {
@@ -699,10 +706,10 @@ __global__ void __launch_bounds__(256) act8_copy_kernel(const __grid_constant__ 
                 float a = 2 * i < nv ? src[2 * i] : 0.f, b = 2 * i + 1 < nv ? src[2 * i + 1] : 0.f;
 #pragma unroll
                 for (int k = 0; k < 3; ++k) {
-                    o[k][i] = pack2<__nv_bfloat16>(a, b);
+                    o[k][i] = pack2<__nv_bfloat16>(bf16_finite(a), bf16_finite(b));
                     const float ra = a - unpack_lo<__nv_bfloat16>(o[k][i]), rb = b - unpack_hi<__nv_bfloat16>(o[k][i]);
-                    a = fabsf(a) <= 3.0e38f ? ra : 0.f;
-                    b = fabsf(b) <= 3.0e38f ? rb : 0.f;
+                    a = fabsf(a) <= 3.402823466e38f ? ra : 0.f;
+                    b = fabsf(b) <= 3.402823466e38f ? rb : 0.f;
                 }
             }
 #pragma unroll

@@ -437,3 +437,28 @@ def test_fp16_takes_larger_values_as_infinite():
         inf = float("inf")
         assert out[0, :5].tolist() == [65504.0, -65504.0, 65504.0, inf, -inf]
         assert bool(torch.isnan(out[1]).all())
+
+
+def test_grad_fp32_dY_of_every_magnitude():
+    # the three parts of an fp32 dY sum to it up to its largest value (3.396e38 and more round to infinity in
+    # bfloat16), and down to 2^-133, bfloat16's smallest step: what lies below is lost, half a step an element
+    g = torch.Generator().manual_seed(12)
+    big = torch.tensor([3.4028234e38, -3.4028234e38, 3.4e38, 3.396e38, -3.39e38, 3.2e38, 3.0123456e38, -1.2345678e38])
+    x = _x(24, 72, torch.float32, seed=12, spread=0.0) * 2.0 ** -8
+    c = _ckpt_of(x)
+    X = acts.decode(c["q"].cpu().numpy(), c["e"].cpu().numpy())
+    dY = big[torch.randint(0, 8, (24, 40), generator=g)] * (torch.rand(24, 40, generator=g) < 0.2)
+    G = torch.empty(40, 72, device="cuda")
+    items = [dict(dY=dY.cuda(), G=G, **c)]
+    mo.act8_grad_batched(items, _ws(items))
+    _check_G(G, items[0]["dY"], X)
+
+    dY = torch.randn(24, 40, generator=g) * torch.exp2(torch.randint(-135, -90, (24, 40), generator=g).float())
+    c = _ckpt_of(x * 2.0 ** 100)
+    X = acts.decode(c["q"].cpu().numpy(), c["e"].cpu().numpy())
+    items = [dict(dY=dY.cuda(), G=G, **c)]
+    mo.act8_grad_batched(items, _ws(items))
+    d = dY.double().numpy()
+    S = np.abs(d).T @ np.abs(X)
+    lost = 2.0 ** -134 * np.abs(X).sum(axis=0)[None, :]
+    assert np.all(np.abs(_np(G) - d.T @ X) <= lost + (3 * 24 + 4) * 2.0 ** -23 * (S + lost) + 2.0 ** -149)
