@@ -658,6 +658,11 @@ def _seam_common(s, name):
     """(rows, cols, dtype codes, matrix(), vector(), rstd(), checkpoint(), norm(), gate rows) of a seam's dict."""
     import torch
     get, lead = s.get, s[name]
+    gr = get("gate_rows")
+    if gr is None or gr == 0 and get("gate") is None:       # without a gate 0 is what there is
+        gr = 1
+    if gr < 1:
+        raise ValueError("gate_rows: must be at least 1")
     rows, cols = _rows_cols(lead, name)
     dt, dev = lead.dtype, _device(lead, name)
     wt = dt
@@ -666,9 +671,6 @@ def _seam_common(s, name):
         if t is not None:
             wt = t.dtype
             break
-    gr = get("gate_rows") or 1
-    if gr < 1:
-        raise ValueError("gate_rows: must be at least 1")
 
     def matrix(k, n=rows):
         t = get(k)

@@ -260,3 +260,18 @@ def test_binding_refuses_other_devices_and_shapes():
         mo.seam_forward(dict(x=x, y=x, pre="batch"))
     with pytest.raises(ValueError):
         mo.seam_forward(dict(x=x[0], y=x, pre="rms"))
+
+
+@pytest.mark.parametrize("make,lead", [(mo.make_seam, "x"), (mo.make_seam_grad, "dx")])
+def test_binding_refuses_gate_rows_below_one(make, lead):
+    t = torch.zeros(4, 40)
+    for gr in (0, -1):
+        with pytest.raises(ValueError, match="gate_rows"):
+            make({lead: t, "gate": t, "gate_rows": gr})
+    with pytest.raises(ValueError, match="gate_rows"):
+        make({lead: t, "gate_rows": -1})
+    # without a gate 0 is what there is; the next check refuses the host tensor
+    for more in (dict(gate_rows=0), dict(gate_rows=0, gate=None), dict(gate=t), dict(gate=t, gate_rows=None),
+                 dict(gate=t, gate_rows=4)):
+        with pytest.raises(ValueError, match="current CUDA device"):
+            make({lead: t, **more})
