@@ -663,6 +663,9 @@ def _seam_common(s, name):
         gr = 1
     if gr < 1:
         raise ValueError("gate_rows: must be at least 1")
+    for k in ("post", "pre"):
+        if get(k, "none") not in NORMS:
+            raise ValueError(f"{k}: must be one of {sorted(NORMS)}")
     rows, cols = _rows_cols(lead, name)
     dt, dev = lead.dtype, _device(lead, name)
     wt = dt
@@ -687,10 +690,7 @@ def _seam_common(s, name):
         return _NO_ACT8 if c is None else _act8(c["q"], c["e"], k, dev, rows, cols, (torch.int8, torch.uint8))
 
     def norm(k):
-        kind = get(k, "none")
-        if kind not in NORMS:
-            raise ValueError(f"{k}: must be one of {sorted(NORMS)}")
-        return NORMS[kind]
+        return NORMS[get(k, "none")]
     return rows, cols, (_code(dt), _code(wt)), matrix, vector, rstd, checkpoint, norm, gr
 
 

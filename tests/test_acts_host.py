@@ -275,3 +275,18 @@ def test_binding_refuses_gate_rows_below_one(make, lead):
                  dict(gate=t, gate_rows=4)):
         with pytest.raises(ValueError, match="current CUDA device"):
             make({lead: t, **more})
+
+
+@pytest.mark.parametrize("make,lead", [(mo.make_seam, "x"), (mo.make_seam_grad, "dx")])
+def test_binding_refuses_unknown_norms_and_other_ranks(make, lead):
+    t = torch.zeros(4, 40)
+    for side in ("post", "pre"):
+        for kind in ("batch", None, 1):
+            with pytest.raises(ValueError, match=f"{side}: must be one of"):
+                make({lead: t, side: kind})
+    for bad in (t[0], t[None]):
+        with pytest.raises(ValueError, match="2-D"):
+            make({lead: bad, "pre": "rms"})
+    for kind in mo.NORMS:           # the known kinds come as far as the host tensor's own refusal
+        with pytest.raises(ValueError, match="current CUDA device"):
+            make({lead: t, "post": kind, "pre": kind})
