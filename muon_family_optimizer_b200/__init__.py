@@ -521,6 +521,18 @@ def _status(t):
     return ctypes.c_void_p(t.data_ptr())
 
 
+def _descriptor(d, kind, make):
+    """A call's descriptor: made from d, or d itself where it is one, whose tensors' device (which make
+    kept) must still be the current one, on which the call launches."""
+    import torch
+    if not isinstance(d, kind):
+        return make(d)
+    dev = getattr(d, "device", None)
+    if dev is not None and dev != torch.cuda.current_device():
+        raise ValueError(f"descriptor: made for CUDA device {dev}, the current one is {torch.cuda.current_device()}")
+    return d
+
+
 def _refuse(t, where, dev, expected):
     if t.get_device() != dev:
         raise ValueError(f"{_name(where)}: must be a tensor of the current CUDA device, is on {t.device}")
@@ -576,7 +588,7 @@ def make_act8_items(items):
     types, size = (torch.int8, torch.uint8), ctypes.sizeof(Act8Item)
     if items:
         dt, dev = items[0]["x"].dtype, _device(items[0]["x"], (0, "x"))
-        arr.x_dtype = _code(dt)
+        arr.x_dtype, arr.device = _code(dt), dev
     for i, p in enumerate(items):
         x = p["x"]
         rows, cols = _rows_cols(x, (i, "x"))
@@ -588,14 +600,14 @@ def make_act8_items(items):
 def act8_encode_batched(items, d_status=None, stream=None):
     """Write the 8-bit checkpoint (q, e) of every item's x (see include/muon.h).
     items: list of dicts (see make_act8_items) or the array made from it."""
-    arr = items if isinstance(items, ctypes.Array) else make_act8_items(items)
+    arr = _descriptor(items, ctypes.Array, make_act8_items)
     _check(lib().act8_encode_batched(arr, len(arr), arr.x_dtype, _status(d_status), _stream_ptr(stream)),
            "act8_encode_batched")
 
 
 def act8_decode_batched(items, stream=None):
     """Write into every item's x the values its checkpoint (q, e) stands for (see include/muon.h)."""
-    arr = items if isinstance(items, ctypes.Array) else make_act8_items(items)
+    arr = _descriptor(items, ctypes.Array, make_act8_items)
     _check(lib().act8_decode_batched(arr, len(arr), arr.x_dtype, _stream_ptr(stream)), "act8_decode_batched")
 
 
@@ -609,7 +621,7 @@ def make_act8_grads(items):
     types, size, f32 = (torch.int8, torch.uint8), ctypes.sizeof(Act8GradItem), torch.float32
     if items:
         dt, wt, dev = items[0]["dY"].dtype, items[0]["G"].dtype, _device(items[0]["dY"], (0, "dY"))
-        arr.dy_dtype, arr.w_dtype = _code(dt), _code(wt)
+        arr.dy_dtype, arr.w_dtype, arr.device = _code(dt), _code(wt), dev
     for i, p in enumerate(items):
         dY, G, q, e, get = p["dY"], p["G"], p["q"], p["e"], p.get
         rows, out = _rows_cols(dY, (i, "dY"))
@@ -649,13 +661,13 @@ def act8_grad_batched(items, workspace=None, d_status=None, stream=None):
     """G = beta G + (dY^T X) for every item, X the layer's input held as an 8-bit checkpoint, scaled and
     shifted by gain and shift (see include/muon.h): the G that muon_step_batched reads.
     workspace: a CUDA uint8 tensor of at least act8_grad_workspace_size(...) bytes."""
-    arr = items if isinstance(items, ctypes.Array) else make_act8_grads(items)
+    arr = _descriptor(items, ctypes.Array, make_act8_grads)
     _check(lib().act8_grad_batched(arr, len(arr), arr.dy_dtype, arr.w_dtype, *_workspace(workspace), _status(d_status),
                                    _stream_ptr(stream)), "act8_grad_batched")
 
 
 def _seam_common(s, name):
-    """(rows, cols, dtype codes, matrix(), vector(), rstd(), checkpoint(), norm(), gate rows) of a seam's dict."""
+    """(rows, cols, dtype codes and device, matrix(), vector(), rstd(), checkpoint(), norm(), gate rows) of a seam's dict."""
     import torch
     get, lead = s.get, s[name]
     gr = get("gate_rows")
@@ -691,7 +703,7 @@ def _seam_common(s, name):
 
     def norm(k):
         return NORMS[get(k, "none")]
-    return rows, cols, (_code(dt), _code(wt)), matrix, vector, rstd, checkpoint, norm, gr
+    return rows, cols, (_code(dt), _code(wt), dev), matrix, vector, rstd, checkpoint, norm, gr
 
 
 def make_seam(s):
@@ -706,7 +718,7 @@ def make_seam(s):
                          get("scale", 1.0), *m("x"), *m("f"), *m("gate", -(-rows // gr)), gr, v("post_gain"),
                          v("post_bias"), v("pre_gain"), v("pre_bias"), *m("out"), *m("y"), *ckpt("post_c"),
                          *ckpt("pre_c"), rstd("post_rstd"), rstd("pre_rstd"))
-    d.x_dtype, d.w_dtype = codes
+    d.x_dtype, d.w_dtype, d.device = codes
     return d
 
 
@@ -714,7 +726,7 @@ def seam_forward(seam, d_status=None, stream=None):
     """The seam between two blocks (see include/muon.h): out = skip x + scale gate norm(f) and
     y = norm(out), the normalised rows kept as 8-bit checkpoints.  seam: dict (see make_seam) or the
     descriptor made from it."""
-    d = seam if isinstance(seam, Seam) else make_seam(seam)
+    d = _descriptor(seam, Seam, make_seam)
     _check(lib().seam_forward(ctypes.byref(d), d.x_dtype, d.w_dtype, _status(d_status), _stream_ptr(stream)),
            "seam_forward")
 
@@ -733,7 +745,7 @@ def make_seam_grad(s):
                               *ckpt("pre_c"), rstd("post_rstd"), rstd("pre_rstd"), *m("dy"), *m("dout"), *m("dx"),
                               *m("df"), *m("dgate", n), v("d_post_gain"), v("d_post_bias"), v("d_pre_gain"),
                               v("d_pre_bias"), get("beta", 0.0))
-    d.x_dtype, d.w_dtype = codes
+    d.x_dtype, d.w_dtype, d.device = codes
     return d
 
 
@@ -749,7 +761,7 @@ def seam_backward(seam, workspace=None, d_status=None, stream=None):
     """Gradients of a seam from its checkpoints (see include/muon.h): dx, df, dgate and the vector
     gradients that muon_model_step's AdamW reads.  seam: dict (see make_seam_grad) or the descriptor
     made from it; workspace: a CUDA uint8 tensor of at least seam_backward_workspace_size(...) bytes."""
-    d = seam if isinstance(seam, SeamGrad) else make_seam_grad(seam)
+    d = _descriptor(seam, SeamGrad, make_seam_grad)
     _check(lib().seam_backward(ctypes.byref(d), d.x_dtype, d.w_dtype, *_workspace(workspace), _status(d_status),
                                _stream_ptr(stream)), "seam_backward")
 

@@ -290,3 +290,17 @@ def test_binding_refuses_unknown_norms_and_other_ranks(make, lead):
     for kind in mo.NORMS:           # the known kinds come as far as the host tensor's own refusal
         with pytest.raises(ValueError, match="current CUDA device"):
             make({lead: t, "post": kind, "pre": kind})
+
+
+def test_binding_refuses_descriptors_of_another_device(monkeypatch):
+    # the tensors' device is kept when a descriptor is made; a call launches on the current one
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    monkeypatch.setattr(mo, "lib", lambda: pytest.fail("reached the library"))
+    grads, items, seam, back = (mo.Act8GradItem * 1)(_grad()), (mo.Act8Item * 1)(mo.Act8Item(_ckpt(), P, 40)), _seam(), _back()
+    for d in (grads, items, seam, back):
+        d.x_dtype = d.dy_dtype = d.w_dtype = mo.BF16
+        d.device = 1
+    for call in (lambda: mo.act8_encode_batched(items), lambda: mo.act8_decode_batched(items),
+                 lambda: mo.act8_grad_batched(grads), lambda: mo.seam_forward(seam), lambda: mo.seam_backward(back)):
+        with pytest.raises(ValueError, match="made for CUDA device 1, the current one is 0"):
+            call()

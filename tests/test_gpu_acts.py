@@ -462,3 +462,20 @@ def test_grad_fp32_dY_of_every_magnitude():
     S = np.abs(d).T @ np.abs(X)
     lost = 2.0 ** -134 * np.abs(X).sum(axis=0)[None, :]
     assert np.all(np.abs(_np(G) - d.T @ X) <= lost + (3 * 24 + 4) * 2.0 ** -23 * (S + lost) + 2.0 ** -149)
+
+
+def test_descriptors_keep_their_tensors_device():
+    it, _ = _case(5, 24, 40, torch.bfloat16, torch.float32)
+    x = torch.zeros(5, 40, dtype=torch.bfloat16, device="cuda")
+    seam = dict(pre="rms", x=x, y=torch.empty_like(x))
+    back = dict(dx=torch.empty_like(x), dout=x)
+    made = [(mo.make_act8_grads([it]), lambda d: mo.act8_grad_batched(d, _ws(d))),
+            (mo.make_act8_items([dict(x=x, q=it["q"], e=it["e"])]), mo.act8_decode_batched),
+            (mo.make_seam(seam), mo.seam_forward), (mo.make_seam_grad(back), mo.seam_backward)]
+    for d, call in made:
+        assert d.device == torch.cuda.current_device()
+        call(d)
+        d.device += 1
+        with pytest.raises(ValueError, match="current one"):
+            call(d)
+    torch.cuda.synchronize()
