@@ -22,12 +22,20 @@
 //                exponent bytes from the ring of raw stages to the swizzled operand;
 //   warps 18-19  fill the raw ring: codes by TMA (128 columns x 64 tokens), exponent
 //                bytes (any alignment) as the aligned words that hold them by cp.async.
-// An operand is full when the converters of both CTAs have arrived on the leader's
-// barrier, and one commit per k-block, to both CTAs, frees dY's stage and the operand's.
-// The converters touch no global memory: the fence that shows their stores to the tensor
-// cores waits for every access of the thread, and with the codes loaded by the converters
-// themselves it waited for the loads of later k-blocks too (2.44 ms for 14336 x 4096 over
-// 8192 tokens).
+// Commits per k-block, to both CTAs, free dY's stage and the operand's.  The converters
+// touch no global memory: the fence that shows their stores to the tensor cores waits for
+// every access of the thread, and with the codes loaded by the converters themselves it
+// waited for the loads of later k-blocks too (2.44 ms for 14336 x 4096 over 8192 tokens).
+//
+// The MMAs read the operands and write the accumulators of both CTAs, so the leader has to
+// observe, at cluster scope, that the other CTA's converters have stored their half and that its
+// epilogue has read the accumulator.  A release at cluster scope by the converters holds each
+// up for about 1700 cycles (14336 x 4096 over 8192 tokens 828 us), by a warp that relays
+// their arrivals 670 to 790 us.  So converters and epilogue arrive on barriers of their own CTA (CTA
+// scope), and the other CTA's warp 1, which has no MMAs to issue, follows each completed phase with a copy of 16
+// bytes into the leader's shared memory.  The copy is ordered behind what the relay has acquired, and its
+// completion, counted on the leader's barrier, is a release at cluster scope, which nobody has to wait for:
+// 631 us (626 with arrivals on the leader's barrier at CTA scope, which the leader need not observe).
 //
 // Bound by the tensor cores where there are thousands of tokens: 14336 x 4096 over 8192
 // 615 us (1560 TFLOP/s; a k-block 0.73 us, of which its MMAs are 0.55), 4096 x 4096
@@ -65,15 +73,19 @@ constexpr int kGroup = 8;               // tile rows walked together
 template <int MH>
 struct Cfg {
     static constexpr int kABytes = MH * kBM * kBK * 2;
-    static constexpr int kAStages = MH == 2 ? 4 : 7;        // dY: as many as fit, its loads come from HBM and L2
-    static constexpr int kBStages = 2;                      // converted X^: its stores come from registers
-    static constexpr int kRaw = MH == 2 ? 6 : 8;            // codes
+    static constexpr int kAStages = MH == 2 ? 3 : 6;        // dY
+    static constexpr int kBStages = 4;                      // converted X^: two for the relay's way (with two 643 us)
+    static constexpr int kRaw = 6;                          // codes
     static constexpr int kBufs = 2 / MH;                    // accumulators in the 512 columns
     static constexpr int kBOffset = kAStages * kABytes, kRawOffset = kBOffset + kBStages * kBBytes;
     static constexpr int kExpOffset = kRawOffset + kRaw * kRawBytes;
     static constexpr int kEditOffset = kExpOffset + kRaw * kExpBytes + 512;     // behind the barriers
     static constexpr int kSmem = 1024 + kEditOffset + kEpiWarps * kEditBytes;
-    static_assert(kEpiWarps == 8 && kSmem <= 227 * 1024 && kConvGroups == kBStages && kBStages <= kAStages && kConvGroups < kRaw, "see the converters");
+    static_assert(kEpiWarps == 8 && kSmem <= 227 * 1024 && kConvGroups < kRaw, "see the converters");
+    // Each stage is filled, converted, and relayed by the same warps every time.  A stage that changed hands could be
+    // reached by a warp that is a phase ahead, whose wait on a parity passes at once: it would be armed twice.
+    static_assert(kRaw % kRawWarps == 0 && kRaw % kConvGroups == 0 && kBStages % kConvGroups == 0, "rings");
+    static_assert(16 * (kBStages + kBufs) <= 128, "the relay");
 };
 // The tensor cores' accumulation truncates: every 16 tokens cost up to a unit in the last place of the running sum,
 // towards zero (measured 1.7e-8 relative per step, 4e-5 over 40,000 terms).  An fp32 G is therefore summed in segments of
@@ -272,15 +284,18 @@ __global__ void __launch_bounds__(kThreads, 1) act8_grad_kernel(const __grid_con
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint8_t* raw = smem + kRawOffset;
     uint64_t* afull_bar = reinterpret_cast<uint64_t*>(smem + kExpOffset + kRaw * kExpBytes);
-    uint64_t* done_bar = afull_bar + kAStages;          // k-block j's MMAs are complete: barrier j % kAStages
-    uint64_t* bfull_bar = done_bar + kAStages;
-    uint64_t* rfull_bar = bfull_bar + kBStages;
+    uint64_t* adone_bar = afull_bar + kAStages;         // the MMAs that read this stage are complete
+    uint64_t* bfull_bar = adone_bar + kAStages;         // this CTA's half of an operand is converted
+    uint64_t* bpeer_bar = bfull_bar + kBStages;         // leader: the other CTA's half
+    uint64_t* bdone_bar = bpeer_bar + kBStages;
+    uint64_t* rfull_bar = bdone_bar + kBStages;
     uint64_t* rempty_bar = rfull_bar + kRaw;
     uint64_t* tfull_bar = rempty_bar + kRaw;
     uint64_t* tempty_bar = tfull_bar + 2;
     uint64_t* drain_bar = tempty_bar + 2;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain_bar + 1);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+    uint8_t* const relayed = smem + kExpOffset + kRaw * kExpBytes + 384;    // leader: 16 bytes per relayed barrier
     // warp and rank in forms the compiler knows to be uniform: the MMA issuer's descriptors then stay in uniform
     // registers
     const int warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
@@ -291,20 +306,28 @@ __global__ void __launch_bounds__(kThreads, 1) act8_grad_kernel(const __grid_con
     if (threadIdx.x == 0) {
         for (int s = 0; s < kAStages; ++s) {
             mbar_init(&afull_bar[s], 1);
-            mbar_init(&done_bar[s], 1);
+            mbar_init(&adone_bar[s], 1);
         }
-        for (int s = 0; s < kBStages; ++s) mbar_init(&bfull_bar[s], 2 * kGroupWarps);   // both CTAs' converter warps
+        for (int s = 0; s < kBStages; ++s) {
+            mbar_init(&bfull_bar[s], kGroupWarps);
+            mbar_init(&bpeer_bar[s], 1);                    // the armed byte count
+            mbar_init(&bdone_bar[s], 1);
+        }
         for (int s = 0; s < kRaw; ++s) {
             mbar_init(&rfull_bar[s], 33);                   // the armed byte count, each lane's exponent bytes
             mbar_init(&rempty_bar[s], kGroupWarps);
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(&tfull_bar[b], 1);
-            mbar_init(&tempty_bar[b], 2 * kEpiWarps);
+            mbar_init(&tempty_bar[b], kEpiWarps + (rank == 0 ? 1 : 0));    // leader: and the armed byte count
         }
         mbar_init(drain_bar, 1);
         *abort_flag = 0;
         fence_mbar_init();
+        if (rank == 0) {
+            for (int s = 0; s < kBStages; ++s) mbar_arrive_expect_tx(&bpeer_bar[s], 16);
+            for (int b = 0; b < kBufs; ++b) mbar_arrive_expect_tx(&tempty_bar[b], 16);
+        }
     }
     if (warp == 1) {
         tmem_alloc_pair(tmem_slot, 512);
@@ -326,7 +349,7 @@ __global__ void __launch_bounds__(kThreads, 1) act8_grad_kernel(const __grid_con
                 const GradItem& I = p.it[k.item];
                 const int col = k.ti * MH * 2 * kBM + (int)rank * kBM;
                 for (int kb = k.kb0; kb < k.kb1; ++kb) {
-                    if (!mbar_wait(&done_bar[stage], phase ^ 1, abort_flag, d_status)) break;
+                    if (!mbar_wait<true>(&adone_bar[stage], phase ^ 1, abort_flag, d_status)) break;
                     uint8_t* sa = smem + stage * kABytes;
                     if (rank == 0) mbar_arrive_expect_tx(&afull_bar[stage], 2 * kABytes);
                     const uint32_t fb = mapa_shared(smem_u32(&afull_bar[stage]), 0);
@@ -360,18 +383,22 @@ __global__ void __launch_bounds__(kThreads, 1) act8_grad_kernel(const __grid_con
               const Work k = decode_work(p, w);
               for (int s0 = k.kb0; ok && s0 < k.kb1; s0 += p.seg, ++it) {
                 const int s1 = min(k.kb1, s0 + p.seg), buf = it % kBufs;
-                ok = __all_sync(0xFFFFFFFFu, mbar_wait(&tempty_bar[buf], ((it / kBufs) & 1) ^ 1, abort_flag, d_status));
+                ok = __all_sync(0xFFFFFFFFu, mbar_wait<true>(&tempty_bar[buf], ((it / kBufs) & 1) ^ 1, abort_flag, d_status));
                 if (!ok) break;
+                if (it >= kBufs && lane == 0) mbar_arrive_expect_tx(&tempty_bar[buf], 16);     // the next reads of this accumulator
                 tc_fence_after();
                 const uint32_t d_tmem = tmem_base + (uint32_t)(buf * kBN);
                 for (int kb = s0; kb < s1; ++kb) {
-                    bool ready = mbar_try_wait(&afull_bar[as], aphase) && mbar_try_wait(&bfull_bar[bs], bphase);
+                    bool ready = mbar_try_wait<true>(&afull_bar[as], aphase) && mbar_try_wait(&bfull_bar[bs], bphase) &&
+                                 mbar_try_wait<true>(&bpeer_bar[bs], bphase);
                     if (!__all_sync(0xFFFFFFFFu, ready)) {
-                        ready = mbar_wait(&afull_bar[as], aphase, abort_flag, d_status) &&
-                                mbar_wait(&bfull_bar[bs], bphase, abort_flag, d_status);
+                        ready = mbar_wait<true>(&afull_bar[as], aphase, abort_flag, d_status) &&
+                                mbar_wait(&bfull_bar[bs], bphase, abort_flag, d_status) &&
+                                mbar_wait<true>(&bpeer_bar[bs], bphase, abort_flag, d_status);
                         if (!__all_sync(0xFFFFFFFFu, ready)) { ok = false; break; }
                     }
                     tc_fence_after();
+                    if (lane == 0) mbar_arrive_expect_tx(&bpeer_bar[bs], 16);      // the stage's next k-block
                     // 16 tokens of an MMA: 16 rows of 128 bytes in each 64-wide box
                     const uint64_t da = desc_a + (uint64_t)(as * (kABytes >> 4)), db = desc_b + (uint64_t)(bs * (kBBytes >> 4));
                     if (elect_one()) {
@@ -381,7 +408,8 @@ __global__ void __launch_bounds__(kThreads, 1) act8_grad_kernel(const __grid_con
                             for (int h = 0; h < MH; ++h)
                                 tc_mma_f16_pair(d_tmem + h * kBN, da + (h * kBM * kBK * 2 >> 4) + s * (2048 >> 4),
                                                 db + s * (2048 >> 4), idesc, kb > s0 || s > 0 ? 1u : 0u);
-                        tc_commit_pair_multicast(smem_u32(&done_bar[as]), 3);
+                        tc_commit_pair_multicast(smem_u32(&adone_bar[as]), 3);
+                        tc_commit_pair_multicast(smem_u32(&bdone_bar[bs]), 3);
                     }
                     __syncwarp();
                     if (++as == kAStages) { as = 0; aphase ^= 1; }
@@ -397,6 +425,53 @@ __global__ void __launch_bounds__(kThreads, 1) act8_grad_kernel(const __grid_con
             __syncwarp();
             const unsigned long long t0 = global_ns();
             while (!mbar_try_wait(drain_bar, 0) && global_ns() - t0 < kWaitLimitNs) {
+            }
+        } else {
+            // ------------------------------------------------ relay
+            // Lane s < kBStages: operand stage s; the next kBufs lanes: accumulators.  Each passes the phases of a barrier of this
+            // CTA on to the leader's in order, as many as there are in this CTA's work list, but for the last reads of each
+            // accumulator, which nothing waits for.
+            const bool op = lane < kBStages, mine = lane < kBStages + kBufs;
+            const int s = op ? lane : mine ? lane - kBStages : 0;
+            uint64_t* const from = op ? &bfull_bar[s] : &tempty_bar[s];
+            const uint32_t to = mapa_shared(smem_u32(op ? &bpeer_bar[s] : &tempty_bar[s]), 0);
+            const uint32_t slot = mapa_shared(smem_u32(relayed + 16 * (mine ? lane : 0)), 0);
+            const uint8_t* const src = op ? smem + kBOffset + s * kBBytes : relayed;    // the operand's own first bytes; unused ones
+            uint32_t j = s, parity = 0, blocks = 0, segs = 0, idle = 0;
+            long long w = unit;
+            unsigned long long t0 = 0;
+            for (;;) {
+                // the work list as far as the lane that is furthest along needs it
+                while (w < p.works && __any_sync(0xFFFFFFFFu, mine && (op ? j >= blocks : j + kBufs >= segs))) {
+                    const Work k = decode_work(p, w);
+                    blocks += (uint32_t)(k.kb1 - k.kb0);
+                    segs += (uint32_t)((k.kb1 - k.kb0 + p.seg - 1) / p.seg);
+                    w += nunits;
+                }
+                const bool left = mine && (op ? j < blocks : j + kBufs < segs);
+                if (!__any_sync(0xFFFFFFFFu, left)) break;
+                const bool ready = left && mbar_test_wait(from, parity);
+                if (ready) {
+                    bulk_copy16_cluster(slot, src, to);
+                    j += op ? kBStages : kBufs;
+                    parity ^= 1;
+                }
+                if (__any_sync(0xFFFFFFFFu, ready)) {
+                    idle = 0;
+                } else if ((++idle & 255u) == 0) {
+                    if (idle == 256u) t0 = global_ns();
+                    const bool late = global_ns() - t0 > kWaitLimitNs;
+                    if (late) {
+                        *abort_flag = 1;
+                        if (d_status && lane == 0) atomicOr(d_status, MUON_FLAG_TIMEOUT);
+                    }
+                    if (__any_sync(0xFFFFFFFFu, late || *abort_flag)) break;
+                }
+            }
+            if (*abort_flag && lane == 0) {     // the copies in flight
+                const unsigned long long t1 = global_ns();
+                while (global_ns() - t1 < 200000ull) {
+                }
             }
         }
     } else if (warp < 2 + kEpiWarps) {
@@ -422,7 +497,7 @@ __global__ void __launch_bounds__(kThreads, 1) act8_grad_kernel(const __grid_con
           }
           for (int s0 = k.kb0; s0 < k.kb1; s0 += p.seg, ++it) {
             const int buf = it % kBufs;
-            if (!mbar_wait(&tfull_bar[buf], (it / kBufs) & 1, abort_flag, d_status)) { ok = false; break; }
+            if (!mbar_wait<true>(&tfull_bar[buf], (it / kBufs) & 1, abort_flag, d_status)) { ok = false; break; }
             tc_fence_after();
             const bool first = s0 == k.kb0;         // later segments are added to G
             // the layer's fields in registers: the loop's fences would have them read again for every row
@@ -534,14 +609,13 @@ __global__ void __launch_bounds__(kThreads, 1) act8_grad_kernel(const __grid_con
             tc_fence_before();
             __syncwarp();
             // only this warp's accumulator reads have to be over, not its stores
-            if (lane == 0) mbar_arrive_cluster_cta(mapa_shared(smem_u32(&tempty_bar[buf]), 0));
+            if (lane == 0) mbar_arrive(&tempty_bar[buf]);
           }
         }
     } else if (warp < 2 + kEpiWarps + kConvWarps) {
         // ---------------------------------------------------- converters
-        // Groups of kGroupWarps warps take k-blocks in turn, as many groups as operand stages, so that a group always
-        // fills the same one.  A k-block is converted in registers before its stage is waited for: the stage is only
-        // held for the stores and the MMAs.
+        // Groups of kGroupWarps warps take k-blocks in turn.  A k-block is converted in registers before its stage is
+        // waited for: the stage is only held for the stores, the relay and the MMAs.
         const int cw = warp - 2 - kEpiWarps, group = cw / kGroupWarps, sub = cw % kGroupWarps;
         constexpr int kTokStep = 64 / kTokens;
         // a warp: two blocks (one 64-column box of the operand), tokens tok0 + kTokStep i
@@ -550,10 +624,10 @@ __global__ void __launch_bounds__(kThreads, 1) act8_grad_kernel(const __grid_con
         // (pieces {0, 4} ^ token) each cover the eight bank groups.
         const int box = sub & 1, blk = lane & 1, tl = (lane >> 1) & 3;
         const int tok0 = (sub >> 1) * 16 + (lane >> 4) * 8 + ((tl < 2 ? tl : tl + 4) ^ ((lane >> 2) & 2)), x = tok0 & 7;
-        const int at = kBOffset + group * kBBytes + box * (64 * kBK * 2) + tok0 * 128;
+        const int at = kBOffset + box * (64 * kBK * 2) + tok0 * 128;
         const int codes_at = tok0 * 128, codes0 = ((box * 4 + blk * 2) ^ x) << 4, codes1 = ((box * 4 + blk * 2 + 1) ^ x) << 4;
         uint32_t rs = group, rphase = 0;                    // raw stage of the group's next k-block
-        uint32_t ds = (group + kAStages - kBStages) % kAStages, dphase = 1;     // done barrier of the one kBStages before it
+        uint32_t bs = group, bphase = 1;                    // operand stage of the group's next k-block
         uint32_t n = 0, j = group;                          // k-blocks of this CTA before this work item; the group's next
         bool ok = true;
         for (long long w = unit; ok && w < p.works; w += nunits) {
@@ -577,17 +651,18 @@ __global__ void __launch_bounds__(kThreads, 1) act8_grad_kernel(const __grid_con
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&rempty_bar[rs]);
                 if ((rs += kConvGroups) >= kRaw) { rs -= kRaw; rphase ^= 1; }
-                // the MMAs that read this operand stage last (none before the group's first k-block)
-                if (j >= kBStages && !mbar_wait(&done_bar[ds], dphase, abort_flag, d_status)) { ok = false; break; }
-                if ((ds += kConvGroups) >= kAStages) { ds -= kAStages; dphase ^= 1; }
+                // the MMAs that read this operand stage last (none before its first k-block)
+                if (!mbar_wait<true>(&bdone_bar[bs], bphase, abort_flag, d_status)) { ok = false; break; }
+                uint8_t* const b = smem + at + bs * kBBytes;
 #pragma unroll
                 for (int i = 0; i < kTokens; ++i)
 #pragma unroll
                     for (int g = 0; g < 4; ++g)
-                        *reinterpret_cast<uint4*>(smem + at + i * (kTokStep * 128) + (((blk * 4 + g) ^ x) << 4)) = o[i][g];
+                        *reinterpret_cast<uint4*>(b + i * (kTokStep * 128) + (((blk * 4 + g) ^ x) << 4)) = o[i][g];
                 fence_proxy_async_smem();                   // the tensor cores read what was stored here
                 __syncwarp();
-                if (lane == 0) mbar_arrive_cluster_cta(mapa_shared(smem_u32(&bfull_bar[group]), 0));
+                if (lane == 0) mbar_arrive(&bfull_bar[bs]);
+                if ((bs += kConvGroups) >= kBStages) { bs -= kBStages; bphase ^= 1; }
             }
         }
     } else {

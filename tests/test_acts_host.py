@@ -304,3 +304,17 @@ def test_binding_refuses_descriptors_of_another_device(monkeypatch):
                  lambda: mo.act8_grad_batched(grads), lambda: mo.seam_forward(seam), lambda: mo.seam_backward(back)):
         with pytest.raises(ValueError, match="made for CUDA device 1, the current one is 0"):
             call()
+
+
+def test_arrivals_on_another_cta_release_at_cluster_scope():
+    # An arrival on an mbarrier of another CTA has to name cluster scope: without a scope it releases to its own CTA only.
+    # tcgen05 commits and the completions of copies, the other signals between CTAs, have that scope by definition.
+    src = os.path.join(ROOT, "muon_family_optimizer_b200", "csrc")
+    found = 0
+    for name in sorted(os.listdir(src)):
+        with open(os.path.join(src, name)) as fh:
+            for line in fh:
+                if "mbarrier.arrive" in line and "shared::cluster" in line and "asm" in line and "tcgen05" not in line:
+                    found += 1
+                    assert ".release.cluster." in line, (name, line)
+    assert found

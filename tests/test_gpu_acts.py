@@ -479,3 +479,31 @@ def test_descriptors_keep_their_tensors_device():
         with pytest.raises(ValueError, match="current one"):
             call(d)
     torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("T,O,C,wt", [(700, 9216, 2304, torch.bfloat16), (6300, 4608, 2304, torch.float32),
+                                      (1900, 1536, 1024, torch.float32), (130, 9000, 2296, torch.float16)])
+def test_grad_many_tiles_per_pair_of_SMs_give_equal_bits(T, O, C, wt):
+    # several tiles and segments one after another through the same stages and accumulators, tall tiles and low ones: every
+    # run gives the first one's bits, and that is the product.  The sum's error as in the tests above: up to 4 T / 64 steps of
+    # 2^-24 2/3 of the result on average (segments hold fewer), and a rounding to G's type.
+    g = torch.Generator(device="cuda").manual_seed(T)
+    dt = torch.float16 if wt == torch.float16 else torch.bfloat16
+    c = _ckpt_of(torch.randn(T, C, generator=g, device="cuda"))
+    dY = (torch.randn(T, O, generator=g, device="cuda") * 0.1).to(dt)
+    G = torch.empty(O, C, dtype=wt, device="cuda")
+    items = mo.make_act8_grads([dict(dY=dY, G=G, **c)])
+    ws = _ws(items)
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    mo.act8_grad_batched(items, ws, d_status=status)
+    first = G.clone()
+    X = torch.empty(T, C, device="cuda")
+    mo.act8_decode_batched([dict(x=X, **c)])
+    ref = dY.double().T @ X.double()
+    tol = min(4 * -(-T // 64), 384) * 2.0 ** -24 * 2 / 3 + torch.finfo(wt).eps / 2
+    assert float((first.double() - ref).norm() / ref.norm()) <= tol
+    for _ in range(20):
+        G.fill_(GUARD)
+        mo.act8_grad_batched(items, ws, d_status=status)
+        assert torch.equal(G, first)
+    assert int(status.item()) == 0
