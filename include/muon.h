@@ -425,6 +425,8 @@ MUON_API muon_status act8_grad_batched(const muon_act8_grad_item* items, int n, 
  *     y   = n pre_gain + pre_bias          n the normalised rows of the rounded x'
  * The gate of row t is row t / gate_rows of `gate` (1: a value for each token; the
  * tokens of a sequence: a row for each sequence; rows: one learned vector).
+ * Means are fp32 sums with up to 42 roundings: a mean's error, at most 42 2^-24 times
+ * the row's mean magnitude, reaches each of its normalised values times r.
  * Without f there is no residual sum: x' = x, and only y is made.  Without a
  * pre-norm (MUON_NORM_NONE) there is no y.  Inputs whose rows are not 16-byte aligned
  * are read as the aligned 4-byte words that hold them.

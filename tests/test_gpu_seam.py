@@ -614,3 +614,18 @@ def test_calls_of_two_threads():
     assert not errors
     for _, _, _, outs, ref, _ in jobs:
         assert all(torch.equal(a, r) for a, r in zip(outs, ref))
+
+
+@pytest.mark.parametrize("C", [72, 768, 1003, 4096, 16384])
+@pytest.mark.parametrize("mean", [1e4, -300.0])
+def test_layer_norm_of_rows_far_from_zero(C, mean):
+    # The bound that the header states: with b = 42 u r mean|v| (u = 2^-24), the mean's error times r, n is off by b, and r, whose
+    # mean square grows by the error's own square, by b^2 / 2; its sums' and the root's roundings 2^-19, two more of n u each.
+    v = (torch.randn(5, C, generator=torch.Generator().manual_seed(C)) + mean).cuda()
+    s = dict(post="layer", x=torch.zeros_like(v), f=v, out=torch.empty_like(v), post_rstd=torch.empty(5, device="cuda"))
+    mo.seam_forward(s)
+    n, r = acts.normalise(_np(v), "layer", float(np.float32(1e-5)))
+    b = 42 * 2.0 ** -24 * r * np.abs(_np(v)).mean(axis=1)
+    assert np.all(np.abs(_np(s["post_rstd"]) - r) <= r * (b * b / 2 + 2.0 ** -19))
+    b = b[:, None]
+    assert np.all(np.abs(_np(s["out"]) - n) <= b + (np.abs(n) + b) * (b * b / 2 + 2.0 ** -19 + 2.0 ** -23))
