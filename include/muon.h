@@ -375,7 +375,8 @@ MUON_API muon_status act8_decode_batched(const muon_act8_item* items, int n, muo
  * dY is split into three bfloat16 parts that sum to it (but for bits below 2^-133).  The tensor cores'
  * running sum is truncated (up to 2^-23 of it every 16 tokens), so an fp32 G is summed
  * in segments of 6144 terms (tokens times parts) that are added rounded to nearest; a 16-bit G
- * in segments of 65,536.  The sums run in a
+ * in segments of 65,536.  Segments, and an fp32 G with beta = 1, are added to in memory, where values
+ * below 2^-126 count as zeros.  The sums run in a
  * fixed order: equal inputs give equal bits.  A NaN block makes NaNs of its columns of
  * G (the step then flags the matrix and keeps its W).
  */

@@ -507,3 +507,20 @@ def test_grad_many_tiles_per_pair_of_SMs_give_equal_bits(T, O, C, wt):
         mo.act8_grad_batched(items, ws, d_status=status)
         assert torch.equal(G, first)
     assert int(status.item()) == 0
+
+
+def test_grad_added_to_subnormal_G():
+    # beta = 1 on an fp32 G of whole tiles: additions in memory, where what lies below 2^-126 counts as zero; each of the
+    # sum's parts (G, the product) may lose that much, the sum is rounded once.
+    T, O, C = 64, 4608, 2304
+    g = torch.Generator(device="cuda").manual_seed(6)
+    c = _ckpt_of(torch.randint(-2, 3, (T, C), generator=g, device="cuda").float() * 2.0 ** -100)
+    dY = (torch.randint(-2, 3, (T, O), generator=g, device="cuda").float() * 2.0 ** -20).to(torch.bfloat16)
+    G0 = torch.randn(O, C, generator=g, device="cuda") * torch.exp2(torch.randint(-140, -110, (O, C), generator=g, device="cuda").float())
+    G = G0.clone()
+    items = [dict(dY=dY, G=G, beta=1.0, **c)]
+    mo.act8_grad_batched(items, _ws(items))
+    X = torch.empty(T, C, device="cuda")
+    mo.act8_decode_batched([dict(x=X, **c)])
+    ref = dY.double().T @ X.double() + G0.double()
+    assert bool(((G.double() - ref).abs() <= 2 * 2.0 ** -126 + 2.0 ** -24 * ref.abs()).all())
