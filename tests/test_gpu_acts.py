@@ -524,3 +524,65 @@ def test_grad_added_to_subnormal_G():
     mo.act8_decode_batched([dict(x=X, **c)])
     ref = dY.double().T @ X.double() + G0.double()
     assert bool(((G.double() - ref).abs() <= 2 * 2.0 ** -126 + 2.0 ** -24 * ref.abs()).all())
+
+
+def _norm_error(it):
+    """|G - the product in 64 bits| / |the product|, Frobenius."""
+    X = torch.empty(it["dY"].shape[0], it["G"].shape[1], device="cuda")
+    mo.act8_decode_batched([dict(x=X, q=it["q"], e=it["e"])])
+    ref = it["dY"].double().T @ X.double()
+    return float((it["G"].double() - ref).norm() / ref.norm())
+
+
+@pytest.mark.parametrize("T", [16381, 4999, 333])
+@pytest.mark.parametrize("dt", [torch.bfloat16, torch.float32])
+def test_grad_long_sums_over_few_tiles(T, dt):
+    # Nine tiles or fewer, so their tokens are split into ranges, the last k-block partly filled.  On average a step of 16 tokens
+    # costs at most 2^-24 of the running sum, which grows like a random walk (2/3 of the result): with at most 96 x 4
+    # steps in a range 1.6e-5, and 2^-24 for each of up to 74 ranges added.
+    it, buf = _case(T, 768, 768, dt, torch.float32, seed=T)
+    mo.act8_grad_batched([it], _ws([it]))
+    assert _norm_error(it) <= 1.6e-5 + 74 * 2.0 ** -24
+    assert bool((buf[768 * 768:] == GUARD).all())
+
+
+@pytest.mark.parametrize("T", [16381, 20001, 6209])
+@pytest.mark.parametrize("dt", DTS)
+@pytest.mark.parametrize("O,C", [(96, 64), (768, 520)])
+def test_grad_sees_every_token_of_a_long_sum(T, dt, O, C):
+    # One token at a time: first, last, around the ends of k-blocks and ranges.  dY of the rest is zero, so the gradient is this
+    # token's outer product, exactly (at most 14 significant bits, added to zeros).
+    x = torch.randn(T, C, generator=torch.Generator().manual_seed(T)).cuda()
+    c = _ckpt_of(x)
+    X = torch.empty(T, C, device="cuda")
+    mo.act8_decode_batched([dict(x=X, **c)])
+    dY, G = torch.zeros(T, O, dtype=dt, device="cuda"), torch.empty(O, C, device="cuda")
+    items = [dict(dY=dY, G=G, **c)]
+    ws = _ws(items)
+    d = (1 + torch.arange(O, device="cuda") % 7).to(dt)
+    tokens = {0, 1, 63, 64, T // 2, 6143, 6144, T - 65, T - 64, T - 2, T - 1} | set(range(1023, T, 1024))
+    for t in sorted(t for t in tokens if t < T):
+        dY[t] = d
+        mo.act8_grad_batched(items, ws)
+        values = X[t].half().double() if dt == torch.float16 else X[t].double()
+        assert torch.equal(G.double(), d.double()[:, None] * values[None, :]), t
+        dY[t] = 0
+
+
+@pytest.mark.parametrize("dt,wt,T", [(torch.float32, torch.bfloat16, 22001), (torch.float32, torch.float16, 22001),
+                                     (torch.bfloat16, torch.bfloat16, 65601), (torch.float16, torch.float16, 65601)])
+def test_grad_16_bit_G_beyond_one_segment(dt, wt, T):
+    # More than 1024 k-blocks (over the parts of an fp32 dY): a 16-bit G goes through ranges of at most as many.  Truncation as
+    # above over at most 4096 steps, a third of them in an fp32 dY's hi part, and the rounding to G's type.
+    for O, C in ((72, 136), (40, 77)):
+        it, buf = _case(T, O, C, dt, wt, seed=O, gain=False)
+        mo.act8_grad_batched([it], _ws([it]))
+        assert _norm_error(it) <= 4096 * 2.0 ** -24 * 2 / 3 + torch.finfo(wt).eps / 2
+        assert bool((buf[O * C:] == GUARD).all())
+        it["dY"].zero_()
+        it["dY"][T - 1] = 1.0                      # the last token alone
+        mo.act8_grad_batched([it], _ws([it]))
+        X = torch.empty(T, C, device="cuda")
+        mo.act8_decode_batched([dict(x=X, q=it["q"], e=it["e"])])
+        last = (X[T - 1].half() if dt == torch.float16 else X[T - 1]).to(wt)
+        assert torch.equal(it["G"], last[None, :].expand(O, C))
