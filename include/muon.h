@@ -456,8 +456,8 @@ typedef struct {
     void* y;   long long ldy;            /* NULL if and only if pre is NONE; may not overlap the others */
     muon_act8 post_c;           /* receives n_f (rows x cols); q NULL: not kept.  Needs f */
     muon_act8 pre_c;            /* receives n; q NULL: not kept.  Needs a pre-norm */
-    float* post_rstd;           /* receives r_f (rows); NULL to skip */
-    float* pre_rstd;            /* receives r (rows); NULL to skip */
+    float* post_rstd;           /* receives r_f (rows); NULL to skip.  Needs a post-norm */
+    float* pre_rstd;            /* receives r (rows); NULL to skip.  Needs a pre-norm */
 } muon_seam;
 
 /*

@@ -933,6 +933,7 @@ muon_status check_seam(const muon_seam* s) {
                s->post_rstd || s->out))
         return MUON_ERR_INVALID_ARG;
     if (f && (!s->out || s->ldout < c)) return MUON_ERR_INVALID_ARG;
+    if (s->post == MUON_NORM_NONE && s->post_rstd) return MUON_ERR_INVALID_ARG;     // there is none to receive
     if (s->gate && (s->ldgate < c || s->gate_rows < 1)) return MUON_ERR_INVALID_ARG;
     if (!pre && (s->y || s->pre_gain || s->pre_bias || s->pre_c.q || s->pre_rstd)) return MUON_ERR_INVALID_ARG;
     if (pre && (!s->y || s->ldy < c)) return MUON_ERR_INVALID_ARG;

@@ -318,3 +318,13 @@ def test_arrivals_on_another_cta_release_at_cluster_scope():
                     found += 1
                     assert ".release.cluster." in line, (name, line)
     assert found
+
+
+def test_seam_refuses_a_deviation_without_its_norm(L):
+    # it would be left unwritten
+    bare = dict(post=0, post_gain=None)
+    assert L.seam_forward(ctypes.byref(_seam(**bare)), mo.BF16, mo.BF16, None, None) == mo.ERR_INVALID_ARG
+    assert L.seam_forward(ctypes.byref(_seam(**bare, rows=0)), mo.BF16, mo.BF16, None, None) != mo.ERR_INVALID_ARG
+    ok = _seam(**bare, post_rstd=None)
+    if not torch.cuda.is_available():           # the addresses are never read: there is no device
+        assert L.seam_forward(ctypes.byref(ok), mo.BF16, mo.BF16, None, None) not in (mo.OK, mo.ERR_INVALID_ARG)
