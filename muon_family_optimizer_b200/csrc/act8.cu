@@ -58,12 +58,19 @@ __device__ __forceinline__ void decode_row(char* x, const signed char* q, const 
         code[i] = c < cols ? q[c] : 0;
         byte[i] = c < cols ? e[c / kActBlock] : 0;
     }
+    float v[8];
+    bool high = false;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        v[i] = (float)code[i] * act8_step(byte[i]);
+        high |= byte[i] >= kActFp16Top;
+    }
+    if (DT == DT_FP16 && __any_sync(0xFFFFFFFFu, high))
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = act8_fp16(v[i]);
 #pragma unroll
     for (int i = 0; i < 8; ++i)
-        if (col + i * 32 < cols) {
-            const float v = (float)code[i] * act8_step(byte[i]);
-            st_elem(x, col + i * 32, DT, DT == DT_FP16 ? act8_fp16(v) : v);
-        }
+        if (col + i * 32 < cols) st_elem(x, col + i * 32, DT, v[i]);
 }
 
 template <int DT, bool ENCODE>
@@ -143,6 +150,30 @@ __global__ void __launch_bounds__(256, DT != DT_FP32 ? 4 : ENCODE ? 2 : 3) act8_
                 }
                 b[r][0] = ok ? e[e0] : 0;
             }
+            // fp16: whether one of the warp's blocks may hold 65536 (act8_fp16), asked once: 16384 x 4096 38 us as without
+            // the question, 43 us with it in every row
+            bool high = false;
+            if constexpr (DT == DT_FP16) {
+#pragma unroll
+                for (int r = 0; r < kRowsPerUnit; ++r) high |= b[r][0] >= kActFp16Top;
+                high = __any_sync(0xFFFFFFFFu, high);
+            }
+            if (DT == DT_FP16 && high) {
+#pragma unroll 1
+                for (int r = 0; r < kRowsPerUnit; ++r) {
+                    // again from memory: a loop that is not unrolled cannot index registers
+                    if (!(in0 && r < rows)) continue;
+                    float v[8];
+                    const long long back = (long long)(kRowsPerUnit - r);
+                    act8_decode8(*reinterpret_cast<const uint2*>(q - back * qstep), e[-back * estep], v);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) v[i] = act8_fp16(v[i]);
+                    Raw8<DT> o;
+                    o.set(v);
+                    o.store(x + r * xstep, true);
+                }
+                continue;
+            }
 #pragma unroll
             for (int r = 0; r < kRowsPerUnit; ++r, x += xstep) {
                 float v[8];
@@ -155,9 +186,6 @@ __global__ void __launch_bounds__(256, DT != DT_FP32 ? 4 : ENCODE ? 2 : 3) act8_
                 } else {
                     Raw8<DT> o;
                     act8_decode8(w[r], b[r][0], v);
-                    if (DT == DT_FP16 && b[r][0] >= kActFp16Top)
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) v[i] = act8_fp16(v[i]);
                     o.set(v);
                     o.store(x, in && r < rows);
                 }
