@@ -35,16 +35,17 @@
 // scope), and the other CTA's warp 1, which has no MMAs to issue, follows each completed phase with a copy of 16
 // bytes into the leader's shared memory.  The copy is ordered behind what the relay has acquired, and its
 // completion, counted on the leader's barrier, is a release at cluster scope, which nobody has to wait for:
-// 631 us (626 with arrivals on the leader's barrier at CTA scope, which the leader need not observe).
+// 629 us (626 with arrivals on the leader's barrier at CTA scope, which the leader need not observe).
 //
 // Bound by the tensor cores where there are thousands of tokens: 14336 x 4096 over 8192
-// 615 us (1560 TFLOP/s; a k-block 0.73 us, of which its MMAs are 0.55), 4096 x 4096
-// over 8192 184 us, over 2048 73 us.  fp32 dY has three bfloat16 parts to multiply: 575 us
+// 629 us in short runs at 1965 MHz (1530 TFLOP/s; a k-block 0.80 us, of which its MMAs are 0.55), 719 us in a run of
+// seconds, where the power cap holds the clock at 1395 MHz; 4096 x 4096 over 8192 190 us, over 2048 62 us (128 tiles
+// for 74 pairs: a second round of parts).  fp32 dY has three bfloat16 parts to multiply: 598 us
 // for 4096 x 4096 over 8192.
 //
 // Layers with few tiles split the tokens (plan_batch): the ranges write fp32
 // parts to the workspace and a second kernel adds them in order.  768 x 768 over 16,384
-// tokens: 35 us, of which the join 7; 16 layers of 2048 x 768 over 333 tokens in fp16 33 us.
+// tokens: 36 us, of which the join 7; 16 layers of 2048 x 768 over 333 tokens in fp16 34 us.
 #include <algorithm>
 #include <cmath>
 #include <cstring>
@@ -483,8 +484,8 @@ __global__ void __launch_bounds__(kThreads, 1) act8_grad_kernel(const __grid_con
         for (long long w = unit; ok && w < p.works; w += nunits) {
           const Work k = decode_work(p, w);
           const GradItem& I = p.it[k.item];
-          // The warp's columns of gain and shift, read while the tile is summed (4096 x 4096 over 2048 tokens, bf16,
-          // with both: 94 us when every 32 columns of the epilogue read theirs, 85 us so, 73 us without them).
+          // The warp's columns of gain and shift, read while the tile is summed (4096 x 4096 over 2048 tokens, bf16:
+          // 62 us without them, 69 us with both, 9 us more where every 32 columns of the epilogue read theirs).
           if (k.slot < 0 && (I.gain || I.shift)) {
               __syncwarp();
 #pragma unroll

@@ -11,11 +11,12 @@
 // its columns' sums in registers and writes them once; a second launch adds the runs in
 // order.
 //
-// 16384 x 4096 bfloat16, two RMS norms: forward 125 us (5.4 TB/s), with a gate per token 150 us;
-// backward 184 us (3.7 TB/s), where the registers that rows, vectors' sums and
-// checkpoints take leave 16 warps per SM, too few to hide the row's chain of sums
-// behind other rows; two layer norms 185 and 283 us.  Two checkpoint values formed again from
-// their codes where they are used, instead of kept, spilled less and issued more: slower.
+// 16384 x 4096 bfloat16, two RMS norms: forward 125 us (5.4 TB/s), with a gate per token or shared by 2048 tokens
+// 150 us; backward 184 us (3.7 TB/s), with a gate per token 212 us, where the registers that rows, vectors' sums and
+// checkpoints take leave 16 warps per SM, too few to hide the row's chain of sums behind other rows; with a shared gate
+// 240 us (the same warps, sums that spill).  Two layer norms 185 us (shared memory for four vectors leaves 16 warps
+// per SM) and 283 us (225 registers: 8 warps per SM).  Checkpoint values formed again from their codes where
+// they are used, instead of kept, spilled less and issued more: slower.
 //
 // Two forms of each pass.  Where every row can be read in 16-byte pieces, a block
 // has exactly the warps its rows need, and each thread copies its own pieces of the next
@@ -51,6 +52,8 @@ struct RunPlan {
     int parts;         // runs per gate group (0: the runs hold whole groups)
 };
 
+// The number of runs is that of the blocks that 1024 threads per SM make.  Forms with bias or gate sums hold fewer
+// (16384 x 768 with bias sums: 6 blocks of 3 warps per SM for 10 planned, so 1366 runs in 1.5 rounds).
 RunPlan plan_runs(int rows, int cols, int gate_rows, bool gate_sums) {
     const int threads = (cols + 255) / 256 * 32, per_sm = std::max(1, std::min(16, 1024 / threads));
     RunPlan P;
@@ -1038,7 +1041,8 @@ cudaError_t launch_fwd(FwdParams& p, bool any, cudaStream_t s) {
 
 // The sums over tokens take 8 to 40 registers per chunk, so short rows have one chunk per thread and a block
 // each, and the forms with bias or shared gate sums, which few seams have, are compiled apart
-// (16384 x 4096: two RMS norms 184 us, two layer norms with bias sums 283 us).
+// (16384 x 4096: two RMS norms 184 us, two layer norms with bias sums 283 us).  Rows of more than 8192 columns have
+// 64 registers per thread and spill in every form: 4096 x 16384 362 us, two layer norms 563 us.
 template <typename T, bool BIAS, bool GSUM, bool ANY>
 cudaError_t launch_bwd_form(BwdParams& p, cudaStream_t s) {
     const int c = p.s.cols, npc = sizeof(T) == 4 ? 2 : 1;
