@@ -10,6 +10,8 @@ Tolerances, from the arithmetic:
         truncates loses a whole unit in the last place per addition), of the three operations of the
         epilogue, and the rounding to G's type: half a unit, eps / 2 of the result.
 """
+import threading
+
 import numpy as np
 import pytest
 import torch
@@ -586,3 +588,37 @@ def test_grad_16_bit_G_beyond_one_segment(dt, wt, T):
         mo.act8_decode_batched([dict(x=X, q=it["q"], e=it["e"])])
         last = (X[T - 1].half() if dt == torch.float16 else X[T - 1]).to(wt)
         assert torch.equal(it["G"], last[None, :].expand(O, C))
+
+
+def test_gradients_of_two_threads_on_two_streams():
+    # calls that overlap on the GPU, each with a workspace of its own: tall tiles, low ones, ranges of tokens, an fp32 dY
+    jobs = []
+    for T, O, C, dt, wt in ((900, 4608, 2304, torch.bfloat16, torch.bfloat16), (5000, 520, 264, torch.float32, torch.float32)):
+        it, _ = _case(T, O, C, dt, wt, seed=O)
+        arr, ws = mo.make_act8_grads([it]), _ws([it])
+        mo.act8_grad_batched(arr, ws)
+        x = torch.empty(T, C, dtype=dt, device="cuda")
+        jobs.append((arr, ws, mo.make_act8_items([dict(x=x, q=it["q"], e=it["e"])]), it, it["G"].clone(), x))
+    torch.cuda.synchronize()
+    errors, start, status = [], threading.Barrier(2), torch.zeros(1, dtype=torch.int32, device="cuda")
+
+    def run(arr, ws, items):
+        try:
+            stream = torch.cuda.Stream()
+            start.wait()
+            for _ in range(200):
+                mo.act8_decode_batched(items, stream=stream)
+                mo.act8_grad_batched(arr, ws, d_status=status, stream=stream)
+        except Exception as e:          # noqa: BLE001 - reported by the test's own thread
+            errors.append(e)
+    threads = [threading.Thread(target=run, args=job[:3]) for job in jobs]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert not errors and int(status.item()) == 0
+    for _, _, _, it, first, x in jobs:
+        assert torch.equal(it["G"], first)
+        X = torch.from_numpy(acts.decode(it["q"].cpu().numpy(), it["e"].cpu().numpy()))
+        assert torch.equal(x.cpu(), X.to(x.dtype))
